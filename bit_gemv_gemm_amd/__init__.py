@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -41,6 +42,19 @@ BGG_ROW_TILE = 64
 BGG_CHUNK = 16
 BGG_MAX_GEMV_M = 16
 BGG_READ_SLACK = 8192
+BGG_TYPE_F16 = 1
+BGG_TYPE_BF16 = 2
+BGG_TYPE_E4M3 = 3
+TYPES = {"f16": BGG_TYPE_F16, "bf16": BGG_TYPE_BF16, "e4m3": BGG_TYPE_E4M3}
+BGG_ROTARY_HALF = 0
+BGG_ROTARY_INTERLEAVED = 1
+ROTARY_LAYOUTS = {"half": BGG_ROTARY_HALF, "interleaved": BGG_ROTARY_INTERLEAVED}
+BGG_ROTARY_NONE = 0
+BGG_ROTARY_LINEAR = 1
+BGG_ROTARY_BASE = 2
+BGG_ROTARY_PARTS = 3
+ROTARY_SCALINGS = {"none": BGG_ROTARY_NONE, "linear": BGG_ROTARY_LINEAR, "base": BGG_ROTARY_BASE,
+                   "parts": BGG_ROTARY_PARTS}
 STATUS = {0: "BGG_OK", 1: "BGG_ERR_NULL", 2: "BGG_ERR_FORMAT", 3: "BGG_ERR_SHAPE",
           4: "BGG_ERR_TRIT", 5: "BGG_ERR_PACKED_BYTE", 6: "BGG_ERR_BUFFER", 7: "BGG_ERR_DESC",
           8: "BGG_ERR_HIP", 9: "BGG_ERR_SCALE"}
@@ -60,6 +74,24 @@ class bgg_weights_desc(ctypes.Structure):
         return "bgg_weights_desc(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
+class bgg_cache_desc(ctypes.Structure):
+    _fields_ = [("magic", ctypes.c_uint32), ("version", ctypes.c_uint32),
+                ("type", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("page_bytes", ctypes.c_uint64), ("total_bytes", ctypes.c_uint64)]
+
+    def __repr__(self):
+        return "bgg_cache_desc(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+# the argument structs of the calls on a cache (field order of bgg.h),
+# packed in one go: a ctypes.Structure takes longer to fill than its kernel
+# takes to run
+_ROTARY_ARGS = struct.Struct("@iiqqqPPPPqqqqPPPfiPPPP")
+_ATTENTION_ARGS = struct.Struct("@ifqqqPPqqPPPPPPqqPPN")
+
+
 class BggError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -68,6 +100,8 @@ class BggError(RuntimeError):
 
 
 _P = ctypes.POINTER(bgg_weights_desc)
+_PC = ctypes.POINTER(bgg_cache_desc)
+_f64 = ctypes.c_double
 _vp, _i64, _u32, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint32, ctypes.c_int32, ctypes.c_size_t
 _SIGS = {
     "bgg_describe": ([_i32, _i64, _i64, _P], _i32),
@@ -86,6 +120,11 @@ _SIGS = {
     "bgg_gemv_kernel_name": ([_P, _i64, ctypes.c_char_p, _sz], _i32),
     "bgg_gemm_workspace_size": ([_P, _i64], _sz),
     "bgg_ternary_gemm": ([_P, _vp, _vp, _vp, _i64, _u32, _vp, _sz, _vp], _i32),
+    "bgg_cache_describe": ([_i32, _i64, _i64, _i64, _i64, _PC], _i32),
+    "bgg_rotary_frequencies": ([_i64, _f64, _i32, _f64, _f64, _f64, _f64, _vp, _vp], _i32),
+    "bgg_rotary_append": ([_PC, _vp, _vp], _i32),
+    "bgg_attention_workspace_size": ([_PC, _i64, _i64], _sz),
+    "bgg_paged_attention": ([_PC, _vp, _vp], _i32),
     "bgg_status_string": ([_i32], ctypes.c_char_p),
     "bgg_last_error": ([], ctypes.c_char_p),
     "bgg_abi_version": ([], _u32),
@@ -263,6 +302,153 @@ def bgg_ternary_gemm(desc, packed_dev, x_dev, y_dev, M: int, flags: int, workspa
     _ok(_lib.bgg_ternary_gemm(ctypes.byref(desc), _dev_ptr(packed_dev, desc.total_bytes, "packed"),
                               _dev_ptr(x_dev, M * desc.K * 2, "x"), _dev_ptr(y_dev, M * desc.N * 2, "y"),
                               M, flags, ws, wsb, _stream(stream)), "bgg_ternary_gemm")
+
+
+# ---------------------------------------------------------------------------
+# the paged cache, rotary positions and attention
+# ---------------------------------------------------------------------------
+_TORCH_TYPES = {BGG_TYPE_F16: torch.float16, BGG_TYPE_BF16: torch.bfloat16,
+                BGG_TYPE_E4M3: torch.float8_e4m3fn}
+_TYPE_OF = {v: k for k, v in _TORCH_TYPES.items()}
+
+
+def bgg_cache_describe(type, pages: int, page_size: int, kv_heads: int, head_dim: int) -> bgg_cache_desc:
+    d = bgg_cache_desc()
+    _ok(_lib.bgg_cache_describe(TYPES[type] if isinstance(type, str) else int(type), pages, page_size, kv_heads,
+                                head_dim, ctypes.byref(d)), "bgg_cache_describe")
+    return d
+
+
+def bgg_rotary_frequencies(rotary_dim: int, base: float, scaling="none", factor: float = 1.0,
+                           trained_length: float = 0.0, low: float = 1.0, high: float = 32.0):
+    """(float32 numpy [rotary_dim / 2] radians per position, magnitude)."""
+    f = np.zeros(max(int(rotary_dim), 0) // 2 + 1, dtype=np.float32)
+    m = ctypes.c_float()
+    sc = ROTARY_SCALINGS[scaling] if isinstance(scaling, str) else int(scaling)
+    _ok(_lib.bgg_rotary_frequencies(rotary_dim, base, sc, factor, trained_length, low, high, f.ctypes.data,
+                                    ctypes.addressof(m)), "bgg_rotary_frequencies")
+    return f[:rotary_dim // 2].copy(), m.value
+
+
+def bgg_attention_workspace_size(cache: bgg_cache_desc, q_heads: int, batch: int) -> int:
+    return int(_lib.bgg_attention_workspace_size(ctypes.byref(cache), q_heads, batch))
+
+
+def _rows(t, rows, head_dim, dtype, dev, what):
+    """(pointer, stride, heads) of row operand t: [rows, heads * head_dim] or
+    [rows, heads, head_dim] on device dev, the values of a row side by side."""
+    shape = t.shape
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{what} must be {dtype} on device {dev}")
+    if len(shape) == 2:
+        n = shape[1]
+        ok = t.stride(1) == 1 and n % head_dim == 0
+    else:
+        n = shape[1] * shape[2] if len(shape) == 3 else 0
+        ok = len(shape) == 3 and shape[2] == head_dim and t.stride(2) == 1 and (shape[1] == 1 or t.stride(1) == head_dim)
+    if not ok or shape[0] != rows:
+        raise ValueError(f"{what} must be [{rows}, heads * {head_dim}] with contiguous rows, got {tuple(shape)}")
+    return t.data_ptr(), t.stride(0) if rows > 1 else n, n // head_dim
+
+
+def _vector(t, n, dtype, dev, what):
+    """Pointer of the contiguous vector t of at least n values (None: 0)."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{what} must be contiguous {dtype} on device {dev} with {n} values")
+    return t.data_ptr()
+
+
+def _cache_ptrs(cache, k_cache, v_cache, dev):
+    dt = _TORCH_TYPES[cache.type]
+    n = cache.pages * cache.page_size * cache.kv_heads * cache.head_dim
+    return _vector(k_cache, n, dt, dev, "k_cache"), _vector(v_cache, n, dt, dev, "v_cache")
+
+
+def _run_on(dev, stream, call, cache, args, where):
+    """call(cache, args, stream) with device dev current."""
+    s = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+    if torch.cuda.current_device() == dev:
+        st = call(cache, args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = call(cache, args, s)
+    if st != 0:
+        raise BggError(st, where)
+
+
+def bgg_rotary_append(cache: bgg_cache_desc, k_cache, v_cache, positions, slots, freqs, q=None, q_out=None, k=None,
+                      v=None, layout="half", magnitude: float = 1.0, k_scale=None, v_scale=None, stream=None) -> None:
+    """Rotate q into q_out, and k and v into their slots of the cache.  The
+    rotated part of a head is 2 * len(freqs) values.  q, k and v: [T, heads *
+    head_dim] (or [T, heads, head_dim]), rows of any stride."""
+    dev, D, T = positions.get_device(), cache.head_dim, positions.numel()
+    if dev < 0:
+        raise ValueError("positions must be a device tensor")
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("neither q nor k")
+    if (k is None) != (v is None):
+        raise ValueError("k and v come together")
+    dt = ref.dtype
+    if dt is not torch.float16 and dt is not torch.bfloat16:
+        raise ValueError(f"q, k and v must be float16 or bfloat16, not {dt}")
+    qp = qs = op = os_ = hq = kp = ks = vp = vs = kc = vc = sl = 0
+    if q is not None:
+        qp, qs, hq = _rows(q, T, D, dt, dev, "q")
+        op, os_, ho = _rows(q_out, T, D, dt, dev, "q_out")
+        if ho != hq:
+            raise ValueError("q_out must have q's heads")
+    if k is not None:
+        kp, ks, hk = _rows(k, T, D, dt, dev, "k")
+        vp, vs, hv = _rows(v, T, D, dt, dev, "v")
+        if hk != cache.kv_heads or hv != cache.kv_heads:
+            raise ValueError(f"k and v must have {cache.kv_heads} heads")
+        kc, vc = _cache_ptrs(cache, k_cache, v_cache, dev)
+        sl = _vector(slots, T, torch.int64, dev, "slots")
+    if T == 0:  # (empty tensors have no pointers)
+        return
+    args = _ROTARY_ARGS.pack(
+        _TYPE_OF[dt], ROTARY_LAYOUTS[layout] if isinstance(layout, str) else layout, 2 * freqs.numel(), T, hq, qp, op,
+        kp, vp, qs, os_, ks, vs, _vector(positions, T, torch.int32, dev, "positions"), sl,
+        _vector(freqs, 1, torch.float32, dev, "freqs"), magnitude, 0, kc, vc,
+        _vector(k_scale, cache.kv_heads, torch.float32, dev, "k_scale"),
+        _vector(v_scale, cache.kv_heads, torch.float32, dev, "v_scale"))
+    _run_on(dev, stream, _lib.bgg_rotary_append, cache, args, "bgg_rotary_append")
+
+
+def bgg_paged_attention(cache: bgg_cache_desc, k_cache, v_cache, page_table, lengths, q, out, workspace,
+                        scale: float, window: int = 0, lse=None, k_scale=None, v_scale=None, stream=None) -> None:
+    """Attention of one new token per sequence.  q and out: [B, heads *
+    head_dim] (or [B, heads, head_dim]); page_table int32 [B, pages]; lengths
+    int32 [B]; lse None or float32 [B, heads]."""
+    dev, B = q.get_device(), q.shape[0]
+    if dev < 0:
+        raise ValueError("q must be a device tensor")
+    dt = q.dtype
+    if dt is not torch.float16 and dt is not torch.bfloat16:
+        raise ValueError(f"q must be float16 or bfloat16, not {dt}")
+    qp, qs, hq = _rows(q, B, cache.head_dim, dt, dev, "q")
+    op, os_, ho = _rows(out, B, cache.head_dim, dt, dev, "out")
+    if ho != hq:
+        raise ValueError("out must have q's heads")
+    kc, vc = _cache_ptrs(cache, k_cache, v_cache, dev)
+    if (page_table.dtype is not torch.int32 or page_table.get_device() != dev or page_table.dim() != 2
+            or page_table.shape[0] != B or page_table.stride(1) != 1 and page_table.shape[1] != 1):
+        raise ValueError(f"page_table must be int32 [{B}, pages] with contiguous rows on device {dev}")
+    width = page_table.shape[1]
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on device {dev}")
+    if B == 0:  # (empty tensors have no pointers)
+        return
+    args = _ATTENTION_ARGS.pack(
+        _TYPE_OF[dt], scale, B, hq, window, qp, op, qs, os_, _vector(lse, B * hq, torch.float32, dev, "lse"), kc, vc,
+        _vector(k_scale, cache.kv_heads, torch.float32, dev, "k_scale"),
+        _vector(v_scale, cache.kv_heads, torch.float32, dev, "v_scale"), page_table.data_ptr(), width,
+        page_table.stride(0) if B > 1 else width, _vector(lengths, B, torch.int32, dev, "lengths"),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _run_on(dev, stream, _lib.bgg_paged_attention, cache, args, "bgg_paged_attention")
 
 
 # ---------------------------------------------------------------------------

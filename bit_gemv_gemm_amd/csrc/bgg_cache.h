@@ -1,0 +1,16 @@
+// Argument checks of the calls on a paged cache (bgg_cache.cpp), shared by
+// the device sources.
+#pragma once
+#include "bgg_internal.h"
+
+namespace bgg {
+
+constexpr int64_t kMaxQHeads = 4096;
+constexpr int64_t kMaxBatch = 65535;
+
+// BGG_OK iff `c` is exactly what bgg_cache_describe makes for its fields.
+bgg_status check_cache(const bgg_cache_desc* c);
+bgg_status check_rotary(const bgg_cache_desc* c, const bgg_rotary_args* a);
+bgg_status check_attention(const bgg_cache_desc* c, const bgg_attention_args* a);
+
+}  // namespace bgg

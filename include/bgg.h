@@ -344,6 +344,196 @@ bgg_status bgg_ternary_gemm(const bgg_weights_desc* desc, const void* packed_dev
                             const void* x_dev, void* y_dev, int64_t M, uint32_t flags,
                             void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The rest of a decoder layer's attention: rotary positions with the append
+ * to a paged cache, and the attention of one new token per sequence over
+ * that cache.  They take the rows that the products above write (q, k and v
+ * side by side in the rows of one grouped product, or apart) and leave the
+ * rows that the output projection reads.  No page passage describes them;
+ * the formulas are stated at each call.
+ * ------------------------------------------------------------------------- */
+
+/* Element types of activations (F16, BF16) and of a cache (all three).
+ * E4M3: the 8-bit float with 4 exponent and 3 mantissa bits, largest finite
+ * value 448, no infinities (no page passage). */
+typedef enum { BGG_TYPE_F16 = 1, BGG_TYPE_BF16 = 2, BGG_TYPE_E4M3 = 3 } bgg_type;
+
+#define BGG_CACHE_MAGIC 0x43474742u /* "BGGC" */
+#define BGG_CACHE_VERSION 1u
+#define BGG_MAX_PAGE_SIZE 65536
+
+/*
+ * Descriptor of one layer's paged cache: two device buffers, keys and
+ * values, of total_bytes each, [pages][kv_heads][page_size][head_dim]
+ * values of `type`, row-major.  Slot s of the cache is token s % page_size
+ * of page s / page_size.  Host struct, filled by bgg_cache_describe, owned
+ * and passed back by the caller on every call.  A cache of type E4M3 comes
+ * with one float per key head for the keys and one for the values (device
+ * arrays [kv_heads], positive and finite): the stored value times its scale
+ * is the key or value.
+ */
+typedef struct bgg_cache_desc {
+  uint32_t magic;       /* BGG_CACHE_MAGIC */
+  uint32_t version;     /* BGG_CACHE_VERSION */
+  int32_t type;         /* bgg_type */
+  int32_t reserved;     /* 0 */
+  int64_t pages;        /* 1 .. 2^31 - 1 */
+  int64_t page_size;    /* tokens per page: a power of two, 16 .. BGG_MAX_PAGE_SIZE */
+  int64_t kv_heads;     /* 1 .. 1024 */
+  int64_t head_dim;     /* 64, 96, 128, 192 or 256 */
+  uint64_t page_bytes;  /* kv_heads * page_size * head_dim values */
+  uint64_t total_bytes; /* pages * page_bytes: the size of each of the two buffers */
+} bgg_cache_desc;
+
+/* Fill *out for a cache (bookkeeping, no page passage).  Host only.
+ * Errors: BGG_ERR_NULL, BGG_ERR_FORMAT (type), BGG_ERR_SHAPE. */
+bgg_status bgg_cache_describe(int32_t type, int64_t pages, int64_t page_size, int64_t kv_heads,
+                              int64_t head_dim, bgg_cache_desc* out);
+
+/* Which values of a head's rotated part turn together (no page passage):
+ * HALF the pairs (i, i + rotary_dim/2), INTERLEAVED the pairs (2i, 2i + 1). */
+typedef enum { BGG_ROTARY_HALF = 0, BGG_ROTARY_INTERLEAVED = 1 } bgg_rotary_layout;
+
+/* How bgg_rotary_frequencies stretches the positions beyond the length the
+ * model was trained on (no page passage), with f_i = base^(-2i/rotary_dim):
+ *   NONE    f_i
+ *   LINEAR  f_i / factor
+ *   BASE    f_i of the base  base * factor^(rotary_dim / (rotary_dim - 2))
+ *   PARTS   with r_i = trained_length f_i / (2 pi) turns over the trained
+ *           length and g_i = (r_i - low) / (high - low) cut to [0, 1]:
+ *           (1 - g_i) f_i / factor + g_i f_i; the magnitude is
+ *           1 + 0.1 ln(factor) (else 1) */
+typedef enum {
+  BGG_ROTARY_NONE = 0,
+  BGG_ROTARY_LINEAR = 1,
+  BGG_ROTARY_BASE = 2,
+  BGG_ROTARY_PARTS = 3
+} bgg_rotary_scaling;
+
+/* The table of radians per position that bgg_rotary_append takes, computed
+ * in 64 bits and rounded once: freqs[i], i < rotary_dim / 2 (host float),
+ * and *magnitude (host float).  factor >= 1 (ignored by NONE);
+ * trained_length > 0 and high > low only matter to PARTS.  Host only, no
+ * page passage.  Errors: BGG_ERR_NULL, BGG_ERR_FORMAT (scaling),
+ * BGG_ERR_SHAPE (rotary_dim odd or outside 2..256, below 4 for BASE; base
+ * not above 1; factor, length or bounds out of range or not finite). */
+bgg_status bgg_rotary_frequencies(int64_t rotary_dim, double base, int32_t scaling, double factor,
+                                  double trained_length, double low, double high, float* freqs,
+                                  float* magnitude);
+
+/* Arguments of bgg_rotary_append.  Rows of token t start at
+ * `pointer + t * stride` (strides in values, multiples of 8, at least the
+ * row's own length); a row holds its heads side by side, head_dim values
+ * each.  Device pointers are 16-byte aligned, positions and scales 4-byte,
+ * slots 8-byte. */
+typedef struct bgg_rotary_args {
+  int32_t type;             /* BGG_TYPE_F16 or BGG_TYPE_BF16: q, q_out, k, v */
+  int32_t layout;           /* bgg_rotary_layout */
+  int64_t rotary_dim;       /* first values of a head that turn: even, 2 .. head_dim */
+  int64_t tokens;           /* T >= 0 */
+  int64_t q_heads;          /* 1 .. 4096 with q, else 0 */
+  const void* q_dev;        /* [T][q_heads][head_dim]; NULL: keys and values only */
+  void* q_out_dev;          /* same shape; may be q_dev with the same stride */
+  const void* k_dev;        /* [T][kv_heads][head_dim]; NULL (with v): queries only */
+  const void* v_dev;        /* same shape */
+  int64_t q_stride;
+  int64_t q_out_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  const int32_t* positions_dev; /* [T], any value */
+  const int64_t* slots_dev;     /* [T]: where token t's key and value go; a slot outside
+                                   0 .. pages * page_size - 1 (say -1) stores nothing.
+                                   Slots of one call are distinct.  Ignored without k. */
+  const float* freqs_dev;       /* [rotary_dim / 2] radians per position */
+  float magnitude;              /* factor on the rotated values */
+  int32_t reserved;             /* 0 */
+  void* k_cache_dev;            /* cache->total_bytes each */
+  void* v_cache_dev;
+  const float* k_scale_dev;     /* [kv_heads], E4M3 only (else NULL) */
+  const float* v_scale_dev;
+} bgg_rotary_args;
+
+/*
+ * Rotary positions of the new tokens' queries and keys, and the append of
+ * their keys and values to the cache (no page passage).  For token t and
+ * pair i of a head's first rotary_dim values (u, w), with
+ * a = positions[t] * freqs[i]:
+ *     (u, w) -> magnitude * (u cos a - w sin a, u sin a + w cos a)
+ * and the rest of the head as it is.  Rotated queries go to q_out, rotated
+ * keys and the values to their slot of the cache; the rest of the cache is
+ * left as it was.  a is formed and brought into one turn in 64 bits, so
+ * that far positions keep their angle; the rotation is fp32, each stored
+ * value rounded once (nearest even; E4M3: the value divided by its head's
+ * scale, then cut to +-448, NaN stays NaN).  k, v and q may be parts of the
+ * same rows; q_out and the caches overlap no input (q_out may be q itself).
+ * tokens == 0 is a no-op.
+ * Errors: BGG_ERR_NULL, BGG_ERR_DESC, BGG_ERR_FORMAT (types: a 16-bit cache
+ * has the type of k and v), BGG_ERR_SHAPE, BGG_ERR_BUFFER (alignment),
+ * BGG_ERR_HIP.
+ */
+bgg_status bgg_rotary_append(const bgg_cache_desc* cache, const bgg_rotary_args* args,
+                             void* stream);
+
+/* Arguments of bgg_paged_attention; rows, strides and alignment as in
+ * bgg_rotary_args. */
+typedef struct bgg_attention_args {
+  int32_t type;            /* BGG_TYPE_F16 or BGG_TYPE_BF16: q and out */
+  float scale;             /* factor on q . k, finite */
+  int64_t batch;           /* B >= 0 sequences, one new token each */
+  int64_t q_heads;         /* a multiple of kv_heads, at most 4096 */
+  int64_t window;          /* > 0: only the last `window` tokens are visible; 0: all */
+  const void* q_dev;       /* [B][q_heads][head_dim] */
+  void* out_dev;           /* same shape */
+  int64_t q_stride;
+  int64_t out_stride;
+  float* lse_dev;          /* [B][q_heads], or NULL */
+  const void* k_cache_dev; /* cache->total_bytes each */
+  const void* v_cache_dev;
+  const float* k_scale_dev; /* [kv_heads], E4M3 only (else NULL) */
+  const float* v_scale_dev;
+  const int32_t* page_table_dev; /* [B][table_stride]: page of tokens p * page_size .. */
+  int64_t table_width;     /* pages a sequence may have, >= 1; table_width * page_size < 2^31 */
+  int64_t table_stride;    /* >= table_width */
+  const int32_t* lengths_dev; /* [B]: tokens in the cache, the new one included */
+  void* workspace;         /* device, 16-byte aligned */
+  size_t workspace_bytes;  /* at least bgg_attention_workspace_size */
+} bgg_attention_args;
+
+/* Device workspace bytes of bgg_paged_attention for a batch of at most
+ * `batch` sequences (0 on a bad descriptor, batch < 1 or q_heads not a
+ * multiple of kv_heads in 1..4096; no page passage). */
+size_t bgg_attention_workspace_size(const bgg_cache_desc* cache, int64_t q_heads, int64_t batch);
+
+/*
+ * Attention of one new token per sequence over the paged cache (no page
+ * passage).  Query head h of sequence b reads key head
+ * h / (q_heads / kv_heads); with n = lengths[b] (cut to 0 ..
+ * table_width * page_size) and the visible tokens t < n, t >= n - window
+ * (window > 0), on pages inside the cache:
+ *     s_t = scale q.k_t,   out = sum_t e^(s_t) v_t / sum_t e^(s_t),
+ *     lse = ln sum_t e^(s_t)
+ * The new token's own key and value are read from the cache like the
+ * others (bgg_rotary_append puts them there).  A sequence without visible
+ * tokens (length 0 or below, or every score -inf) gets out = 0 and
+ * lse = -inf.  A page number outside 0 .. pages - 1 (say -1 for a page that
+ * a window has left behind) hides its tokens.  What the cache holds at
+ * hidden tokens, NaN included, has no influence.
+ * Products q.k are exact in fp32 sums; softmax statistics and sums are
+ * fp32; the probabilities enter their product with the values as a sum of
+ * two 16-bit terms; out is rounded once.  The cache is read once per 16
+ * query heads of a key head.  The same inputs give the same bits.
+ * `workspace`: its first 4 * batch * kv_heads * ceil(q_heads / kv_heads /
+ * 16) bytes count the parts of a sequence and must be zero when a call
+ * starts: zero-fill a new workspace once (or call
+ * bgg_gemv_workspace_reset); every successful call leaves them zero.
+ * batch == 0 is a no-op.
+ * Errors: BGG_ERR_NULL, BGG_ERR_DESC, BGG_ERR_FORMAT (types: a 16-bit cache
+ * has the type of q), BGG_ERR_SHAPE, BGG_ERR_BUFFER (alignment, workspace
+ * size), BGG_ERR_HIP.
+ */
+bgg_status bgg_paged_attention(const bgg_cache_desc* cache, const bgg_attention_args* args,
+                               void* stream);
+
 /* Static English name of a status (bookkeeping, no page passage). */
 const char* bgg_status_string(int32_t status);
 
