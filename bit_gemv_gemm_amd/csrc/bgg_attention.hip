@@ -1,6 +1,13 @@
 // Attention of one new token per sequence over a paged cache:
 // s_t = scale q.k_t, out = sum_t e^(s_t) v_t / sum_t e^(s_t).
+//
+// Every key and value is read once per 16 query heads of its key head, and
+// each read value does 2 * 16 multiply-adds on the matrix cores, so the
+// kernel is bound by the cache's bytes.
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cfloat>
 
 #include "bgg_cache.h"
 #include "bgg_lowp.h"
@@ -9,75 +16,584 @@ using namespace bgg;
 
 namespace {
 
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kWaves = 4;
+constexpr int kTokens = 32;  // tokens of a tile: one wave's step
+constexpr int kHeads = 16;   // query heads of a workgroup (columns of the products)
+
 struct AttnParams {
   const uint16_t* q;
   uint16_t* out;
   int64_t q_stride, out_stride;
   float* lse;
-  const void *k_cache, *v_cache;
+  const uint8_t *k_cache, *v_cache;
   const float *k_scale, *v_scale;
   const int32_t* table;
   int64_t table_stride;
   const int32_t* lengths;
-  int64_t window, max_tokens;
+  int64_t window;
+  uint32_t* counters;
+  float* parts;
   float scale;
-  int pages, q_heads, kv_heads, page_shift;
+  int max_tokens, pages, batch, q_heads, kv_heads, group, head_blocks, page_shift;
+  int target_items, min_tiles;
 };
 
-// One wave per (query head, sequence): the tokens one after the other, the
-// head's values spread over the lanes, running maximum and sum.
-template <class T, class C, int D>
-__global__ void __launch_bounds__(64) k_paged_attention(AttnParams p) {
-  constexpr int N = (D + 63) / 64;
-  const int lane = threadIdx.x, h = blockIdx.x;
-  const int64_t b = blockIdx.y;
-  const int kh = h / (p.q_heads / p.kv_heads);
-  const int64_t len = p.lengths[b];
-  const int64_t n = len < 0 ? 0 : len < p.max_tokens ? len : p.max_tokens;
-  const int64_t lo = p.window > 0 && n > p.window ? n - p.window : 0;
-  const float ks = p.k_scale ? p.k_scale[kh] : 1.0f, vs = p.v_scale ? p.v_scale[kh] : 1.0f;
-  float q[N], acc[N], m = -INFINITY, l = 0.0f;
+// ---------------------------------------------------------------------------
+// lane moves
+// ---------------------------------------------------------------------------
+// Sum over the lanes up to and including this one.
+__device__ __forceinline__ int scan_add(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1, 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2, 3
+  return v;
+}
+__device__ __forceinline__ float wave_add(float v) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int d = lane + 64 * i;
-    q[i] = d < D ? T::value(p.q[b * p.q_stride + (int64_t)h * D + d]) : 0.0f;
-    acc[i] = 0.0f;
+  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
+  return v;
+}
+// Maximum and sum over the four lanes that hold one column (l, l ^ 16,
+// l ^ 32, l ^ 48).
+__device__ __forceinline__ float column_max(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float column_sum(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// ---------------------------------------------------------------------------
+// Which sequence, heads and tokens a workgroup takes.  The visible tokens of
+// the batch, in tiles of 32, are cut into chunks of about
+// (all tiles) * (head blocks) / target_items tiles, so that a ragged batch
+// fills the GPU evenly whatever its longest sequence; every sequence has one
+// chunk at least, and its chunks are equal but for rounding.  The lengths
+// are on the device, so each wave works this out by itself: lane l sums over
+// the sequences [l per, (l + 1) per).
+// ---------------------------------------------------------------------------
+struct Item {
+  int b, head_block;  // head_block = key head * head_blocks + block of 16 of its query heads
+  int chunk, chunks;
+  int part;            // of a sequence with several chunks: this one among all such
+  int lo, n;           // visible tokens
+  int tile, tile_end;  // this chunk's tiles (token / 32)
+};
+
+__device__ __forceinline__ void visible(const AttnParams& p, int b, int& lo, int& n) {
+  const int len = p.lengths[b];
+  n = len < 0 ? 0 : len < p.max_tokens ? len : p.max_tokens;
+  lo = p.window > 0 && n > p.window ? n - (int)p.window : 0;
+}
+__device__ __forceinline__ int tiles_of(int lo, int n) {
+  return n > lo ? (n - 1) / kTokens - lo / kTokens + 1 : 0;
+}
+__device__ __forceinline__ int chunks_of(int tiles, int size) {
+  return tiles <= size ? 1 : (tiles + size - 1) / size;
+}
+
+__device__ __forceinline__ int both_counts(int chunks) {
+  return chunks | (chunks > 1 ? chunks << 16 : 0);
+}
+
+__device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item& it) {
+  const int lane = threadIdx.x & 63;
+  const int H = p.kv_heads * p.head_blocks;
+  const int per = (p.batch + 63) / 64;
+  const int b0 = lane * per, b1 = min(p.batch, b0 + per);
+  float tiles = 0.0f;
+  for (int b = b0; b < b1; ++b) {
+    int lo, n;
+    visible(p, b, lo, n);
+    tiles += (float)tiles_of(lo, n);
   }
-  const int64_t mask = (int64_t(1) << p.page_shift) - 1;
-  for (int64_t t = lo; t < n; ++t) {
-    const int page = p.table[b * p.table_stride + (t >> p.page_shift)];
-    if (page < 0 || page >= p.pages) continue;
-    const int64_t at = ((((int64_t)page * p.kv_heads + kh) << p.page_shift) + (t & mask)) * D;
-    const auto* k = (const typename C::bits_t*)p.k_cache + at;
-    const auto* v = (const typename C::bits_t*)p.v_cache + at;
-    float s = 0.0f, vv[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int d = lane + 64 * i;
-      if (d < D) s = fmaf(q[i], C::value(k[d]), s);
-      vv[i] = d < D ? C::value(v[d]) : 0.0f;
+  // (the sum's fp32 rounding is covered by the factor: the chunks never get
+  // more than target_items + batch * H workgroups)
+  const float all = wave_add(tiles);
+  const float even = ceilf(all * (float)H / (float)p.target_items * 1.0001f);
+  const int size = __builtin_amdgcn_readfirstlane(max(p.min_tiles, (int)fminf(even, 1e8f)));
+  // chunks in the low half, those of sequences with several in the high half
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    int lo, n;
+    visible(p, b, lo, n);
+    mine += both_counts(chunks_of(tiles_of(lo, n), size));
+  }
+  const int seq_item = index / H;  // chunks before this one, over all sequences
+  const int upto = scan_add(mine);
+  const uint64_t past = __ballot((upto & 0xFFFF) > seq_item);
+  if (past == 0) return false;
+  const int owner = __builtin_ctzll(past);
+  int before = __builtin_amdgcn_readlane(upto - mine, owner);
+  int b = owner * per;
+  if (per > 1) {  // (per <= 64: a sequence per lane)
+    const int bb = b + lane;
+    int c = 0;
+    if (lane < per && bb < p.batch) {
+      int lo, n;
+      visible(p, bb, lo, n);
+      c = both_counts(chunks_of(tiles_of(lo, n), size));
     }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-    s *= p.scale * ks;
-    if (s == -INFINITY) continue;
-    const float mn = fmaxf(m, s), f = expf(m - mn), e = expf(s - mn);
-    l = l * f + e;
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = acc[i] * f + e * vv[i];
-    m = mn;
+    const int u = scan_add(c) + before;
+    const int o = __builtin_ctzll(__ballot((u & 0xFFFF) > seq_item));
+    before = __builtin_amdgcn_readlane(u - c, o);
+    b += o;
   }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int d = lane + 64 * i;
-    if (d < D) p.out[b * p.out_stride + (int64_t)h * D + d] = T::bits(l > 0.0f || l != l ? acc[i] * vs / l : 0.0f);
+  visible(p, b, it.lo, it.n);
+  it.lo = __builtin_amdgcn_readfirstlane(it.lo);
+  it.n = __builtin_amdgcn_readfirstlane(it.n);
+  const int t = tiles_of(it.lo, it.n), first = it.lo / kTokens;
+  it.b = b;
+  it.head_block = index % H;
+  it.chunks = chunks_of(t, size);
+  it.chunk = seq_item - (before & 0xFFFF);
+  it.part = (before >> 16) + it.chunk;
+  const int each = (t + it.chunks - 1) / it.chunks;
+  it.tile = first + it.chunk * each;
+  it.tile_end = first + min(t, (it.chunk + 1) * each);
+  return true;
+}
+
+// ---------------------------------------------------------------------------
+// Element types of the products: q.k in the type of q, the probabilities and
+// values in the cache's 16-bit type (fp16 for E4M3, whose values fp16 holds).
+// ---------------------------------------------------------------------------
+template <class T>
+struct Mma;
+template <>
+struct Mma<F16> {
+  using op = f16x8;
+  static __device__ __forceinline__ f32x4 mul(op a, op b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
   }
-  if (p.lse && lane == 0) p.lse[b * p.q_heads + h] = m + logf(l);
+  static __device__ __forceinline__ op split(const float (&v)[8], float (&rest)[8]) {
+    op r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      r[i] = (_Float16)v[i];
+      rest[i] = v[i] - (float)r[i];
+    }
+    return r;
+  }
+  // four e4m3 bytes -> four values
+  static __device__ __forceinline__ void widen(uint32_t w, uint32_t* out) {
+    out[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
+    out[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true));
+  }
+};
+template <>
+struct Mma<BF16> {
+  using op = bf16x8;
+  static __device__ __forceinline__ f32x4 mul(op a, op b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ op split(const float (&v)[8], float (&rest)[8]) {
+    op r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      r[i] = (__bf16)v[i];
+      rest[i] = v[i] - (float)r[i];
+    }
+    return r;
+  }
+  static __device__ __forceinline__ void widen(uint32_t w, uint32_t* out) {
+    out[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+    out[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
+  }
+};
+template <class T, class C>
+struct ValueType {
+  using type = C;
+};
+template <class T>
+struct ValueType<T, E4M3> {
+  using type = F16;
+};
+
+template <int BYTES>
+__device__ __forceinline__ void load_bytes(const uint8_t* p, uint32_t* out) {
+  if constexpr (BYTES == 16) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(p);
+    out[0] = v.x, out[1] = v.y, out[2] = v.z, out[3] = v.w;
+  } else if constexpr (BYTES == 8) {
+    const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+    out[0] = v.x, out[1] = v.y;
+  } else if constexpr (BYTES == 4) {
+    out[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else {
+    static_assert(BYTES == 2, "load_bytes: 2, 4, 8 or 16");
+    out[0] = *reinterpret_cast<const uint16_t*>(p);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Registers of a tile.  Both products of a tile are 16x16x32 matrix
+// operations whose operands need no move between lanes:
+//   S^T = K Q^T: rows are 16 tokens, columns the query heads, K = 32 of the
+//     head's values.  Lane (r = lane % 16, g = lane / 16) gives K row r,
+//     values 32 step + 8 g .. + 7 (one 16-byte load; 8-bit caches: one
+//     16-byte load at 64 u + 16 g covers the steps 2 u and 2 u + 1), and Q
+//     the same values of head r.  It gets the scores of head r (= column)
+//     and tokens 4 g .. 4 g + 3 of the 16.
+//   O^T = V^T P^T: rows are head values, columns the query heads, K = the
+//     tile's 32 tokens.  The order of K is free, so the lane's eight are the
+//     tokens whose scores it has: 4 g + i and 16 + 4 g + i.  It loads those
+//     eight rows of V, values r * PL .. of each (16 lanes read a whole row),
+//     and pairs the halves of two tokens' words by byte permutes: operation
+//     c has the row values c of every lane's PL = D / 16.
+// So the softmax needs lane moves only to join maxima, and the accumulator
+// of head r sits with its maximum and sum in the same lanes.
+// ---------------------------------------------------------------------------
+template <class T, class C, int D>
+struct Tile {
+  using V = typename ValueType<T, C>::type;
+  static constexpr int ES = sizeof(typename C::bits_t);  // bytes of a cached value
+  static constexpr int Steps = D / 32;
+  static constexpr int PL = D / 16;  // row values of V per lane
+  // V's two loads per row: E0 values (the largest power of two that one
+  // load holds), then E1
+  static constexpr int E0 = ES == 1 ? (PL >= 16 ? 16 : PL >= 8 ? 8 : 4) : (PL >= 8 ? 8 : 4);
+  static constexpr int E1 = PL - E0;
+  static constexpr int W0 = E0 * ES / 4, W1 = (E1 * ES + 3) / 4;
+  static constexpr int KW = D * ES / 4 / 4;  // words of a K row per lane
+  static constexpr int Row = D * ES;         // bytes of a cached row
+
+  uint32_t k[2][KW];
+  uint32_t v[8][W0 + W1];
+
+  __device__ __forceinline__ void load_k(const uint8_t* const (&base)[2], int lane) {
+    const int r = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint8_t* row = base[j] + r * Row;
+      if constexpr (ES == 2) {
+#pragma unroll
+        for (int s = 0; s < Steps; ++s) load_bytes<16>(row + 64 * s + 16 * g, &k[j][4 * s]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) load_bytes<16>(row + 64 * u + 16 * g, &k[j][4 * u]);
+        if constexpr (D % 64) load_bytes<8>(row + (D / 64) * 64 + 8 * g, &k[j][4 * (D / 64)]);
+      }
+    }
+  }
+  __device__ __forceinline__ void load_v(const uint8_t* const (&base)[2], int lane) {
+    const int r = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint8_t* row = base[e >> 2] + (4 * g + (e & 3)) * Row;
+      load_bytes<E0 * ES>(row + r * (E0 * ES), &v[e][0]);
+      if constexpr (E1 > 0) load_bytes<E1 * ES>(row + 16 * E0 * ES + r * (E1 * ES), &v[e][W0]);
+    }
+  }
+  // the head value of operation c in lane row r
+  static __device__ __forceinline__ int dim(int r, int c) {
+    return c < E0 ? r * E0 + c : 16 * E0 + r * E1 + (c - E0);
+  }
+
+  // operand of q.k step s: the values d(s, g, e) of Q or K (see load_k)
+  static __device__ __forceinline__ int q_dim(int s, int g) {
+    if (ES == 2 || 64 * (s / 2) + 64 > D) return 32 * s + 8 * g;
+    return 64 * (s / 2) + 16 * g + 8 * (s % 2);
+  }
+  __device__ __forceinline__ typename Mma<T>::op k_op(int j, int s) const {
+    uint32_t w[4];
+    if constexpr (ES == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = k[j][4 * s + i];
+    } else {
+      Mma<T>::widen(k[j][2 * s], w);
+      Mma<T>::widen(k[j][2 * s + 1], w + 2);
+    }
+    typename Mma<T>::op r;
+    __builtin_memcpy(&r, w, 16);
+    return r;
+  }
+  // operand of operations c and c + 1 (c even): tokens e of their row values
+  __device__ __forceinline__ void v_ops(int c, typename Mma<V>::op& a, typename Mma<V>::op& b) const {
+    uint32_t lo[4], hi[4];
+    const int in = c < E0 ? c : c - E0, base = c < E0 ? 0 : W0;
+    if constexpr (ES == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x = v[2 * i][base + in / 2], y = v[2 * i + 1][base + in / 2];
+        lo[i] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+        hi[i] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+      }
+    } else {
+      // bytes (x.c, y.c, x.c+1, y.c+1), then each pair to fp16
+      const uint32_t sel = in % 4 == 0 ? 0x05010400u : 0x07030602u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x = v[2 * i][base + in / 4], y = v[2 * i + 1][base + in / 4];
+        uint32_t w[2];
+        Mma<V>::widen(__builtin_amdgcn_perm(y, x, sel), w);
+        lo[i] = w[0], hi[i] = w[1];
+      }
+    }
+    __builtin_memcpy(&a, lo, 16);
+    __builtin_memcpy(&b, hi, 16);
+  }
+};
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// A maximum is raised only where a score passes it by more than kSlack (in
+// powers of two), so most tiles need no lane moves and no rescaling.
+// Probabilities are kept 2^kLift times their value: at most 2^(kLift +
+// kSlack) = 2^15, inside fp16, and its subnormals begin at 2^-21 of the
+// maximum.
+constexpr float kSlack = 8.0f, kLift = 7.0f;
+
+// One workgroup per item: its waves take the chunk's tiles in turn, each
+// with its own maximum, sum and accumulator; joined through LDS, then, where
+// a sequence has several chunks, through the workspace: the workgroup that
+// arrives last adds the parts in chunk order.
+template <class T, class C, int D>
+__global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 384 ? 1 : 2) k_paged_attention(AttnParams p) {
+  using TL = Tile<T, C, D>;
+  using V = typename TL::V;
+  constexpr int PL = TL::PL;
+  constexpr int RowF = D + 4;  // floats between heads in LDS
+  __shared__ float red[kWaves][kHeads][RowF];
+  __shared__ float red_m[kWaves][kHeads], red_l[kWaves][kHeads];
+  __shared__ uint32_t arrived;
+
+  Item it;
+  if (!find_item(p, blockIdx.x, it)) return;
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kh = it.head_block / p.head_blocks, hb = it.head_block % p.head_blocks;
+  const int heads = min(kHeads, p.group - hb * kHeads);
+  const int h0 = kh * p.group + hb * kHeads;
+
+  typename Mma<T>::op q[TL::Steps];
+#pragma unroll
+  for (int s = 0; s < TL::Steps; ++s) {
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (r < heads)
+      load_bytes<16>(reinterpret_cast<const uint8_t*>(p.q + it.b * p.q_stride + (int64_t)(h0 + r) * D + TL::q_dim(s, g)), w);
+    __builtin_memcpy(&q[s], w, 16);
+  }
+  const float factor = p.scale * (p.k_scale ? p.k_scale[kh] : 1.0f) * kLog2e;
+
+  f32x4 acc[PL];
+#pragma unroll
+  for (int c = 0; c < PL; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  float m = -FLT_MAX, l = 0.0f;
+
+  // the page numbers of this wave's tiles, a tile per lane (64 at a time)
+  const int32_t* table = p.table + it.b * p.table_stride;
+  int page_of[2] = {-1, -1};
+  auto load_pages = [&](int tile) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int t = (tile + kWaves * lane) * kTokens + 16 * j;
+      page_of[j] = tile + kWaves * lane < it.tile_end && t < it.n ? table[t >> p.page_shift] : -1;
+      if (page_of[j] >= p.pages) page_of[j] = -1;
+    }
+  };
+  struct Place {
+    const uint8_t *k[2], *v[2];
+    bool ok[2];
+  };
+  auto place = [&](int step, int tile) {
+    Place a;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int page = __builtin_amdgcn_readlane(page_of[j], step & 63);
+      a.ok[j] = page >= 0;
+      const int t = (tile * kTokens + 16 * j) & ((1 << p.page_shift) - 1);
+      const int64_t at = ((((int64_t)(page < 0 ? 0 : page) * p.kv_heads + kh) << p.page_shift) + t) * TL::Row;
+      a.k[j] = p.k_cache + at;
+      a.v[j] = p.v_cache + at;
+    }
+    return a;
+  };
+
+  TL tl;
+  const int first = it.tile + wave;
+  Place now;
+  if (first < it.tile_end) {
+    load_pages(first);
+    now = place(0, first);
+    tl.load_k(now.k, lane);
+    tl.load_v(now.v, lane);
+  }
+  for (int tile = first, step = 0; tile < it.tile_end; tile += kWaves, ++step) {
+    const bool more = tile + kWaves < it.tile_end;
+    // scores of head r: tokens 16 j + 4 g + i
+    f32x4 s[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      s[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int st = 0; st < TL::Steps; ++st) s[j] = Mma<T>::mul(tl.k_op(j, st), q[st], s[j]);
+    }
+    Place next;
+    if (more) {
+      if (((step + 1) & 63) == 0) load_pages(tile + kWaves);
+      next = place(step + 1, tile + kWaves);
+      tl.load_k(next.k, lane);
+    }
+    const int t0 = tile * kTokens;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = s[e >> 2][e & 3] * factor;
+    if (!(t0 >= it.lo && t0 + kTokens <= it.n && now.ok[0] && now.ok[1])) {
+      // hidden tokens: no score, and no value that could be NaN
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int t = t0 + 16 * (e >> 2) + 4 * g + (e & 3);
+        const bool seen = now.ok[e >> 2] && t >= it.lo && t < it.n;
+        x[e] = seen ? x[e] : -INFINITY;
+#pragma unroll
+        for (int w = 0; w < TL::W0 + TL::W1; ++w) tl.v[e][w] = seen ? tl.v[e][w] : 0u;
+      }
+    }
+    float top = x[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+    if (__any(top > m + kSlack)) {
+      const float mn = fmaxf(m, column_max(top));
+      const float f = __builtin_amdgcn_exp2f(m - mn);
+      l *= f;
+#pragma unroll
+      for (int c = 0; c < PL; ++c) acc[c] *= f;
+      m = mn;
+    }
+    float pr[8], rest[8], none[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      pr[e] = __builtin_amdgcn_exp2f(x[e] - m + kLift);
+      l += pr[e];
+    }
+    const typename Mma<V>::op hi = Mma<V>::split(pr, rest), lo = Mma<V>::split(rest, none);
+#pragma unroll
+    for (int c = 0; c < PL; c += 2) {
+      typename Mma<V>::op a, b;
+      tl.v_ops(c, a, b);
+      acc[c] = Mma<V>::mul(a, hi, acc[c]);
+      acc[c] = Mma<V>::mul(a, lo, acc[c]);
+      acc[c + 1] = Mma<V>::mul(b, hi, acc[c + 1]);
+      acc[c + 1] = Mma<V>::mul(b, lo, acc[c + 1]);
+    }
+    if (more) {
+      tl.load_v(next.v, lane);
+      now = next;
+    }
+  }
+
+  // the waves' parts
+  l = column_sum(l);
+  if (g == 0) red_m[wave][r] = m, red_l[wave][r] = l;
+  __syncthreads();
+  float mw = red_m[0][r];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) mw = fmaxf(mw, red_m[w][r]);
+  if (r < heads) {
+    const float f = __builtin_amdgcn_exp2f(m - mw);
+#pragma unroll
+    for (int c = 0; c < PL; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) red[wave][r][TL::dim(4 * g + i, c)] = acc[c][i] * f;
+  }
+  __syncthreads();
+  const float vs = p.v_scale ? p.v_scale[kh] : 1.0f;
+  const int H = p.kv_heads * p.head_blocks;
+  const int64_t slot = (int64_t)min(kHeads, p.group) * (D + 2);  // floats of a part
+  float* part = p.parts + ((int64_t)it.part * H + it.head_block) * slot;
+  for (int i = threadIdx.x; i < heads * D; i += 64 * kWaves) {
+    const int h = i / D, d = i % D;
+    float mh = red_m[0][h], lh = 0.0f, o = 0.0f;
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) mh = fmaxf(mh, red_m[w][h]);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      lh += red_l[w][h] * __builtin_amdgcn_exp2f(red_m[w][h] - mh);
+      o += red[w][h][d];
+    }
+    if (it.chunks == 1) {
+      const bool none = lh == 0.0f;
+      p.out[it.b * p.out_stride + (int64_t)(h0 + h) * D + d] = T::bits(none ? 0.0f : o * vs / lh);
+      if (d == 0 && p.lse)
+        p.lse[(int64_t)it.b * p.q_heads + h0 + h] = none ? -INFINITY : (mh + (log2f(lh) - kLift)) * kLn2;
+    } else {
+      part[h * (D + 2) + d] = o;
+      if (d == 0) part[h * (D + 2) + D] = mh, part[h * (D + 2) + D + 1] = lh;
+    }
+  }
+  if (it.chunks == 1) return;
+
+  // this part is written before its arrival shows; the last arrival reads
+  // the others' after it
+  __threadfence();
+  __syncthreads();
+  uint32_t* counter = p.counters + (it.part - it.chunk) * H + it.head_block;
+  if (threadIdx.x == 0)
+    arrived = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (arrived != (uint32_t)it.chunks - 1) return;
+  __threadfence();
+  if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const float* parts = part - (int64_t)it.chunk * H * slot;
+  for (int i = threadIdx.x; i < heads * D; i += 64 * kWaves) {
+    const int h = i / D, d = i % D;
+    float mh = -FLT_MAX, lh = 0.0f, o = 0.0f;
+    for (int c = 0; c < it.chunks; ++c) mh = fmaxf(mh, parts[c * H * slot + h * (D + 2) + D]);
+    for (int c = 0; c < it.chunks; ++c) {
+      const float* x = parts + c * H * slot + h * (D + 2);
+      const float f = __builtin_amdgcn_exp2f(x[D] - mh);
+      lh += x[D + 1] * f;
+      o += x[d] * f;
+    }
+    const bool none = lh == 0.0f;
+    p.out[it.b * p.out_stride + (int64_t)(h0 + h) * D + d] = T::bits(none ? 0.0f : o * vs / lh);
+    if (d == 0 && p.lse)
+      p.lse[(int64_t)it.b * p.q_heads + h0 + h] = none ? -INFINITY : (mh + (log2f(lh) - kLift)) * kLn2;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// plan and launch
+// ---------------------------------------------------------------------------
+constexpr int kMinTiles = 4;  // a tile per wave
+
+struct AttnPlan {
+  int64_t heads;  // head blocks of all key heads
+  int64_t target, items, parts;
+  uint64_t total_bytes;
+};
+// The arrival counters sit at the start of every workspace, whatever the
+// call's shape, so that one workspace serves any sequence of calls: a
+// sequence of several chunks counts in the word of its first part.
+constexpr uint64_t kCounterBytes = BGG_ATTENTION_COUNTER_BYTES;
+
+AttnPlan plan_attention(const bgg_cache_desc* c, int64_t q_heads, int64_t batch) {
+  AttnPlan p;
+  p.heads = c->kv_heads * ceil_div(q_heads / c->kv_heads, kHeads);
+  p.target = std::min<int64_t>(2 * device_cus(), kCounterBytes / 8);
+  p.items = p.target + batch * p.heads;
+  // (a sequence of n > 1 chunks has more than (n - 1) >= n / 2 full ones)
+  p.parts = 2 * p.target;
+  const int64_t heads = std::min<int64_t>(kHeads, q_heads / c->kv_heads);
+  p.total_bytes = kCounterBytes + align256((uint64_t)(p.parts * heads * (c->head_dim + 2) * 4));
+  return p;
 }
 
 template <class T, class C>
-void launch_dim(const AttnParams& p, int64_t batch, int64_t head_dim, hipStream_t s) {
-  const dim3 grid((unsigned)p.q_heads, (unsigned)batch), block(64);
+void launch_dim(const AttnParams& p, int64_t items, int64_t head_dim, hipStream_t s) {
+  const dim3 grid((unsigned)items), block(64 * kWaves);
   switch (head_dim) {
     case 64: hipLaunchKernelGGL((k_paged_attention<T, C, 64>), grid, block, 0, s, p); break;
     case 96: hipLaunchKernelGGL((k_paged_attention<T, C, 96>), grid, block, 0, s, p); break;
@@ -85,10 +601,6 @@ void launch_dim(const AttnParams& p, int64_t batch, int64_t head_dim, hipStream_
     case 192: hipLaunchKernelGGL((k_paged_attention<T, C, 192>), grid, block, 0, s, p); break;
     default: hipLaunchKernelGGL((k_paged_attention<T, C, 256>), grid, block, 0, s, p); break;
   }
-}
-
-uint64_t counter_bytes(const bgg_cache_desc* c, int64_t q_heads, int64_t batch) {
-  return align256(4ull * (uint64_t)batch * c->kv_heads * ceil_div(q_heads / c->kv_heads, 16));
 }
 
 }  // namespace
@@ -99,49 +611,56 @@ size_t bgg_attention_workspace_size(const bgg_cache_desc* c, int64_t q_heads, in
   if (check_cache(c) != BGG_OK || q_heads < 1 || q_heads > kMaxQHeads || q_heads % c->kv_heads ||
       batch < 1 || batch > kMaxBatch)
     return 0;
-  return (size_t)counter_bytes(c, q_heads, batch);
+  return (size_t)plan_attention(c, q_heads, batch).total_bytes;
 }
 
 bgg_status bgg_paged_attention(const bgg_cache_desc* c, const bgg_attention_args* a, void* stream) {
   bgg_status st = check_attention(c, a);
   if (st) return st;
   if (a->batch == 0) return BGG_OK;
-  const size_t need = bgg_attention_workspace_size(c, a->q_heads, a->batch);
-  if (a->workspace_bytes < need)
-    return fail(BGG_ERR_BUFFER, "bgg_paged_attention: workspace has %zu bytes, needs %zu",
-                a->workspace_bytes, need);
+  const AttnPlan plan = plan_attention(c, a->q_heads, a->batch);
+  if (a->workspace_bytes < plan.total_bytes)
+    return fail(BGG_ERR_BUFFER, "bgg_paged_attention: workspace has %zu bytes, needs %llu",
+                a->workspace_bytes, (unsigned long long)plan.total_bytes);
   AttnParams p{};
   p.q = (const uint16_t*)a->q_dev;
   p.out = (uint16_t*)a->out_dev;
   p.q_stride = a->q_stride;
   p.out_stride = a->out_stride;
   p.lse = a->lse_dev;
-  p.k_cache = a->k_cache_dev;
-  p.v_cache = a->v_cache_dev;
+  p.k_cache = (const uint8_t*)a->k_cache_dev;
+  p.v_cache = (const uint8_t*)a->v_cache_dev;
   p.k_scale = a->k_scale_dev;
   p.v_scale = a->v_scale_dev;
   p.table = a->page_table_dev;
   p.table_stride = a->table_stride;
   p.lengths = a->lengths_dev;
   p.window = a->window;
-  p.max_tokens = a->table_width * c->page_size;
+  p.counters = (uint32_t*)a->workspace;
+  p.parts = (float*)((uint8_t*)a->workspace + kCounterBytes);
+  p.max_tokens = (int)(a->table_width * c->page_size);
   p.scale = a->scale;
   p.pages = (int)c->pages;
+  p.batch = (int)a->batch;
   p.q_heads = (int)a->q_heads;
   p.kv_heads = (int)c->kv_heads;
+  p.group = (int)(a->q_heads / c->kv_heads);
+  p.head_blocks = (int)ceil_div(p.group, kHeads);
   p.page_shift = __builtin_ctzll((unsigned long long)c->page_size);
+  p.target_items = (int)plan.target;
+  p.min_tiles = kMinTiles;
   hipStream_t s = (hipStream_t)stream;
   const bool e4m3 = c->type == BGG_TYPE_E4M3;
   if (a->type == BGG_TYPE_F16) {
     if (e4m3)
-      launch_dim<F16, E4M3>(p, a->batch, c->head_dim, s);
+      launch_dim<F16, E4M3>(p, plan.items, c->head_dim, s);
     else
-      launch_dim<F16, F16>(p, a->batch, c->head_dim, s);
+      launch_dim<F16, F16>(p, plan.items, c->head_dim, s);
   } else {
     if (e4m3)
-      launch_dim<BF16, E4M3>(p, a->batch, c->head_dim, s);
+      launch_dim<BF16, E4M3>(p, plan.items, c->head_dim, s);
     else
-      launch_dim<BF16, BF16>(p, a->batch, c->head_dim, s);
+      launch_dim<BF16, BF16>(p, plan.items, c->head_dim, s);
   }
   return hip_check("bgg_paged_attention");
 }

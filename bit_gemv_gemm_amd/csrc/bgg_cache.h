@@ -6,7 +6,7 @@
 namespace bgg {
 
 constexpr int64_t kMaxQHeads = 4096;
-constexpr int64_t kMaxBatch = 65535;
+constexpr int64_t kMaxBatch = 4096;  // (a wave looks through 64 sequences per lane)
 
 // BGG_OK iff `c` is exactly what bgg_cache_describe makes for its fields.
 bgg_status check_cache(const bgg_cache_desc* c);

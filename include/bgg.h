@@ -361,6 +361,7 @@ typedef enum { BGG_TYPE_F16 = 1, BGG_TYPE_BF16 = 2, BGG_TYPE_E4M3 = 3 } bgg_type
 #define BGG_CACHE_MAGIC 0x43474742u /* "BGGC" */
 #define BGG_CACHE_VERSION 1u
 #define BGG_MAX_PAGE_SIZE 65536
+#define BGG_ATTENTION_COUNTER_BYTES 16384 /* zero words at the start of its workspace */
 
 /*
  * Descriptor of one layer's paged cache: two device buffers, keys and
@@ -479,7 +480,7 @@ bgg_status bgg_rotary_append(const bgg_cache_desc* cache, const bgg_rotary_args*
 typedef struct bgg_attention_args {
   int32_t type;            /* BGG_TYPE_F16 or BGG_TYPE_BF16: q and out */
   float scale;             /* factor on q . k, finite */
-  int64_t batch;           /* B >= 0 sequences, one new token each */
+  int64_t batch;           /* 0 <= B <= 4096 sequences, one new token each */
   int64_t q_heads;         /* a multiple of kv_heads, at most 4096 */
   int64_t window;          /* > 0: only the last `window` tokens are visible; 0: all */
   const void* q_dev;       /* [B][q_heads][head_dim] */
@@ -500,7 +501,7 @@ typedef struct bgg_attention_args {
 } bgg_attention_args;
 
 /* Device workspace bytes of bgg_paged_attention for a batch of at most
- * `batch` sequences (0 on a bad descriptor, batch < 1 or q_heads not a
+ * `batch` sequences (0 on a bad descriptor, batch outside 1..4096 or q_heads not a
  * multiple of kv_heads in 1..4096; no page passage). */
 size_t bgg_attention_workspace_size(const bgg_cache_desc* cache, int64_t q_heads, int64_t batch);
 
@@ -522,10 +523,10 @@ size_t bgg_attention_workspace_size(const bgg_cache_desc* cache, int64_t q_heads
  * fp32; the probabilities enter their product with the values as a sum of
  * two 16-bit terms; out is rounded once.  The cache is read once per 16
  * query heads of a key head.  The same inputs give the same bits.
- * `workspace`: its first 4 * batch * kv_heads * ceil(q_heads / kv_heads /
- * 16) bytes count the parts of a sequence and must be zero when a call
- * starts: zero-fill a new workspace once (or call
- * bgg_gemv_workspace_reset); every successful call leaves them zero.
+ * `workspace`: its first BGG_ATTENTION_COUNTER_BYTES count the parts of a
+ * sequence and must be zero when a call starts: zero-fill a new workspace
+ * once (or call bgg_gemv_workspace_reset); every successful call, of any
+ * shape, leaves them zero.  Calls that share a workspace must not overlap.
  * batch == 0 is a no-op.
  * Errors: BGG_ERR_NULL, BGG_ERR_DESC, BGG_ERR_FORMAT (types: a 16-bit cache
  * has the type of q), BGG_ERR_SHAPE, BGG_ERR_BUFFER (alignment, workspace

@@ -144,7 +144,7 @@ def test_rotary_descriptor_and_no_tokens():
 
 @pytest.mark.parametrize("change,status", [
     (dict(type=3), FORMAT), (dict(type=2), FORMAT), (dict(ksc=P, vsc=P), FORMAT), (dict(scale=math.nan), SHAPE),
-    (dict(scale=math.inf), SHAPE), (dict(batch=-1), SHAPE), (dict(batch=65536), SHAPE), (dict(q_heads=3), SHAPE),
+    (dict(scale=math.inf), SHAPE), (dict(batch=-1), SHAPE), (dict(batch=4097), SHAPE), (dict(q_heads=3), SHAPE),
     (dict(q_heads=0), SHAPE), (dict(q_heads=4098), SHAPE), (dict(window=-1), SHAPE), (dict(width=0), SHAPE),
     (dict(width=1 << 27, stride=1 << 27), SHAPE), (dict(stride=3), SHAPE), (dict(qs=255), SHAPE), (dict(os=128), SHAPE),
     (dict(q=0), NULL), (dict(out=0), NULL), (dict(kc=0), NULL), (dict(vc=0), NULL), (dict(table=0), NULL),
@@ -167,6 +167,6 @@ def test_attention_descriptor_workspace_and_empty_batch():
     d = describe()
     size = bgg.bgg_attention_workspace_size
     assert size(d, 4, 1) > 0 and size(d, 4, 64) >= size(d, 4, 1)
-    assert size(d, 3, 1) == size(d, 0, 1) == size(d, 4, 0) == size(d, 4, 65536) == 0
+    assert size(d, 3, 1) == size(d, 0, 1) == size(d, 4, 0) == size(d, 4, 4097) == 0
     d.version += 1
     assert size(d, 4, 1) == 0

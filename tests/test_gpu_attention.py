@@ -116,7 +116,7 @@ def run_check(c):
     d = Device(c)
     d.step()
     d.check()
-    assert not d.ws[:256].any(), "the counters are zero again"
+    assert not d.ws[:16384].any(), "the counters are zero again"
     return d
 
 
@@ -295,7 +295,8 @@ def test_long_context_sampled():
 def test_one_workspace_for_calls_of_every_size():
     """Calls in stream order share a workspace; also two captured graphs,
     replayed in turn with eager calls between them."""
-    cs = [case([900, 30], hq=12, hk=2, seed=1), case([5] * 9, hq=4, hk=4, D=64, seed=2), case([2500], hq=32, hk=2, seed=3)]
+    cs = [case([900, 30], hq=12, hk=2, seed=1), case([5] * 9, hq=4, hk=4, D=64, seed=2), case([2500], hq=32, hk=2, seed=3),
+          case([10] * 30 + [300 + 90 * i for i in range(12)], hq=16, hk=16, D=64, seed=4)]
     ds = [Device(c) for c in cs]
     ws = bgg.workspace(max(d.ws.numel() for d in ds))
     want = []
@@ -322,10 +323,11 @@ def test_one_workspace_for_calls_of_every_size():
         graphs[0].replay()
         ds[2].step()
         graphs[1].replay()
+        ds[3].step()
         torch.cuda.synchronize()
         for d, (o, l) in zip(ds, want):
             assert torch.equal(d.out, o) and torch.equal(d.lse, l)
-    assert not ws[:256].any()
+    assert not ws[:16384].any()
 
 
 def test_lengths_that_grow_between_replays():
