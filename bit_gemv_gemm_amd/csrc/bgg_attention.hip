@@ -277,14 +277,15 @@ struct Tile {
     const int r = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const uint8_t* row = base[j] + r * Row;
+      const uint8_t* row = base[j];
+      const uint32_t at = r * Row + (ES == 2 ? 16 * g : 0);
       if constexpr (ES == 2) {
 #pragma unroll
-        for (int s = 0; s < Steps; ++s) load_bytes<16>(row + 64 * s + 16 * g, &k[j][4 * s]);
+        for (int s = 0; s < Steps; ++s) load_bytes<16>(row + at + 64 * s, &k[j][4 * s]);
       } else {
 #pragma unroll
-        for (int u = 0; u < D / 64; ++u) load_bytes<16>(row + 64 * u + 16 * g, &k[j][4 * u]);
-        if constexpr (D % 64) load_bytes<8>(row + (D / 64) * 64 + 8 * g, &k[j][4 * (D / 64)]);
+        for (int u = 0; u < D / 64; ++u) load_bytes<16>(row + (at + 16 * g) + 64 * u, &k[j][4 * u]);
+        if constexpr (D % 64) load_bytes<8>(row + (at + 8 * g) + (D / 64) * 64, &k[j][4 * (D / 64)]);
       }
     }
   }
@@ -292,9 +293,11 @@ struct Tile {
     const int r = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint8_t* row = base[e >> 2] + (4 * g + (e & 3)) * Row;
-      load_bytes<E0 * ES>(row + r * (E0 * ES), &v[e][0]);
-      if constexpr (E1 > 0) load_bytes<E1 * ES>(row + 16 * E0 * ES + r * (E1 * ES), &v[e][W0]);
+      const uint8_t* row = base[e >> 2];
+      const uint32_t at = 4 * g * Row;
+      load_bytes<E0 * ES>(row + (at + r * (E0 * ES)) + (e & 3) * Row, &v[e][0]);
+      if constexpr (E1 > 0)
+        load_bytes<E1 * ES>(row + (at + r * (E1 * ES)) + ((e & 3) * Row + 16 * E0 * ES), &v[e][W0]);
     }
   }
   // the head value of operation c in lane row r
@@ -354,6 +357,102 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // kSlack) = 2^15, inside fp16, and its subnormals begin at 2^-21 of the
 // maximum.
 constexpr float kSlack = 8.0f, kLift = 7.0f;
+
+// Floats of a part: accumulators [rows][D], maxima [rows], sums [rows].
+__host__ __device__ constexpr int64_t part_floats(int64_t rows, int64_t D) {
+  return (rows * (D + 2) + 3) / 4 * 4;
+}
+
+// Values d .. d + 3 of query head h: the accumulator over the sum, rounded.
+template <class T>
+__device__ __forceinline__ void store_out(const AttnParams& p, int b, int h, int D, int d, f32x4 o, float m,
+                                          float l, float vs) {
+  const bool none = l == 0.0f;
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    w[i] = (uint32_t)T::bits(none ? 0.0f : o[2 * i] * vs / l) |
+           ((uint32_t)T::bits(none ? 0.0f : o[2 * i + 1] * vs / l) << 16);
+  *reinterpret_cast<u32x2*>(p.out + b * p.out_stride + (int64_t)h * D + d) = u32x2{w[0], w[1]};
+  if (d == 0 && p.lse)
+    p.lse[(int64_t)b * p.q_heads + h] = none ? -INFINITY : (m + (log2f(l) - kLift)) * kLn2;
+}
+
+// The parts of a sequence's chunks (at parts, parts + step, ...) into its
+// output: maxima and sums, then the accumulators weighted, four values per
+// thread; with fewer than 256 such columns the threads also share the chunks
+// out among them.  `lds` holds 16 D + 16 * 64 floats or more.
+template <class T, int D>
+__device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, const float* parts,
+                                           int64_t step, int rows, int heads, int h0, float vs,
+                                           float* lds, float* lds16) {
+  constexpr int kThreads = 64 * kWaves, kBlock = 64;  // chunks weighted at a time
+  constexpr int kCols = (kHeads * (D / 4) + kThreads - 1) / kThreads;
+  const int tid = threadIdx.x, hr = tid & 15, cr = tid >> 4;
+  float* weight = lds;  // [kBlock][16]
+  // maxima, then sums, of head hr over the chunks cr, cr + 16, ...
+  float mh = -FLT_MAX, lh = 0.0f;
+  if (hr < heads)
+    for (int c = cr; c < it.chunks; c += 16) mh = fmaxf(mh, parts[c * step + rows * D + hr]);
+  __syncthreads();
+  weight[cr * 16 + hr] = mh;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 16; ++j) mh = fmaxf(mh, weight[j * 16 + hr]);
+  __syncthreads();
+  const int columns = heads * (D / 4);
+  const int share = columns >= kThreads ? 1 : kThreads / columns;  // threads per column
+  const int part_of = share > 1 ? tid / columns : 0, col0 = share > 1 ? tid % columns : tid;
+  f32x4 o[kCols];
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) o[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int c0 = 0; c0 < it.chunks; c0 += kBlock) {
+    const int n = min(kBlock, it.chunks - c0);
+    if (c0) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kBlock / 16; ++j) {
+      const int c = cr + 16 * j;
+      float w = 0.0f;
+      if (c < n && hr < heads) {
+        const float* x = parts + (c0 + c) * step + rows * D + hr;
+        w = __builtin_amdgcn_exp2f(x[0] - mh);
+        lh += x[rows] * w;
+      }
+      weight[c * 16 + hr] = w;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) {
+      const int col = col0 + k * kThreads;
+      if (col >= columns || part_of >= share) continue;
+      const int h = col / (D / 4);
+      const float* x = parts + c0 * step + 4 * col;
+#pragma unroll 16
+      for (int c = part_of; c < n; c += share)
+        o[k] += *reinterpret_cast<const f32x4*>(x + c * step) * weight[c * 16 + h];
+    }
+  }
+  // the sums of the 16 threads of a head, and the shares of a column
+  float* sums = lds + kBlock * 16;
+  __syncthreads();
+  weight[cr * 16 + hr] = lh;
+  if (cr == 0) lds16[hr] = mh;
+  if (share > 1 && part_of > 0 && part_of < share)
+    *reinterpret_cast<f32x4*>(sums + 4 * (part_of * columns + col0)) = o[0];
+  __syncthreads();
+  if (part_of > 0) return;
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) {
+    const int col = col0 + k * kThreads;
+    if (col >= columns) continue;
+    for (int j = 1; j < share; ++j) o[k] += *reinterpret_cast<const f32x4*>(sums + 4 * (j * columns + col));
+    const int h = col / (D / 4);
+    float l = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) l += weight[j * 16 + h];
+    store_out<T>(p, it.b, h0 + h, D, 4 * (col % (D / 4)), o[k], lds16[h], l, vs);
+  }
+}
 
 // One workgroup per item: its waves take the chunk's tiles in turn, each
 // with its own maximum, sum and accumulator; joined through LDS, then, where
@@ -428,9 +527,13 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
     load_pages(first);
     now = place(0, first);
     tl.load_k(now.k, lane);
+    __builtin_amdgcn_sched_barrier(0);  // (keys first: the loop waits for them alone)
     tl.load_v(now.v, lane);
+    __builtin_amdgcn_sched_barrier(0);
   }
   for (int tile = first, step = 0; tile < it.tile_end; tile += kWaves, ++step) {
+    // the tile after this one, or this one again (loads without a branch
+    // keep the waits for the loads before them exact)
     const bool more = tile + kWaves < it.tile_end;
     // scores of head r: tokens 16 j + 4 g + i
     f32x4 s[2];
@@ -440,12 +543,11 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
 #pragma unroll
       for (int st = 0; st < TL::Steps; ++st) s[j] = Mma<T>::mul(tl.k_op(j, st), q[st], s[j]);
     }
-    Place next;
-    if (more) {
-      if (((step + 1) & 63) == 0) load_pages(tile + kWaves);
-      next = place(step + 1, tile + kWaves);
-      tl.load_k(next.k, lane);
-    }
+    if (more && ((step + 1) & 63) == 0) load_pages(tile + kWaves);
+    const Place next = place(step + more, tile + (more ? kWaves : 0));
+    __builtin_amdgcn_sched_barrier(0);
+    tl.load_k(next.k, lane);
+    __builtin_amdgcn_sched_barrier(0);
     const int t0 = tile * kTokens;
     float x[8];
 #pragma unroll
@@ -488,10 +590,10 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
       acc[c + 1] = Mma<V>::mul(b, hi, acc[c + 1]);
       acc[c + 1] = Mma<V>::mul(b, lo, acc[c + 1]);
     }
-    if (more) {
-      tl.load_v(next.v, lane);
-      now = next;
-    }
+    __builtin_amdgcn_sched_barrier(0);
+    tl.load_v(next.v, lane);
+    __builtin_amdgcn_sched_barrier(0);
+    now = next;
   }
 
   // the waves' parts
@@ -509,28 +611,28 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
       for (int i = 0; i < 4; ++i) red[wave][r][TL::dim(4 * g + i, c)] = acc[c][i] * f;
   }
   __syncthreads();
+  // thread i takes four values of a head
   const float vs = p.v_scale ? p.v_scale[kh] : 1.0f;
-  const int H = p.kv_heads * p.head_blocks;
-  const int64_t slot = (int64_t)min(kHeads, p.group) * (D + 2);  // floats of a part
+  const int H = p.kv_heads * p.head_blocks, rows = min(kHeads, p.group);
+  const int64_t slot = part_floats(rows, D);
   float* part = p.parts + ((int64_t)it.part * H + it.head_block) * slot;
-  for (int i = threadIdx.x; i < heads * D; i += 64 * kWaves) {
-    const int h = i / D, d = i % D;
-    float mh = red_m[0][h], lh = 0.0f, o = 0.0f;
+  const int columns = heads * (D / 4);
+  for (int i = threadIdx.x; i < columns; i += 64 * kWaves) {
+    const int h = i / (D / 4), d = 4 * (i % (D / 4));
+    float mh = red_m[0][h], lh = 0.0f;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) mh = fmaxf(mh, red_m[w][h]);
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
       lh += red_l[w][h] * __builtin_amdgcn_exp2f(red_m[w][h] - mh);
-      o += red[w][h][d];
+      o += *reinterpret_cast<const f32x4*>(&red[w][h][d]);
     }
     if (it.chunks == 1) {
-      const bool none = lh == 0.0f;
-      p.out[it.b * p.out_stride + (int64_t)(h0 + h) * D + d] = T::bits(none ? 0.0f : o * vs / lh);
-      if (d == 0 && p.lse)
-        p.lse[(int64_t)it.b * p.q_heads + h0 + h] = none ? -INFINITY : (mh + (log2f(lh) - kLift)) * kLn2;
+      store_out<T>(p, it.b, h0 + h, D, d, o, mh, lh, vs);
     } else {
-      part[h * (D + 2) + d] = o;
-      if (d == 0) part[h * (D + 2) + D] = mh, part[h * (D + 2) + D + 1] = lh;
+      *reinterpret_cast<f32x4*>(part + h * D + d) = o;
+      if (d == 0) part[rows * D + h] = mh, part[rows * D + rows + h] = lh;
     }
   }
   if (it.chunks == 1) return;
@@ -546,22 +648,8 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
   if (arrived != (uint32_t)it.chunks - 1) return;
   __threadfence();
   if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  const float* parts = part - (int64_t)it.chunk * H * slot;
-  for (int i = threadIdx.x; i < heads * D; i += 64 * kWaves) {
-    const int h = i / D, d = i % D;
-    float mh = -FLT_MAX, lh = 0.0f, o = 0.0f;
-    for (int c = 0; c < it.chunks; ++c) mh = fmaxf(mh, parts[c * H * slot + h * (D + 2) + D]);
-    for (int c = 0; c < it.chunks; ++c) {
-      const float* x = parts + c * H * slot + h * (D + 2);
-      const float f = __builtin_amdgcn_exp2f(x[D] - mh);
-      lh += x[D + 1] * f;
-      o += x[d] * f;
-    }
-    const bool none = lh == 0.0f;
-    p.out[it.b * p.out_stride + (int64_t)(h0 + h) * D + d] = T::bits(none ? 0.0f : o * vs / lh);
-    if (d == 0 && p.lse)
-      p.lse[(int64_t)it.b * p.q_heads + h0 + h] = none ? -INFINITY : (mh + (log2f(lh) - kLift)) * kLn2;
-  }
+  join_parts<T, D>(p, it, part - (int64_t)it.chunk * H * slot, H * slot, rows, heads, h0, vs,
+                   &red[0][0][0], &red_m[0][0]);
 }
 
 // ---------------------------------------------------------------------------
@@ -586,8 +674,8 @@ AttnPlan plan_attention(const bgg_cache_desc* c, int64_t q_heads, int64_t batch)
   p.items = p.target + batch * p.heads;
   // (a sequence of n > 1 chunks has more than (n - 1) >= n / 2 full ones)
   p.parts = 2 * p.target;
-  const int64_t heads = std::min<int64_t>(kHeads, q_heads / c->kv_heads);
-  p.total_bytes = kCounterBytes + align256((uint64_t)(p.parts * heads * (c->head_dim + 2) * 4));
+  p.total_bytes = kCounterBytes + align256(
+      4 * (uint64_t)(p.parts * part_floats(std::min<int64_t>(kHeads, q_heads / c->kv_heads), c->head_dim)));
   return p;
 }
 
