@@ -55,10 +55,19 @@ __device__ __forceinline__ int scan_add(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2, 3
   return v;
 }
+template <int MOVE, int ROWS>
+__device__ __forceinline__ float add_from(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), MOVE, ROWS, 0xF, false));
+}
+// Sum over all lanes, in every lane.
 __device__ __forceinline__ float wave_add(float v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
-  return v;
+  v = add_from<0x111, 0xF>(v);
+  v = add_from<0x112, 0xF>(v);
+  v = add_from<0x114, 0xF>(v);
+  v = add_from<0x118, 0xF>(v);
+  v = add_from<0x142, 0xA>(v);
+  v = add_from<0x143, 0xC>(v);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 // Maximum and sum over the four lanes that hold one column (l, l ^ 16,
 // l ^ 32, l ^ 48).
@@ -122,17 +131,38 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item& 
   // (the sum's fp32 rounding is covered by the factor: the chunks never get
   // more than target_items + batch * H workgroups)
   const float all = wave_add(tiles);
-  const float even = ceilf(all * (float)H / (float)p.target_items * 1.0001f);
-  const int size = __builtin_amdgcn_readfirstlane(max(p.min_tiles, (int)fminf(even, 1e8f)));
+  const float even = fminf(ceilf(all * (float)H / (float)p.target_items * 1.0001f), 1e8f);
   // chunks in the low half, those of sequences with several in the high half
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    int lo, n;
-    visible(p, b, lo, n);
-    mine += both_counts(chunks_of(tiles_of(lo, n), size));
+  auto counts = [&](int size) {
+    int c = 0;
+    for (int b = b0; b < b1; ++b) {
+      int lo, n;
+      visible(p, b, lo, n);
+      c += both_counts(chunks_of(tiles_of(lo, n), size));
+    }
+    return c;
+  };
+  // The last chunk of every sequence is a full workgroup too, so the even
+  // size gives a few workgroups more than the GPU takes at once, and they
+  // would run alone at the end: a larger size that gives target_items at
+  // most, if one up to twice the even size does (16 ragged sequences up to
+  // 8000 tokens of 4 x 256 bf16: 280 workgroups 39.8 us, 256 29.7 us).
+  int size = 0, mine = 0, upto = 0;
+  if (p.batch * H <= p.target_items) {
+#pragma unroll 1
+    for (int k = 8; k <= 16; k += 2) {
+      size = max(p.min_tiles, (int)(even * (float)k * 0.125f));
+      mine = counts(size);
+      upto = scan_add(mine);
+      if ((__builtin_amdgcn_readlane(upto, 63) & 0xFFFF) * H <= p.target_items) break;
+    }
+  } else {
+    size = max(p.min_tiles, (int)even);
+    mine = counts(size);
+    upto = scan_add(mine);
   }
+  size = __builtin_amdgcn_readfirstlane(size);
   const int seq_item = index / H;  // chunks before this one, over all sequences
-  const int upto = scan_add(mine);
   const uint64_t past = __ballot((upto & 0xFFFF) > seq_item);
   if (past == 0) return false;
   const int owner = __builtin_ctzll(past);
@@ -363,6 +393,26 @@ __host__ __device__ constexpr int64_t part_floats(int64_t rows, int64_t D) {
   return (rows * (D + 2) + 3) / 4 * 4;
 }
 
+// The parts pass from one workgroup to another, maybe on another die with
+// its own L2, by stores and loads that go through to the memory all dies
+// share (relaxed atomics of device scope).  Plain stores with a fence would
+// write back and drop a die's whole L2 for every workgroup: 2 us each, one
+// after the other (1 x 262144 tokens in 512 workgroups: 283 us).
+__device__ __forceinline__ void put2(float* p, float a, float b) {
+  const uint64_t v = (uint64_t)__float_as_uint(a) | ((uint64_t)__float_as_uint(b) << 32);
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void put1(float* p, float a) {
+  __hip_atomic_store(reinterpret_cast<uint32_t*>(p), __float_as_uint(a), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float get1(const float* p) {
+  return __uint_as_float(
+      __hip_atomic_load(reinterpret_cast<const uint32_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+}
+__device__ __forceinline__ uint64_t get2(const float* p) {
+  return __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // Values d .. d + 3 of query head h: the accumulator over the sum, rounded.
 template <class T>
 __device__ __forceinline__ void store_out(const AttnParams& p, int b, int h, int D, int d, f32x4 o, float m,
@@ -380,45 +430,73 @@ __device__ __forceinline__ void store_out(const AttnParams& p, int b, int h, int
 
 // The parts of a sequence's chunks (at parts, parts + step, ...) into its
 // output: maxima and sums, then the accumulators weighted, four values per
-// thread; with fewer than 256 such columns the threads also share the chunks
-// out among them.  `lds` holds 16 D + 16 * 64 floats or more.
+// thread; with fewer columns of four than threads the threads also share the
+// chunks out among them.  The loads that need nothing but addresses -- the
+// maxima and sums of the first 64 chunks and the first accumulators -- go
+// out together, so that up to 16 chunks cost one trip to memory.  `lds` holds
+// 16 * 64 + 16 D floats or more.
 template <class T, int D>
 __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, const float* parts,
                                            int64_t step, int rows, int heads, int h0, float vs,
                                            float* lds, float* lds16) {
-  constexpr int kThreads = 64 * kWaves, kBlock = 64;  // chunks weighted at a time
+  constexpr int kThreads = 64 * kWaves, kRows = kThreads / 16;  // threads of a head
+  constexpr int kBlock = 64;                                    // chunks weighted at a time
+  constexpr int kMine = kBlock / kRows;                         // of them by one thread
+  constexpr int kFlight = 16;                                   // a thread's parts in flight
   constexpr int kCols = (kHeads * (D / 4) + kThreads - 1) / kThreads;
   const int tid = threadIdx.x, hr = tid & 15, cr = tid >> 4;
   float* weight = lds;  // [kBlock][16]
-  // maxima, then sums, of head hr over the chunks cr, cr + 16, ...
-  float mh = -FLT_MAX, lh = 0.0f;
-  if (hr < heads)
-    for (int c = cr; c < it.chunks; c += 16) mh = fmaxf(mh, parts[c * step + rows * D + hr]);
-  __syncthreads();
-  weight[cr * 16 + hr] = mh;
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < 16; ++j) mh = fmaxf(mh, weight[j * 16 + hr]);
-  __syncthreads();
   const int columns = heads * (D / 4);
   const int share = columns >= kThreads ? 1 : kThreads / columns;  // threads per column
   const int part_of = share > 1 ? tid / columns : 0, col0 = share > 1 ? tid % columns : tid;
+
+  // maxima and sums of head hr over the chunks c0 + cr, c0 + cr + kRows, ...
+  float mc[kMine], lc[kMine];
+  auto load_stats = [&](int c0) {
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      const int c = c0 + cr + kRows * j;
+      const bool in = c < it.chunks && hr < heads;
+      const float* x = parts + (in ? c : 0) * step + rows * D + (in ? hr : 0);
+      mc[j] = get1(x);
+      lc[j] = get1(x + rows);
+      if (!in) mc[j] = -FLT_MAX, lc[j] = 0.0f;
+    }
+  };
+  uint64_t a[kFlight][2];
+  auto load_flight = [&](int col, int c0, int n, int cb) {
+    const float* x = parts + c0 * step + 4 * col;
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j) {
+      const int c = min(cb + j * share, n - 1);
+      a[j][0] = get2(x + c * step);
+      a[j][1] = get2(x + c * step + 2);
+    }
+  };
+  load_stats(0);
+  load_flight(min(col0, columns - 1), 0, min(kBlock, it.chunks), min(part_of, share - 1));
+
+  float mh = -FLT_MAX, lh = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) mh = fmaxf(mh, mc[j]);
+  if (hr < heads)
+    for (int c = kBlock + cr; c < it.chunks; c += kRows) mh = fmaxf(mh, get1(parts + c * step + rows * D + hr));
+  weight[cr * 16 + hr] = mh;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) mh = fmaxf(mh, weight[j * 16 + hr]);
   f32x4 o[kCols];
 #pragma unroll
   for (int k = 0; k < kCols; ++k) o[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   for (int c0 = 0; c0 < it.chunks; c0 += kBlock) {
     const int n = min(kBlock, it.chunks - c0);
-    if (c0) __syncthreads();
+    if (c0) load_stats(c0);
+    __syncthreads();  // (the weights of the last block, and the maxima, are read)
 #pragma unroll
-    for (int j = 0; j < kBlock / 16; ++j) {
-      const int c = cr + 16 * j;
-      float w = 0.0f;
-      if (c < n && hr < heads) {
-        const float* x = parts + (c0 + c) * step + rows * D + hr;
-        w = __builtin_amdgcn_exp2f(x[0] - mh);
-        lh += x[rows] * w;
-      }
-      weight[c * 16 + hr] = w;
+    for (int j = 0; j < kMine; ++j) {
+      const float w = __builtin_amdgcn_exp2f(mc[j] - mh);
+      lh += lc[j] * w;
+      weight[(cr + kRows * j) * 16 + hr] = w;
     }
     __syncthreads();
 #pragma unroll
@@ -426,13 +504,19 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
       const int col = col0 + k * kThreads;
       if (col >= columns || part_of >= share) continue;
       const int h = col / (D / 4);
-      const float* x = parts + c0 * step + 4 * col;
-#pragma unroll 16
-      for (int c = part_of; c < n; c += share)
-        o[k] += *reinterpret_cast<const f32x4*>(x + c * step) * weight[c * 16 + h];
+      for (int cb = part_of; cb < n; cb += kFlight * share) {
+        if (k > 0 || c0 > 0 || cb != part_of) load_flight(col, c0, n, cb);
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j) {
+          if (cb + j * share >= n) continue;
+          const float w = weight[(cb + j * share) * 16 + h];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[k][i] += __uint_as_float((uint32_t)(a[j][i / 2] >> (32 * (i % 2)))) * w;
+        }
+      }
     }
   }
-  // the sums of the 16 threads of a head, and the shares of a column
+  // the sums of the threads of a head, and the shares of a column
   float* sums = lds + kBlock * 16;
   __syncthreads();
   weight[cr * 16 + hr] = lh;
@@ -449,7 +533,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
     const int h = col / (D / 4);
     float l = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) l += weight[j * 16 + h];
+    for (int j = 0; j < kRows; ++j) l += weight[j * 16 + h];
     store_out<T>(p, it.b, h0 + h, D, 4 * (col % (D / 4)), o[k], lds16[h], l, vs);
   }
 }
@@ -631,22 +715,23 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
     if (it.chunks == 1) {
       store_out<T>(p, it.b, h0 + h, D, d, o, mh, lh, vs);
     } else {
-      *reinterpret_cast<f32x4*>(part + h * D + d) = o;
-      if (d == 0) part[rows * D + h] = mh, part[rows * D + rows + h] = lh;
+      put2(part + h * D + d, o[0], o[1]);
+      put2(part + h * D + d + 2, o[2], o[3]);
+      if (d == 0) put1(part + rows * D + h, mh), put1(part + rows * D + rows + h, lh);
     }
   }
   if (it.chunks == 1) return;
 
-  // this part is written before its arrival shows; the last arrival reads
+  // every thread's stores of this part have reached the shared memory (their
+  // count is back to zero) before its arrival shows; the last arrival reads
   // the others' after it
-  __threadfence();
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   uint32_t* counter = p.counters + (it.part - it.chunk) * H + it.head_block;
   if (threadIdx.x == 0)
-    arrived = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    arrived = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   if (arrived != (uint32_t)it.chunks - 1) return;
-  __threadfence();
   if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   join_parts<T, D>(p, it, part - (int64_t)it.chunk * H * slot, H * slot, rows, heads, h0, vs,
                    &red[0][0][0], &red_m[0][0]);
@@ -655,7 +740,10 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
 // ---------------------------------------------------------------------------
 // plan and launch
 // ---------------------------------------------------------------------------
-constexpr int kMinTiles = 4;  // a tile per wave
+// Tiles of a chunk at least: four for each wave.  Fewer gain less than the
+// join costs (one sequence of 500 tokens, 8 x 128 f16: chunks of 4, 8, 16
+// tiles 10.3, 11.2, 9.5 us).
+constexpr int kMinTiles = 16;
 
 struct AttnPlan {
   int64_t heads;  // head blocks of all key heads
@@ -670,7 +758,10 @@ constexpr uint64_t kCounterBytes = BGG_ATTENTION_COUNTER_BYTES;
 AttnPlan plan_attention(const bgg_cache_desc* c, int64_t q_heads, int64_t batch) {
   AttnPlan p;
   p.heads = c->kv_heads * ceil_div(q_heads / c->kv_heads, kHeads);
-  p.target = std::min<int64_t>(2 * device_cus(), kCounterBytes / 8);
+  // one workgroup per CU: each one more per CU costs its own start and part
+  // (1 x 262144 tokens f16: 1, 2, 3, 4 per CU 189, 193, 200, 208 us; 16
+  // ragged sequences up to 8000 tokens of 4 x 256 bf16: 39, 44, 51, 59 us)
+  p.target = std::min<int64_t>(device_cus(), kCounterBytes / 8);
   p.items = p.target + batch * p.heads;
   // (a sequence of n > 1 chunks has more than (n - 1) >= n / 2 full ones)
   p.parts = 2 * p.target;
