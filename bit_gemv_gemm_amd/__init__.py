@@ -362,13 +362,19 @@ def _vector(t, n, dtype, dev, what):
 
 def _cache_ptrs(cache, k_cache, v_cache, dev):
     dt = _TORCH_TYPES[cache.type]
-    n = cache.pages * cache.page_size * cache.kv_heads * cache.head_dim
+    n = cache.total_bytes // dt.itemsize
     return _vector(k_cache, n, dt, dev, "k_cache"), _vector(v_cache, n, dt, dev, "v_cache")
+
+
+# the current stream's handle without building a torch.cuda.Stream (1 us of
+# a call's 8)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _run_on(dev, stream, call, cache, args, where):
     """call(cache, args, stream) with device dev current."""
-    s = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+    s = _raw_stream(dev) if stream is None else _stream(stream)
     if torch.cuda.current_device() == dev:
         st = call(cache, args, s)
     else:
