@@ -42,6 +42,14 @@ BGG_ROW_TILE = 64
 BGG_CHUNK = 16
 BGG_MAX_GEMV_M = 16
 BGG_READ_SLACK = 8192
+BGG_ACT_NONE = 0
+BGG_ACT_RELU = 1
+BGG_ACT_RELU2 = 2
+BGG_ACT_SILU = 3
+BGG_ACT_GELU = 4
+BGG_ACT_GELU_TANH = 5
+ACTIVATIONS = {"none": BGG_ACT_NONE, "relu": BGG_ACT_RELU, "relu2": BGG_ACT_RELU2, "silu": BGG_ACT_SILU,
+               "gelu": BGG_ACT_GELU, "gelu_tanh": BGG_ACT_GELU_TANH}
 BGG_TYPE_F16 = 1
 BGG_TYPE_BF16 = 2
 BGG_TYPE_E4M3 = 3
@@ -85,9 +93,10 @@ class bgg_cache_desc(ctypes.Structure):
         return "bgg_cache_desc(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
-# the argument structs of the calls on a cache (field order of bgg.h),
-# packed in one go: a ctypes.Structure takes longer to fill than its kernel
-# takes to run
+# the argument structs of the epilogue and of the calls on a cache (field
+# order of bgg.h), packed in one go: a ctypes.Structure takes longer to fill
+# than its kernel takes to run
+_EPILOGUE = struct.Struct("@iiPPPqq")
 _ROTARY_ARGS = struct.Struct("@iiqqqPPPPqqqqPPPfiPPPP")
 _ATTENTION_ARGS = struct.Struct("@ifqqqPPqqPPPPPPqqPPN")
 
@@ -120,6 +129,9 @@ _SIGS = {
     "bgg_gemv_kernel_name": ([_P, _i64, ctypes.c_char_p, _sz], _i32),
     "bgg_gemm_workspace_size": ([_P, _i64], _sz),
     "bgg_ternary_gemm": ([_P, _vp, _vp, _vp, _i64, _u32, _vp, _sz, _vp], _i32),
+    "bgg_ternary_gemv_epilogue": ([_P, _vp, _vp, _vp, _i64, _u32, _vp, _vp, _sz, _vp], _i32),
+    "bgg_gemv_run_epilogue": ([_P, _vp, _vp, _i64, _vp, _vp, _sz, _vp], _i32),
+    "bgg_ternary_gemm_epilogue": ([_P, _vp, _vp, _vp, _i64, _u32, _vp, _vp, _sz, _vp], _i32),
     "bgg_cache_describe": ([_i32, _i64, _i64, _i64, _i64, _PC], _i32),
     "bgg_rotary_frequencies": ([_i64, _f64, _i32, _f64, _f64, _f64, _f64, _vp, _vp], _i32),
     "bgg_rotary_append": ([_PC, _vp, _vp], _i32),
@@ -304,6 +316,86 @@ def bgg_ternary_gemm(desc, packed_dev, x_dev, y_dev, M: int, flags: int, workspa
                               M, flags, ws, wsb, _stream(stream)), "bgg_ternary_gemm")
 
 
+# the current stream's handle without building a torch.cuda.Stream (1 us of
+# a call's 8)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _run_on(dev, stream, where, call, *args):
+    """call(*args, stream) with device dev current."""
+    s = _raw_stream(dev) if stream is None else _stream(stream)
+    if torch.cuda.current_device() == dev:
+        st = call(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = call(*args, s)
+    if st != 0:
+        raise BggError(st, where)
+
+
+# ---------------------------------------------------------------------------
+# products with an epilogue
+# ---------------------------------------------------------------------------
+def _operand(t, M, N, dev, what):
+    """(pointer, stride) of epilogue operand t: float16 [M, N], rows of any
+    stride (None: 0, 0)."""
+    if t is None:
+        return 0, 0
+    if t.dtype is not torch.float16 or t.get_device() != dev or t.shape != (M, N) or (N > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be float16 [{M}, {N}] with contiguous rows on device {dev}")
+    return t.data_ptr(), t.stride(0) if M > 1 else N
+
+
+def _epilogue(N, M, dev, activation, bias, mul, residual):
+    mp, ms = _operand(mul, M, N, dev, "mul")
+    rp, rs = _operand(residual, M, N, dev, "residual")
+    return _EPILOGUE.pack(ACTIVATIONS[activation] if isinstance(activation, str) else activation, 0,
+                          _vector(bias, N, torch.float16, dev, "bias"), mp, rp, ms, rs)
+
+
+def _device_of(y, *others):
+    """y's device, which the others (or None) share."""
+    dev = y.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("the buffers of one call must be on one device")
+    return dev
+
+
+def bgg_ternary_gemv_epilogue(desc, packed_dev, x_dev, y_dev, M: int, flags: int, workspace, activation="none",
+                              bias=None, mul=None, residual=None, stream=None) -> None:
+    """y = act(W x' + bias) * mul + residual, 1 <= M <= 16 tokens; bias [N],
+    mul and residual [M, N], all float16 or None."""
+    dev, N = _device_of(y_dev, packed_dev, x_dev, workspace), desc.N
+    wsb = workspace.numel() * workspace.element_size()
+    _run_on(dev, stream, "bgg_ternary_gemv_epilogue", _lib.bgg_ternary_gemv_epilogue, desc,
+            _dev_ptr(packed_dev, desc.total_bytes, "packed"), _dev_ptr(x_dev, M * desc.K * 2, "x"),
+            _dev_ptr(y_dev, M * N * 2, "y"), M, flags, _epilogue(N, M, dev, activation, bias, mul, residual),
+            _dev_ptr(workspace, 0, "workspace"), wsb)
+
+
+def bgg_gemv_run_epilogue(desc, packed_dev, y_dev, M: int, workspace, activation="none", bias=None, mul=None,
+                          residual=None, stream=None) -> None:
+    """bgg_gemv_run with an epilogue (see bgg_ternary_gemv_epilogue)."""
+    dev, N = _device_of(y_dev, packed_dev, workspace), desc.N
+    wsb = workspace.numel() * workspace.element_size()
+    _run_on(dev, stream, "bgg_gemv_run_epilogue", _lib.bgg_gemv_run_epilogue, desc,
+            _dev_ptr(packed_dev, desc.total_bytes, "packed"), _dev_ptr(y_dev, M * N * 2, "y"), M,
+            _epilogue(N, M, dev, activation, bias, mul, residual), _dev_ptr(workspace, 0, "workspace"), wsb)
+
+
+def bgg_ternary_gemm_epilogue(desc, packed_dev, x_dev, y_dev, M: int, flags: int, workspace, activation="none",
+                              bias=None, mul=None, residual=None, stream=None) -> None:
+    """y = act(W x' + bias) * mul + residual for a prompt of M tokens."""
+    dev, N = _device_of(y_dev, packed_dev, x_dev, workspace), desc.N
+    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _run_on(dev, stream, "bgg_ternary_gemm_epilogue", _lib.bgg_ternary_gemm_epilogue, desc,
+            _dev_ptr(packed_dev, desc.total_bytes, "packed"), _dev_ptr(x_dev, M * desc.K * 2, "x"),
+            _dev_ptr(y_dev, M * N * 2, "y"), M, flags, _epilogue(N, M, dev, activation, bias, mul, residual),
+            _dev_ptr(workspace, 0, "workspace"), wsb)
+
+
 # ---------------------------------------------------------------------------
 # the paged cache, rotary positions and attention
 # ---------------------------------------------------------------------------
@@ -366,24 +458,6 @@ def _cache_ptrs(cache, k_cache, v_cache, dev):
     return _vector(k_cache, n, dt, dev, "k_cache"), _vector(v_cache, n, dt, dev, "v_cache")
 
 
-# the current stream's handle without building a torch.cuda.Stream (1 us of
-# a call's 8)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
-def _run_on(dev, stream, call, cache, args, where):
-    """call(cache, args, stream) with device dev current."""
-    s = _raw_stream(dev) if stream is None else _stream(stream)
-    if torch.cuda.current_device() == dev:
-        st = call(cache, args, s)
-    else:
-        with torch.cuda.device(dev):
-            st = call(cache, args, s)
-    if st != 0:
-        raise BggError(st, where)
-
-
 def bgg_rotary_append(cache: bgg_cache_desc, k_cache, v_cache, positions, slots, freqs, q=None, q_out=None, k=None,
                       v=None, layout="half", magnitude: float = 1.0, k_scale=None, v_scale=None, stream=None) -> None:
     """Rotate q into q_out, and k and v into their slots of the cache.  The
@@ -421,7 +495,7 @@ def bgg_rotary_append(cache: bgg_cache_desc, k_cache, v_cache, positions, slots,
         _vector(freqs, 1, torch.float32, dev, "freqs"), magnitude, 0, kc, vc,
         _vector(k_scale, cache.kv_heads, torch.float32, dev, "k_scale"),
         _vector(v_scale, cache.kv_heads, torch.float32, dev, "v_scale"))
-    _run_on(dev, stream, _lib.bgg_rotary_append, cache, args, "bgg_rotary_append")
+    _run_on(dev, stream, "bgg_rotary_append", _lib.bgg_rotary_append, cache, args)
 
 
 def bgg_paged_attention(cache: bgg_cache_desc, k_cache, v_cache, page_table, lengths, q, out, workspace,
@@ -454,7 +528,7 @@ def bgg_paged_attention(cache: bgg_cache_desc, k_cache, v_cache, page_table, len
         _vector(v_scale, cache.kv_heads, torch.float32, dev, "v_scale"), page_table.data_ptr(), width,
         page_table.stride(0) if B > 1 else width, _vector(lengths, B, torch.int32, dev, "lengths"),
         workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _run_on(dev, stream, _lib.bgg_paged_attention, cache, args, "bgg_paged_attention")
+    _run_on(dev, stream, "bgg_paged_attention", _lib.bgg_paged_attention, cache, args)
 
 
 # ---------------------------------------------------------------------------

@@ -12,7 +12,8 @@ LIB = os.path.join(HERE, "libbgg.so")
 PROBE_LIB = os.path.join(HERE, "libbgg_probe.so")
 PROBE_SOURCES = ["probe_stream.hip"]
 SOURCES = ["bgg_host.cpp", "bgg_rotate.hip", "bgg_gemv.hip", "bgg_gemv_noalloc.hip", "bgg_mxv.hip", "bgg_unpack.hip", "bgg_gemm.hip",
-           "bgg_ternarize.hip", "bgg_cache.cpp", "bgg_rotary.hip", "bgg_attention.hip"]
+           "bgg_ternarize.hip", "bgg_cache.cpp", "bgg_rotary.hip", "bgg_attention.hip",
+           "bgg_epilogue.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # Packed-fp32 VALU forms are kept out of the generated code.

@@ -283,11 +283,13 @@ inline int64_t device_cus() {
 // PQ2_0 for 1..4 tokens, PTQ1_0 for 1..2): whether it serves (format, M),
 // the workspace bytes it uses at the start of a GEMV workspace (row words
 // that every launch leaves zero), the name of the kernel it launches
-// (snprintf's return), and the launch.
+// (snprintf's return), and the launch (ep: the epilogue, or nullptr).
+struct EpilogueOut;
 bool mxv_supported(const bgg_weights_desc* d, int64_t M);
 uint64_t mxv_workspace_bytes();
 int mxv_kernel_name(const bgg_weights_desc* d, int64_t M, char* out, size_t cap);
 bgg_status mxv_launch(const bgg_weights_desc* d, const void* packed, const void* x, void* y,
-                      int64_t M, int rotate, void* workspace, hipStream_t st);
+                      int64_t M, int rotate, void* workspace, hipStream_t st,
+                      const EpilogueOut* ep);
 
 }  // namespace bgg

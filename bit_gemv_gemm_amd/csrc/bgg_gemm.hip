@@ -30,7 +30,7 @@
 #include <cmath>
 #include <cstdlib>
 
-#include "bgg_device.h"
+#include "bgg_epilogue.h"
 
 using bgg::fail;
 using bgg::f16x8;
@@ -65,11 +65,40 @@ __device__ __forceinline__ void lds_dma_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-__global__ void __launch_bounds__(256, 2)
-    k_gemm_pq2(const uint16_t* __restrict__ X, const uint8_t* __restrict__ packed,
+// The 16 sums of a lane in a 32 x 32 block (column n, rows m0 + 8 (r / 4) +
+// r % 4), to P (K split) or y.  An epilogue's operands of the block are all
+// loaded before its first value is stored.
+template <class Out>
+__device__ __forceinline__ void store_block(const f32x16& acc, int64_t m0, int64_t n, int64_t M, int64_t N,
+                                            float* __restrict__ P, const Out& out) {
+  if (n >= N) return;
+  if (gridDim.z > 1) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int64_t m = m0 + 8 * (r / 4) + (r % 4);
+      if (m < M) P[(blockIdx.z * M + m) * N + n] = acc[r];
+    }
+    return;
+  }
+  typename Out::Operands o[16];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int64_t m = m0 + 8 * (r / 4) + (r % 4);
+    if (m < M) o[r] = out.load(m, n);
+  }
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int64_t m = m0 + 8 * (r / 4) + (r % 4);
+    if (m < M) out.store(m, n, acc[r], o[r]);
+  }
+}
+
+template <class Out>
+__device__ __forceinline__ void gemm_pq2_body(
+    const uint16_t* __restrict__ X, const uint8_t* __restrict__ packed,
                const uint16_t* __restrict__ scales, int64_t M, int64_t N, int64_t K, int64_t C,
                int64_t G,
-               int64_t NT, int64_t kmid, float* __restrict__ P, uint16_t* __restrict__ Y) {
+               int64_t NT, int64_t kmid, float* __restrict__ P, const Out& out) {
   __shared__ __attribute__((aligned(16))) uint4 As0[kBM * 16];
   __shared__ __attribute__((aligned(16))) uint4 As1[kBM * 16];
 
@@ -178,18 +207,22 @@ __global__ void __launch_bounds__(256, 2)
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int64_t n = tw * kTileRows + j * 32 + li;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int64_t m = m0 + i * 32 + 8 * (r / 4) + 4 * h + (r % 4);
-        if (m < M && n < N) {
-          if (gridDim.z > 1)
-            P[(blockIdx.z * M + m) * N + n] = acc[i][j][r];
-          else
-            Y[m * N + n] = __half_as_ushort(__float2half_rn(acc[i][j][r]));
-        }
-      }
+      store_block(acc[i][j], m0 + i * 32 + 4 * h, tw * kTileRows + j * 32 + li, M, N, P, out);
     }
+}
+__global__ void __launch_bounds__(256, 2)
+    k_gemm_pq2(const uint16_t* __restrict__ X, const uint8_t* __restrict__ packed,
+               const uint16_t* __restrict__ scales, int64_t M, int64_t N, int64_t K, int64_t C,
+               int64_t G,
+               int64_t NT, int64_t kmid, float* __restrict__ P, uint16_t* __restrict__ Y) {
+  gemm_pq2_body(X, packed, scales, M, N, K, C, G, NT, kmid, P, bgg::PlainOut{Y, N});
+}
+__global__ void __launch_bounds__(256, 2)
+    k_gemm_pq2_ep(const uint16_t* __restrict__ X, const uint8_t* __restrict__ packed,
+               const uint16_t* __restrict__ scales, int64_t M, int64_t N, int64_t K, int64_t C,
+               int64_t G,
+               int64_t NT, int64_t kmid, float* __restrict__ P, bgg::EpilogueOut out) {
+  gemm_pq2_body(X, packed, scales, M, N, K, C, G, NT, kmid, P, out);
 }
 
 // y = fp16(P[0] + P[1] + ... + P[S-1]) over M*N values (fp32 sums in that
@@ -225,6 +258,39 @@ __global__ void __launch_bounds__(256) k_gemm_sum(const float* __restrict__ P, i
   }
 }
 
+// The same sums through an epilogue, four consecutive values of a row per
+// thread.
+__global__ void __launch_bounds__(256) k_gemm_sum_ep(const float* __restrict__ P, int S, int64_t M, int64_t N,
+                                                     bgg::EpilogueOut out) {
+  const int64_t per = (N + 3) / 4, MN = M * N;
+  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (idx >= M * per) return;
+  const int64_t m = idx / per, n0 = 4 * (idx % per);
+  const float* src = P + m * N + n0;
+  float a[4];
+  bgg::EpilogueOut::Operands o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = out.load(m, n0 + i < N ? n0 + i : N - 1);
+  if ((N & 3) == 0) {  // (then every row and partial is aligned)
+    float4 v = *reinterpret_cast<const float4*>(src);
+    for (int z = 1; z < S; ++z) {
+      const float4 b = *reinterpret_cast<const float4*>(src + z * MN);
+      v.x += b.x, v.y += b.y, v.z += b.z, v.w += b.w;
+    }
+    a[0] = v.x, a[1] = v.y, a[2] = v.z, a[3] = v.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = n0 + i < N ? i : 0;
+      a[i] = src[k];
+      for (int z = 1; z < S; ++z) a[i] += src[z * MN + k];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n0 + i < N) out.store(m, n0 + i, a[i], o[i]);
+}
+
 // ---------------------------------------------------------------------------
 // PTQ1_0 (allhereai.com/news/1346, packing paragraph: the compact packing;
 // wmrh.cn/news/471187, section 关键机制: five trits per byte).  The same
@@ -240,11 +306,12 @@ __global__ void __launch_bounds__(256) k_gemm_sum(const float* __restrict__ P, i
 constexpr int kBK3 = 80;
 constexpr int kLdsStride3 = kBK3 + 8;  // halves per LDS row (176 bytes)
 
-__global__ void __launch_bounds__(256, 2)
-    k_gemm_ptq1(const uint16_t* __restrict__ X, const uint8_t* __restrict__ packed,
+template <class Out>
+__device__ __forceinline__ void gemm_ptq1_body(
+    const uint16_t* __restrict__ X, const uint8_t* __restrict__ packed,
                 const uint16_t* __restrict__ scales, int64_t M, int64_t N, int64_t K, int64_t C,
                 int64_t G,
-                int64_t NT, int64_t kmid, float* __restrict__ P, uint16_t* __restrict__ Y) {
+                int64_t NT, int64_t kmid, float* __restrict__ P, const Out& out) {
   __shared__ __attribute__((aligned(16))) uint16_t As[2][kBM * kLdsStride3];
   __shared__ uint32_t lut[256];
 
@@ -403,18 +470,22 @@ __global__ void __launch_bounds__(256, 2)
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int64_t n = tw * kTileRows + j * 32 + li;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int64_t m = m0 + i * 32 + 8 * (r / 4) + 4 * h + (r % 4);
-        if (m < M && n < N) {
-          if (gridDim.z > 1)
-            P[(blockIdx.z * M + m) * N + n] = acc[i][j][r];
-          else
-            Y[m * N + n] = __half_as_ushort(__float2half_rn(acc[i][j][r]));
-        }
-      }
+      store_block(acc[i][j], m0 + i * 32 + 4 * h, tw * kTileRows + j * 32 + li, M, N, P, out);
     }
+}
+__global__ void __launch_bounds__(256, 2)
+    k_gemm_ptq1(const uint16_t* __restrict__ X, const uint8_t* __restrict__ packed,
+                const uint16_t* __restrict__ scales, int64_t M, int64_t N, int64_t K, int64_t C,
+                int64_t G,
+                int64_t NT, int64_t kmid, float* __restrict__ P, uint16_t* __restrict__ Y) {
+  gemm_ptq1_body(X, packed, scales, M, N, K, C, G, NT, kmid, P, bgg::PlainOut{Y, N});
+}
+__global__ void __launch_bounds__(256, 2)
+    k_gemm_ptq1_ep(const uint16_t* __restrict__ X, const uint8_t* __restrict__ packed,
+                const uint16_t* __restrict__ scales, int64_t M, int64_t N, int64_t K, int64_t C,
+                int64_t G,
+                int64_t NT, int64_t kmid, float* __restrict__ P, bgg::EpilogueOut out) {
+  gemm_ptq1_body(X, packed, scales, M, N, K, C, G, NT, kmid, P, out);
 }
 
 // ---------------------------------------------------------------------------
@@ -556,33 +627,23 @@ GemmPlan gemm_plan(const bgg_weights_desc* d, int64_t M, bool rotate, uint64_t a
   return p;
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t bgg_gemm_workspace_size(const bgg_weights_desc* d, int64_t M) {
-  if (bgg::check_desc(d) != BGG_OK || M < 1) return 0;
-  const GemmPlan p = gemm_plan(d, M, true, UINT64_MAX);
-  return (size_t)(p.rot_bytes + p.rewrite_bytes + p.part_bytes);
-}
-
-bgg_status bgg_ternary_gemm(const bgg_weights_desc* d, const void* packed_dev, const void* x_dev,
-                            void* y_dev, int64_t M, uint32_t flags, void* workspace,
-                            size_t workspace_bytes, void* stream) {
+bgg_status ternary_gemm(const char* who, const bgg_weights_desc* d, const void* packed_dev, const void* x_dev,
+                        void* y_dev, int64_t M, uint32_t flags, const bgg::EpilogueOut* ep,
+                        void* workspace, size_t workspace_bytes, void* stream) {
   bgg_status st = bgg::check_desc(d);
   if (st) return st;
   if (d->format != BGG_FMT_PQ2_0 && d->format != BGG_FMT_PTQ1_0)
-    return fail(BGG_ERR_FORMAT, "bgg_ternary_gemm: only PQ2_0 and PTQ1_0 weights have a "
-                                "prompt-time kernel");
-  if (!packed_dev || !x_dev || !y_dev) return fail(BGG_ERR_NULL, "bgg_ternary_gemm: NULL buffer");
+    return fail(BGG_ERR_FORMAT, "%s: only PQ2_0 and PTQ1_0 weights have a "
+                                "prompt-time kernel", who);
+  if (!packed_dev || !x_dev || !y_dev) return fail(BGG_ERR_NULL, "%s: NULL buffer", who);
   if (M < 1 || M > (int64_t(1) << 31))
-    return fail(BGG_ERR_SHAPE, "bgg_ternary_gemm: M must be >= 1 (got %lld)", (long long)M);
+    return fail(BGG_ERR_SHAPE, "%s: M must be >= 1 (got %lld)", who, (long long)M);
   if (flags & ~(uint32_t)BGG_ROTATE_INPUT)
-    return fail(BGG_ERR_SHAPE, "bgg_ternary_gemm: unknown flags 0x%x", flags);
+    return fail(BGG_ERR_SHAPE, "%s: unknown flags 0x%x", who, flags);
   if (!aligned16(packed_dev) || !aligned16(x_dev) || ((uintptr_t)y_dev & 1))
-    return fail(BGG_ERR_BUFFER, "bgg_ternary_gemm: misaligned buffer");
+    return fail(BGG_ERR_BUFFER, "%s: misaligned buffer", who);
   if (workspace && !aligned16(workspace))
-    return fail(BGG_ERR_BUFFER, "bgg_ternary_gemm: misaligned workspace");
+    return fail(BGG_ERR_BUFFER, "%s: misaligned workspace", who);
   hipStream_t s = (hipStream_t)stream;
   const bool rotate = (flags & BGG_ROTATE_INPUT) != 0;
   const GemmPlan p = gemm_plan(d, M, rotate, workspace ? (uint64_t)workspace_bytes : 0);
@@ -590,8 +651,8 @@ bgg_status bgg_ternary_gemm(const bgg_weights_desc* d, const void* packed_dev, c
   const void* xr = x_dev;
   if (rotate) {
     if (!workspace || workspace_bytes < p.rot_bytes)
-      return fail(BGG_ERR_BUFFER, "bgg_ternary_gemm: rotation needs a 16-byte aligned workspace "
-                                  "of %llu bytes", (unsigned long long)p.rot_bytes);
+      return fail(BGG_ERR_BUFFER, "%s: rotation needs a 16-byte aligned workspace "
+                                  "of %llu bytes", who, (unsigned long long)p.rot_bytes);
     if ((st = bgg_hadamard_rotate(x_dev, workspace, M, d->K, stream))) return st;
     xr = workspace;
   }
@@ -617,18 +678,61 @@ bgg_status bgg_ternary_gemm(const bgg_weights_desc* d, const void* packed_dev, c
     const dim3 grid((unsigned)((d->N + kBN - 1) / kBN), (unsigned)((mc + kBM - 1) / kBM),
                     (unsigned)p.splits);
     uint16_t* y = (uint16_t*)y_dev + m0 * d->N;
-    hipLaunchKernelGGL(pq2 ? k_gemm_pq2 : k_gemm_ptq1, grid, dim3(256), 0, s,
-                       (const uint16_t*)xr + m0 * d->K, wts, scales, mc, d->N, d->K, C, d->groups,
-                       d->row_tiles, kmid, P, y);
-    if (P) {
+    bgg::EpilogueOut out;
+    if (ep) {
+      out = *ep;
+      out.y = y;
+      if (out.mul) out.mul += m0 * out.mul_stride;
+      if (out.residual) out.residual += m0 * out.residual_stride;
+      hipLaunchKernelGGL(pq2 ? k_gemm_pq2_ep : k_gemm_ptq1_ep, grid, dim3(256), 0, s,
+                         (const uint16_t*)xr + m0 * d->K, wts, scales, mc, d->N, d->K, C, d->groups,
+                         d->row_tiles, kmid, P, out);
+    } else {
+      hipLaunchKernelGGL(pq2 ? k_gemm_pq2 : k_gemm_ptq1, grid, dim3(256), 0, s,
+                         (const uint16_t*)xr + m0 * d->K, wts, scales, mc, d->N, d->K, C, d->groups,
+                         d->row_tiles, kmid, P, y);
+    }
+    if (P && ep) {
+      hipLaunchKernelGGL(k_gemm_sum_ep, dim3((unsigned)ceil_div(mc * ceil_div(d->N, 4), 256)), dim3(256), 0, s,
+                         (const float*)P, p.splits, mc, d->N, out);
+    } else if (P) {
       const int64_t mn = mc * d->N;
       hipLaunchKernelGGL(k_gemm_sum, dim3((unsigned)ceil_div(ceil_div(mn, 4), 256)), dim3(256), 0,
                          s, (const float*)P, p.splits, mn, y);
     }
   }
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return fail(BGG_ERR_HIP, "bgg_ternary_gemm: %s", hipGetErrorString(e));
+  if (e != hipSuccess) return fail(BGG_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
   return BGG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t bgg_gemm_workspace_size(const bgg_weights_desc* d, int64_t M) {
+  if (bgg::check_desc(d) != BGG_OK || M < 1) return 0;
+  const GemmPlan p = gemm_plan(d, M, true, UINT64_MAX);
+  return (size_t)(p.rot_bytes + p.rewrite_bytes + p.part_bytes);
+}
+
+bgg_status bgg_ternary_gemm(const bgg_weights_desc* d, const void* packed_dev, const void* x_dev,
+                            void* y_dev, int64_t M, uint32_t flags, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  return ternary_gemm("bgg_ternary_gemm", d, packed_dev, x_dev, y_dev, M, flags, nullptr, workspace,
+                      workspace_bytes, stream);
+}
+
+bgg_status bgg_ternary_gemm_epilogue(const bgg_weights_desc* d, const void* packed_dev,
+                                     const void* x_dev, void* y_dev, int64_t M, uint32_t flags,
+                                     const bgg_epilogue* ep, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  bgg_status st = bgg::check_desc(d);
+  if (st) return st;
+  bgg::EpilogueOut out;
+  if ((st = bgg::epilogue_out("bgg_ternary_gemm_epilogue", ep, y_dev, d->N, &out))) return st;
+  return ternary_gemm("bgg_ternary_gemm_epilogue", d, packed_dev, x_dev, y_dev, M, flags, &out, workspace,
+                      workspace_bytes, stream);
 }
 
 }  // extern "C"

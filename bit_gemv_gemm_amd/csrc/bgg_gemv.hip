@@ -306,11 +306,11 @@ constexpr int kMaxSumSlices = kMaxSlices;  // arrivals the row words count
 constexpr int64_t kSumRows = kRowWordRows;
 constexpr uint64_t kSumBytes = 2 * kRowWordBytes;  // fine and coarse words
 
-template <int M, int W>
+template <int M, int W, class Out>
 __device__ __forceinline__ void wg_finish(const float (&acc)[M], float (*red)[M][64], int wave,
                                           int lane, int64_t row, int64_t N, int Mreal, int Sg,
                                           int64_t local_row, unsigned long long* __restrict__ sums,
-                                          uint16_t* __restrict__ y) {
+                                          const Out& out) {
 #pragma unroll
   for (int m = 0; m < M; ++m) red[wave][m][lane] = acc[m];
   __syncthreads();
@@ -325,14 +325,14 @@ __device__ __forceinline__ void wg_finish(const float (&acc)[M], float (*red)[M]
   if (Sg == 1) {
 #pragma unroll
     for (int m = 0; m < M; ++m)
-      if (m < Mreal && row < N) y[(int64_t)m * N + row] = f2h(s[m]);
+      if (m < Mreal && row < N) out.store(m, row, s[m], out.load(m, row));
     return;
   }
   if (row >= N) return;
   const RowWords rw = row_words_of(sums);
 #pragma unroll
   for (int m = 0; m < M; ++m)
-    if (m < Mreal) add_partial(rw, m, local_row, Sg, s[m], y + (int64_t)m * N + row);
+    if (m < Mreal) add_partial(rw, m, local_row, Sg, s[m], out, row);
 }
 
 // ---------------------------------------------------------------------------
@@ -399,14 +399,13 @@ struct FuseArgs {
 // groups; workgroup = W consecutive K slices.  grid: NT * Sg workgroups of
 // 64*W threads.
 // ---------------------------------------------------------------------------
-template <int M, int BPS, int W>
-__global__ void __launch_bounds__(64 * W)
-    k_gemv_pq2(const uint8_t* __restrict__ packed, uint64_t scale_offset, int64_t C, int64_t G,
+template <int M, int BPS, int W, class Out>
+__device__ __forceinline__ void gemv_pq2_body(
+    const uint8_t* __restrict__ packed, uint64_t scale_offset, int64_t C, int64_t G,
                int64_t N, int Sg, int Mreal, const uint32_t* __restrict__ frag,
                int64_t frag_words_per_token, const int32_t* __restrict__ metaQ,
                const float* __restrict__ metaF, int64_t gpad, unsigned long long* __restrict__ sums,
-               int64_t tile0, int64_t ntl, int64_t nta, int sgb, int light_last,
-               uint16_t* __restrict__ y) {
+               int64_t tile0, int64_t ntl, int64_t nta, int sgb, int light_last, const Out& out) {
   __shared__ float red[W][M][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -488,7 +487,25 @@ __global__ void __launch_bounds__(64 * W)
     }
   }
   wg_finish<M, W>(acc, red, wave, lane, tile * kTile + lane, N, Mreal, ws.Sg,
-                  ws.local * kTile + lane, sums, y);
+                  ws.local * kTile + lane, sums, out);
+}
+template <int M, int BPS, int W>
+__global__ void __launch_bounds__(64 * W)
+    k_gemv_pq2(const uint8_t* __restrict__ packed, uint64_t scale_offset, int64_t C, int64_t G,
+               int64_t N, int Sg, int Mreal, const uint32_t* __restrict__ frag,
+               int64_t frag_words_per_token, const int32_t* __restrict__ metaQ,
+               const float* __restrict__ metaF, int64_t gpad, unsigned long long* __restrict__ sums,
+               int64_t tile0, int64_t ntl, int64_t nta, int sgb, int light_last, uint16_t* __restrict__ y) {
+  gemv_pq2_body<M, BPS, W>(packed, scale_offset, C, G, N, Sg, Mreal, frag, frag_words_per_token, metaQ, metaF, gpad, sums, tile0, ntl, nta, sgb, light_last, PlainOut{y, N});
+}
+template <int M, int BPS, int W>
+__global__ void __launch_bounds__(64 * W)
+    k_gemv_pq2_ep(const uint8_t* __restrict__ packed, uint64_t scale_offset, int64_t C, int64_t G,
+               int64_t N, int Sg, int Mreal, const uint32_t* __restrict__ frag,
+               int64_t frag_words_per_token, const int32_t* __restrict__ metaQ,
+               const float* __restrict__ metaF, int64_t gpad, unsigned long long* __restrict__ sums,
+               int64_t tile0, int64_t ntl, int64_t nta, int sgb, int light_last, EpilogueOut out) {
+  gemv_pq2_body<M, BPS, W>(packed, scale_offset, C, G, N, Sg, Mreal, frag, frag_words_per_token, metaQ, metaF, gpad, sums, tile0, ntl, nta, sgb, light_last, out);
 }
 
 // ---------------------------------------------------------------------------
@@ -605,14 +622,13 @@ __device__ __forceinline__ void ptq1_part(const uint4 (&w)[8 / H], const float (
   }
 }
 
-template <int M, int H, int W, bool FUSE>
-__global__ void __launch_bounds__(64 * W)
-    k_gemv_ptq1(const uint8_t* __restrict__ packed, uint64_t scale_offset, int64_t C, int64_t G,
+template <int M, int H, int W, bool FUSE, class Out>
+__device__ __forceinline__ void gemv_ptq1_body(
+    const uint8_t* __restrict__ packed, uint64_t scale_offset, int64_t C, int64_t G,
                 int64_t N, int Sg, int Mreal, const uint32_t* __restrict__ frag,
                 int64_t frag_words_per_token, const int32_t* __restrict__ metaQ,
                 const float* __restrict__ metaF, int64_t gpad, unsigned long long* __restrict__ sums,
-                int64_t tile0, int64_t ntl, int64_t nta, int sgb, int light_last, FuseArgs fa,
-                uint16_t* __restrict__ y) {
+                int64_t tile0, int64_t ntl, int64_t nta, int sgb, int light_last, FuseArgs fa, const Out& out) {
   constexpr int CH = kPeriodChunks / H;  // chunks per part
   static_assert(W * 64 >= 256, "the LUT build needs 256 threads");
   static_assert(!FUSE || M == 1, "the one-launch GEMV is for one token");
@@ -696,7 +712,25 @@ __global__ void __launch_bounds__(64 * W)
       ptq1_part<M, H, H - 1, kHoles>(w, sc, gf, fp, lbase, lane_off, acc);
   }
   wg_finish<M, W>(acc, red, wave, lane, tile * kTile + lane, N, Mreal, ws.Sg,
-                  ws.local * kTile + lane, sums, y);
+                  ws.local * kTile + lane, sums, out);
+}
+template <int M, int H, int W, bool FUSE>
+__global__ void __launch_bounds__(64 * W)
+    k_gemv_ptq1(const uint8_t* __restrict__ packed, uint64_t scale_offset, int64_t C, int64_t G,
+                int64_t N, int Sg, int Mreal, const uint32_t* __restrict__ frag,
+                int64_t frag_words_per_token, const int32_t* __restrict__ metaQ,
+                const float* __restrict__ metaF, int64_t gpad, unsigned long long* __restrict__ sums,
+                int64_t tile0, int64_t ntl, int64_t nta, int sgb, int light_last, FuseArgs fa, uint16_t* __restrict__ y) {
+  gemv_ptq1_body<M, H, W, FUSE>(packed, scale_offset, C, G, N, Sg, Mreal, frag, frag_words_per_token, metaQ, metaF, gpad, sums, tile0, ntl, nta, sgb, light_last, fa, PlainOut{y, N});
+}
+template <int M, int H, int W, bool FUSE>
+__global__ void __launch_bounds__(64 * W)
+    k_gemv_ptq1_ep(const uint8_t* __restrict__ packed, uint64_t scale_offset, int64_t C, int64_t G,
+                int64_t N, int Sg, int Mreal, const uint32_t* __restrict__ frag,
+                int64_t frag_words_per_token, const int32_t* __restrict__ metaQ,
+                const float* __restrict__ metaF, int64_t gpad, unsigned long long* __restrict__ sums,
+                int64_t tile0, int64_t ntl, int64_t nta, int sgb, int light_last, FuseArgs fa, EpilogueOut out) {
+  gemv_ptq1_body<M, H, W, FUSE>(packed, scale_offset, C, G, N, Sg, Mreal, frag, frag_words_per_token, metaQ, metaF, gpad, sums, tile0, ntl, nta, sgb, light_last, fa, out);
 }
 
 // ---------------------------------------------------------------------------
@@ -873,7 +907,7 @@ __device__ __forceinline__ void mx_group_g64(const i32x8 (&A)[kMxDigits], uint32
   }
 }
 
-template <int FMT, int BPS, int W>
+template <int FMT, int BPS, int W, class Out>
 __device__ __forceinline__ void mx_gemv_body(const uint8_t* __restrict__ packed,
                                              uint64_t scale_offset, int64_t C, int64_t G,
                                              int64_t N, int Sg, int Mreal,
@@ -883,7 +917,7 @@ __device__ __forceinline__ void mx_gemv_body(const uint8_t* __restrict__ packed,
                                              const float* __restrict__ xh,
                                              unsigned long long* __restrict__ sums, int64_t tile0,
                                              int64_t ntl, int64_t nta, int sgb, int light_last,
-                                             uint16_t* __restrict__ y) {
+                                             const Out& out) {
   constexpr bool kQ1 = FMT == BGG_FMT_Q1_0, kG64 = FMT == BGG_FMT_Q2_0_G64;
   __shared__ float red[W][kMmaSlots * kMmaRedStride];
   const int lane = threadIdx.x & 63;
@@ -1008,10 +1042,10 @@ __device__ __forceinline__ void mx_gemv_body(const uint8_t* __restrict__ packed,
     for (int q = 1; q < W; ++q) v += red[q][t * kMmaRedStride + r];
     const int64_t row = tile * kTile + r;
     if (ws.Sg == 1) {
-      if (row < N) y[(int64_t)t * N + row] = f2h(v);
+      if (row < N) out.store(t, row, v, out.load(t, row));
       continue;
     }
-    if (row < N) add_partial(row_words_of(sums), t, ws.local * kTile + r, ws.Sg, v, y + (int64_t)t * N + row);
+    if (row < N) add_partial(row_words_of(sums), t, ws.local * kTile + r, ws.Sg, v, out, row);
   }
 }
 
@@ -1020,22 +1054,23 @@ __device__ __forceinline__ void mx_gemv_body(const uint8_t* __restrict__ packed,
       int Sg, int Mreal, const uint4 *__restrict__ xa, const uint32_t *__restrict__ xs,        \
       const float *__restrict__ xc, const float *__restrict__ xh,                              \
       unsigned long long *__restrict__ sums, int64_t tile0, int64_t ntl, int64_t nta, int sgb, \
-      int light_last, uint16_t *__restrict__ y
+      int light_last
 #define BGG_MX_ARGS \
-  packed, scale_offset, C, G, N, Sg, Mreal, xa, xs, xc, xh, sums, tile0, ntl, nta, sgb, light_last, y
+  packed, scale_offset, C, G, N, Sg, Mreal, xa, xs, xc, xh, sums, tile0, ntl, nta, sgb, light_last
 // one kernel per format, so that a profiler names them apart
-template <int BPS, int W>
-__global__ void __launch_bounds__(64 * W) k_gemv_pq2_mx(BGG_MX_PARAMS) {
-  mx_gemv_body<BGG_FMT_PQ2_0, BPS, W>(BGG_MX_ARGS);
-}
-template <int BPS, int W>
-__global__ void __launch_bounds__(64 * W) k_gemv_q1_mx(BGG_MX_PARAMS) {
-  mx_gemv_body<BGG_FMT_Q1_0, BPS, W>(BGG_MX_ARGS);
-}
-template <int BPS, int W>
-__global__ void __launch_bounds__(64 * W) k_gemv_q2g64_mx(BGG_MX_PARAMS) {
-  mx_gemv_body<BGG_FMT_Q2_0_G64, BPS, W>(BGG_MX_ARGS);
-}
+#define BGG_MX_KERNELS(NAME, FMT)                                                            \
+  template <int BPS, int W>                                                                   \
+  __global__ void __launch_bounds__(64 * W) NAME(BGG_MX_PARAMS, uint16_t* __restrict__ y) {   \
+    mx_gemv_body<FMT, BPS, W>(BGG_MX_ARGS, PlainOut{y, N});                                   \
+  }                                                                                           \
+  template <int BPS, int W>                                                                   \
+  __global__ void __launch_bounds__(64 * W) NAME##_ep(BGG_MX_PARAMS, EpilogueOut out) {       \
+    mx_gemv_body<FMT, BPS, W>(BGG_MX_ARGS, out);                                              \
+  }
+BGG_MX_KERNELS(k_gemv_pq2_mx, BGG_FMT_PQ2_0)
+BGG_MX_KERNELS(k_gemv_q1_mx, BGG_FMT_Q1_0)
+BGG_MX_KERNELS(k_gemv_q2g64_mx, BGG_FMT_Q2_0_G64)
+#undef BGG_MX_KERNELS
 #undef BGG_MX_PARAMS
 #undef BGG_MX_ARGS
 
@@ -1054,13 +1089,13 @@ __global__ void __launch_bounds__(64 * W) k_gemv_q2g64_mx(BGG_MX_PARAMS) {
 // ---------------------------------------------------------------------------
 constexpr int kPtqCodeStride = 44;  // words per row in LDS: 40 + 4 against bank conflicts
 
-template <int W>
-__global__ void __launch_bounds__(64 * W)
-    k_gemv_ptq1_mx(const uint8_t* __restrict__ packed, uint64_t scale_offset, int64_t C, int64_t G,
+template <int W, class Out>
+__device__ __forceinline__ void gemv_ptq1_mx_body(
+    const uint8_t* __restrict__ packed, uint64_t scale_offset, int64_t C, int64_t G,
                    int64_t N, int Sg, int Mreal, const uint4* __restrict__ xa,
                    const uint32_t* __restrict__ xs, const float* __restrict__ xc,
                    unsigned long long* __restrict__ sums, int64_t tile0, int64_t ntl, int64_t nta,
-                   int sgb, int light_last, uint16_t* __restrict__ y) {
+                   int sgb, int light_last, const Out& out) {
   static_assert(W * 64 >= 256, "the LUT build needs 256 threads");
   static_assert(kMmaSlots * kMmaRedStride <= kTile * kPtqCodeStride, "red fits in a wave's codes");
   constexpr int PRE = 2;  // groups whose A operands are in flight
@@ -1195,11 +1230,29 @@ __global__ void __launch_bounds__(64 * W)
     for (int q = 1; q < W; ++q) v += red[q * kRedWave + t * kMmaRedStride + r];
     const int64_t row = tile * kTile + r;
     if (ws.Sg == 1) {
-      if (row < N) y[(int64_t)t * N + row] = f2h(v);
+      if (row < N) out.store(t, row, v, out.load(t, row));
       continue;
     }
-    if (row < N) add_partial(row_words_of(sums), t, ws.local * kTile + r, ws.Sg, v, y + (int64_t)t * N + row);
+    if (row < N) add_partial(row_words_of(sums), t, ws.local * kTile + r, ws.Sg, v, out, row);
   }
+}
+template <int W>
+__global__ void __launch_bounds__(64 * W)
+    k_gemv_ptq1_mx(const uint8_t* __restrict__ packed, uint64_t scale_offset, int64_t C, int64_t G,
+                   int64_t N, int Sg, int Mreal, const uint4* __restrict__ xa,
+                   const uint32_t* __restrict__ xs, const float* __restrict__ xc,
+                   unsigned long long* __restrict__ sums, int64_t tile0, int64_t ntl, int64_t nta,
+                   int sgb, int light_last, uint16_t* __restrict__ y) {
+  gemv_ptq1_mx_body<W>(packed, scale_offset, C, G, N, Sg, Mreal, xa, xs, xc, sums, tile0, ntl, nta, sgb, light_last, PlainOut{y, N});
+}
+template <int W>
+__global__ void __launch_bounds__(64 * W)
+    k_gemv_ptq1_mx_ep(const uint8_t* __restrict__ packed, uint64_t scale_offset, int64_t C, int64_t G,
+                   int64_t N, int Sg, int Mreal, const uint4* __restrict__ xa,
+                   const uint32_t* __restrict__ xs, const float* __restrict__ xc,
+                   unsigned long long* __restrict__ sums, int64_t tile0, int64_t ntl, int64_t nta,
+                   int sgb, int light_last, EpilogueOut out) {
+  gemv_ptq1_mx_body<W>(packed, scale_offset, C, G, N, Sg, Mreal, xa, xs, xc, sums, tile0, ntl, nta, sgb, light_last, out);
 }
 
 // Activations for the matrix-core kernels.  Per 128-group and token slot:
@@ -1455,7 +1508,7 @@ void launch_prep(const bgg_weights_desc* d, const GemvPlan& p, const uint16_t* x
 // fa.x; else it reads the preparation in the workspace.
 template <bool FUSE>
 void launch_gemv1(const bgg_weights_desc* d, const GemvPlan& p, const uint8_t* packed, uint16_t* y,
-                  uint8_t* ws, const FuseArgs& fa, hipStream_t st) {
+                  uint8_t* ws, const FuseArgs& fa, hipStream_t st, const EpilogueOut* ep) {
   const uint32_t* frag = reinterpret_cast<const uint32_t*>(ws + p.off_frag);
   const int32_t* mq = reinterpret_cast<const int32_t*>(ws + p.off_meta_q);
   const float* mf = reinterpret_cast<const float*>(ws + p.off_meta_f);
@@ -1477,10 +1530,16 @@ void launch_gemv1(const bgg_weights_desc* d, const GemvPlan& p, const uint8_t* p
     const dim3 grid((unsigned)(nta * Sg + (ntl - nta) * sgb));
     if constexpr (!FUSE) {
       if (d->format == BGG_FMT_PQ2_0) {
-#define BGG_PQ2(BPS)                                                                              \
-  hipLaunchKernelGGL((k_gemv_pq2<1, BPS, 8>), grid, block, 0, st, packed, d->scale_offset, d->chunks, \
-                     p.G, d->N, Sg, 1, frag, p.frag_words_per_token, mq, mf, p.gpad, sums, t0, ntl,  \
-                     nta, sgb, light, y)
+#define BGG_PQ2_ARGS                                                                             \
+  packed, d->scale_offset, d->chunks, p.G, d->N, Sg, 1, frag, p.frag_words_per_token, mq, mf, p.gpad, \
+      sums, t0, ntl, nta, sgb, light
+#define BGG_PQ2(BPS)                                                                                    \
+  do {                                                                                                  \
+    if (ep)                                                                                             \
+      hipLaunchKernelGGL((k_gemv_pq2_ep<1, BPS, 8>), grid, block, 0, st, BGG_PQ2_ARGS, *ep);            \
+    else                                                                                                \
+      hipLaunchKernelGGL((k_gemv_pq2<1, BPS, 8>), grid, block, 0, st, BGG_PQ2_ARGS, y);                 \
+  } while (0)
         switch (p.per_slice) {
           case 8: BGG_PQ2(8); break;
           case 5: BGG_PQ2(5); break;
@@ -1488,25 +1547,33 @@ void launch_gemv1(const bgg_weights_desc* d, const GemvPlan& p, const uint8_t* p
           default: BGG_PQ2(2); break;
         }
 #undef BGG_PQ2
+#undef BGG_PQ2_ARGS
         continue;
       }
     }
-#define BGG_PTQ1(H)                                                                                    \
-  hipLaunchKernelGGL((k_gemv_ptq1<1, H, 8, FUSE>), grid, block, 0, st, packed, d->scale_offset,    \
-                     d->chunks, p.G, d->N, Sg, 1, frag, p.frag_words_per_token, mq, mf, p.gpad, sums, \
-                     t0, ntl, nta, sgb, light, fa, y)
+#define BGG_PTQ1_ARGS                                                                            \
+  packed, d->scale_offset, d->chunks, p.G, d->N, Sg, 1, frag, p.frag_words_per_token, mq, mf, p.gpad, \
+      sums, t0, ntl, nta, sgb, light, fa
+#define BGG_PTQ1(H)                                                                                     \
+  do {                                                                                                  \
+    if (ep)                                                                                             \
+      hipLaunchKernelGGL((k_gemv_ptq1_ep<1, H, 8, FUSE>), grid, block, 0, st, BGG_PTQ1_ARGS, *ep);      \
+    else                                                                                                \
+      hipLaunchKernelGGL((k_gemv_ptq1<1, H, 8, FUSE>), grid, block, 0, st, BGG_PTQ1_ARGS, y);           \
+  } while (0)
     if (p.per_slice == 2)
       BGG_PTQ1(2);
     else
       BGG_PTQ1(1);
 #undef BGG_PTQ1
+#undef BGG_PTQ1_ARGS
   }
 }
 
 // The matrix-core GEMV for several tokens (one launch, or one per kSumRows
 // rows of split tiles); the plan's work split is the VALU kernels'.
 void launch_gemv_mma(const bgg_weights_desc* d, const GemvPlan& p, const uint8_t* packed,
-                     uint16_t* y, int Mreal, uint8_t* ws, hipStream_t st) {
+                     uint16_t* y, int Mreal, uint8_t* ws, hipStream_t st, const EpilogueOut* ep) {
   const uint4* xa = reinterpret_cast<const uint4*>(ws + p.off_frag);
   const uint32_t* xs = reinterpret_cast<const uint32_t*>(ws + p.off_meta_q);
   const float* xc = reinterpret_cast<const float*>(xs + p.G * kMmaSlots);
@@ -1522,14 +1589,25 @@ void launch_gemv_mma(const bgg_weights_desc* d, const GemvPlan& p, const uint8_t
     const int light = p.Sg > 1 && p.S % p.W != 0 ? 1 : 0;
     const dim3 grid((unsigned)(nta * Sg + (ntl - nta) * sgb));
     if (d->format == BGG_FMT_PTQ1_0) {
-      hipLaunchKernelGGL((k_gemv_ptq1_mx<8>), grid, block, 0, st, packed, d->scale_offset,
-                         d->chunks, p.G, d->N, Sg, Mreal, xa, xs, xc, sums, t0, ntl, nta, sgb,
-                         light, y);
+      if (ep)
+        hipLaunchKernelGGL((k_gemv_ptq1_mx_ep<8>), grid, block, 0, st, packed, d->scale_offset,
+                           d->chunks, p.G, d->N, Sg, Mreal, xa, xs, xc, sums, t0, ntl, nta, sgb,
+                           light, *ep);
+      else
+        hipLaunchKernelGGL((k_gemv_ptq1_mx<8>), grid, block, 0, st, packed, d->scale_offset,
+                           d->chunks, p.G, d->N, Sg, Mreal, xa, xs, xc, sums, t0, ntl, nta, sgb,
+                           light, y);
       continue;
     }
+#define BGG_MMA_ARGS                                                                           \
+  packed, d->scale_offset, d->chunks, p.G, d->N, Sg, Mreal, xa, xs, xc, xh, sums, t0, ntl, nta, sgb, light
 #define BGG_MMA_ONE(KERN, BPS)                                                                 \
-  hipLaunchKernelGGL((KERN<BPS, 8>), grid, block, 0, st, packed, d->scale_offset, d->chunks,    \
-                     p.G, d->N, Sg, Mreal, xa, xs, xc, xh, sums, t0, ntl, nta, sgb, light, y)
+  do {                                                                                          \
+    if (ep)                                                                                     \
+      hipLaunchKernelGGL((KERN##_ep<BPS, 8>), grid, block, 0, st, BGG_MMA_ARGS, *ep);           \
+    else                                                                                        \
+      hipLaunchKernelGGL((KERN<BPS, 8>), grid, block, 0, st, BGG_MMA_ARGS, y);                  \
+  } while (0)
 #define BGG_MMA(KERN)                          \
   switch (p.per_slice) {                       \
     case 8: BGG_MMA_ONE(KERN, 8); break;       \
@@ -1550,6 +1628,7 @@ void launch_gemv_mma(const bgg_weights_desc* d, const GemvPlan& p, const uint8_t
     }
 #undef BGG_MMA
 #undef BGG_MMA_ONE
+#undef BGG_MMA_ARGS
   }
 }
 
@@ -1569,6 +1648,71 @@ bgg_status gemv_args_check(const char* who, const bgg_weights_desc* d, int64_t M
     return fail(BGG_ERR_BUFFER, "%s: workspace has %zu bytes, needs %llu", who, workspace_bytes,
                 (unsigned long long)plan->total);
   return BGG_OK;
+}
+
+bgg_status gemv_run(const char* who, const bgg_weights_desc* d, const void* packed_dev, void* y_dev,
+                    int64_t M, const EpilogueOut* ep, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+  GemvPlan p;
+  bgg_status st = gemv_args_check(who, d, M, workspace, workspace_bytes, &p);
+  if (st) return st;
+  if (!packed_dev || !y_dev) return fail(BGG_ERR_NULL, "%s: NULL buffer", who);
+  if (!aligned16(packed_dev) || ((uintptr_t)y_dev & 1))
+    return fail(BGG_ERR_BUFFER, "%s: misaligned buffer", who);
+  hipStream_t s = (hipStream_t)stream;
+  const uint8_t* pk = (const uint8_t*)packed_dev;
+  uint8_t* ws = (uint8_t*)workspace;
+  uint16_t* y = (uint16_t*)y_dev;
+  if (p.mma) {
+    launch_gemv_mma(d, p, pk, y, (int)M, ws, s, ep);
+    return hip_check(who);
+  }
+  launch_gemv1<false>(d, p, pk, y, ws, FuseArgs{}, s, ep);  // (one token: the plan has no mma)
+  return hip_check(who);
+}
+
+bgg_status ternary_gemv(const char* who, const bgg_weights_desc* d, const void* packed_dev,
+                        const void* x_dev, void* y_dev, int64_t M, uint32_t flags,
+                        const EpilogueOut* ep, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  bgg_status st = check_desc(d);
+  if (st) return st;
+  if (!packed_dev || !y_dev) return fail(BGG_ERR_NULL, "%s: NULL buffer", who);
+  if (!aligned16(packed_dev) || ((uintptr_t)y_dev & 1))
+    return fail(BGG_ERR_BUFFER, "%s: misaligned buffer", who);
+  if (mxv_supported(d, M)) {
+    GemvPlan p;
+    st = gemv_args_check(who, d, M, workspace, workspace_bytes, &p);
+    if (st) return st;
+    if (!x_dev) return fail(BGG_ERR_NULL, "%s: NULL x", who);
+    if (!aligned16(x_dev)) return fail(BGG_ERR_BUFFER, "%s: misaligned x", who);
+    if (flags & ~(uint32_t)BGG_ROTATE_INPUT)
+      return fail(BGG_ERR_SHAPE, "%s: unknown flags 0x%x", who, flags);
+    return mxv_launch(d, packed_dev, x_dev, y_dev, M, (flags & BGG_ROTATE_INPUT) ? 1 : 0, workspace,
+                      (hipStream_t)stream, ep);
+  }
+  // one PTQ1_0 token runs in one launch; everything else not served above
+  // (several PTQ1_0 tokens, five and more PQ2_0 tokens, the sister formats,
+  // PQ2_0 K beyond the one-launch kernel's reach) in two steps
+  if (M != 1 || d->format != BGG_FMT_PTQ1_0) {
+    st = bgg_gemv_prepare(d, x_dev, M, flags, workspace, workspace_bytes, stream);
+    if (st) return st;
+    return gemv_run(who, d, packed_dev, y_dev, M, ep, workspace, workspace_bytes, stream);
+  }
+  // one token: a single launch that also encodes the activations
+  GemvPlan p;
+  st = gemv_args_check(who, d, M, workspace, workspace_bytes, &p);
+  if (st) return st;
+  if (!x_dev) return fail(BGG_ERR_NULL, "%s: NULL x", who);
+  if (!aligned16(x_dev)) return fail(BGG_ERR_BUFFER, "%s: misaligned x", who);
+  if (flags & ~(uint32_t)BGG_ROTATE_INPUT)
+    return fail(BGG_ERR_SHAPE, "%s: unknown flags 0x%x", who, flags);
+  FuseArgs fa;
+  fa.x = (const uint16_t*)x_dev;
+  fa.rotate = (flags & BGG_ROTATE_INPUT) ? 1 : 0;
+  launch_gemv1<true>(d, p, (const uint8_t*)packed_dev, (uint16_t*)y_dev, (uint8_t*)workspace, fa,
+                     (hipStream_t)stream, ep);
+  return hip_check(who);
 }
 
 }  // namespace
@@ -1637,65 +1781,36 @@ bgg_status bgg_gemv_prepare(const bgg_weights_desc* d, const void* x_dev, int64_
 
 bgg_status bgg_gemv_run(const bgg_weights_desc* d, const void* packed_dev, void* y_dev, int64_t M,
                         void* workspace, size_t workspace_bytes, void* stream) {
-  GemvPlan p;
-  bgg_status st = gemv_args_check("bgg_gemv_run", d, M, workspace, workspace_bytes, &p);
+  return gemv_run("bgg_gemv_run", d, packed_dev, y_dev, M, nullptr, workspace, workspace_bytes, stream);
+}
+
+bgg_status bgg_gemv_run_epilogue(const bgg_weights_desc* d, const void* packed_dev, void* y_dev,
+                                 int64_t M, const bgg_epilogue* ep, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  bgg_status st = check_desc(d);
   if (st) return st;
-  if (!packed_dev || !y_dev) return fail(BGG_ERR_NULL, "bgg_gemv_run: NULL buffer");
-  if (!aligned16(packed_dev) || ((uintptr_t)y_dev & 1))
-    return fail(BGG_ERR_BUFFER, "bgg_gemv_run: misaligned buffer");
-  hipStream_t s = (hipStream_t)stream;
-  const uint8_t* pk = (const uint8_t*)packed_dev;
-  uint8_t* ws = (uint8_t*)workspace;
-  uint16_t* y = (uint16_t*)y_dev;
-  if (p.mma) {
-    launch_gemv_mma(d, p, pk, y, (int)M, ws, s);
-    return hip_check("bgg_gemv_run");
-  }
-  launch_gemv1<false>(d, p, pk, y, ws, FuseArgs{}, s);  // (one token: the plan has no mma)
-  return hip_check("bgg_gemv_run");
+  EpilogueOut out;
+  if ((st = epilogue_out("bgg_gemv_run_epilogue", ep, y_dev, d->N, &out))) return st;
+  return gemv_run("bgg_gemv_run_epilogue", d, packed_dev, y_dev, M, &out, workspace, workspace_bytes, stream);
 }
 
 bgg_status bgg_ternary_gemv(const bgg_weights_desc* d, const void* packed_dev, const void* x_dev,
                             void* y_dev, int64_t M, uint32_t flags, void* workspace,
                             size_t workspace_bytes, void* stream) {
+  return ternary_gemv("bgg_ternary_gemv", d, packed_dev, x_dev, y_dev, M, flags, nullptr, workspace,
+                      workspace_bytes, stream);
+}
+
+bgg_status bgg_ternary_gemv_epilogue(const bgg_weights_desc* d, const void* packed_dev,
+                                     const void* x_dev, void* y_dev, int64_t M, uint32_t flags,
+                                     const bgg_epilogue* ep, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
   bgg_status st = check_desc(d);
   if (st) return st;
-  if (!packed_dev || !y_dev) return fail(BGG_ERR_NULL, "bgg_ternary_gemv: NULL buffer");
-  if (!aligned16(packed_dev) || ((uintptr_t)y_dev & 1))
-    return fail(BGG_ERR_BUFFER, "bgg_ternary_gemv: misaligned buffer");
-  if (mxv_supported(d, M)) {
-    GemvPlan p;
-    st = gemv_args_check("bgg_ternary_gemv", d, M, workspace, workspace_bytes, &p);
-    if (st) return st;
-    if (!x_dev) return fail(BGG_ERR_NULL, "bgg_ternary_gemv: NULL x");
-    if (!aligned16(x_dev)) return fail(BGG_ERR_BUFFER, "bgg_ternary_gemv: misaligned x");
-    if (flags & ~(uint32_t)BGG_ROTATE_INPUT)
-      return fail(BGG_ERR_SHAPE, "bgg_ternary_gemv: unknown flags 0x%x", flags);
-    return mxv_launch(d, packed_dev, x_dev, y_dev, M, (flags & BGG_ROTATE_INPUT) ? 1 : 0, workspace,
-                      (hipStream_t)stream);
-  }
-  // one PTQ1_0 token runs in one launch; everything else not served above
-  // (several PTQ1_0 tokens, five and more PQ2_0 tokens, the sister formats,
-  // PQ2_0 K beyond the one-launch kernel's reach) in two steps
-  if (M != 1 || d->format != BGG_FMT_PTQ1_0) {
-    st = bgg_gemv_prepare(d, x_dev, M, flags, workspace, workspace_bytes, stream);
-    if (st) return st;
-    return bgg_gemv_run(d, packed_dev, y_dev, M, workspace, workspace_bytes, stream);
-  }
-  // one token: a single launch that also encodes the activations
-  GemvPlan p;
-  st = gemv_args_check("bgg_ternary_gemv", d, M, workspace, workspace_bytes, &p);
-  if (st) return st;
-  if (!x_dev) return fail(BGG_ERR_NULL, "bgg_ternary_gemv: NULL x");
-  if (!aligned16(x_dev)) return fail(BGG_ERR_BUFFER, "bgg_ternary_gemv: misaligned x");
-  if (flags & ~(uint32_t)BGG_ROTATE_INPUT)
-    return fail(BGG_ERR_SHAPE, "bgg_ternary_gemv: unknown flags 0x%x", flags);
-  FuseArgs fa;
-  fa.x = (const uint16_t*)x_dev;
-  fa.rotate = (flags & BGG_ROTATE_INPUT) ? 1 : 0;
-  launch_gemv1<true>(d, p, (const uint8_t*)packed_dev, (uint16_t*)y_dev, (uint8_t*)workspace, fa,
-                     (hipStream_t)stream);
-  return hip_check("bgg_ternary_gemv");
+  EpilogueOut out;
+  if ((st = epilogue_out("bgg_ternary_gemv_epilogue", ep, y_dev, d->N, &out))) return st;
+  return ternary_gemv("bgg_ternary_gemv_epilogue", d, packed_dev, x_dev, y_dev, M, flags, &out, workspace,
+                      workspace_bytes, stream);
 }
 
 }  // extern "C"

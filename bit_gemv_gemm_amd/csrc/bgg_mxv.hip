@@ -107,13 +107,18 @@ struct MxvArgs {
 // The four row blocks' results of one lane (token m, rows 16 b + col of the
 // tile): stored directly (one slice), else through the row words (all four
 // arrivals issued before any is checked).
-__device__ __forceinline__ void store_rows(const MxvArgs& a, int m, int64_t ltile, int64_t tile, int col,
-                                           const float (&v)[kBlocks]) {
+template <class Out>
+__device__ __forceinline__ void store_rows(const MxvArgs& a, const Out& out, int m, int64_t ltile, int64_t tile,
+                                           int col, const float (&v)[kBlocks]) {
+  typename Out::Operands o[kBlocks];
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b)
+    if (tile * kTile + 16 * b + col < a.N) o[b] = out.load(m, tile * kTile + 16 * b + col);
   if (a.P == 1) {
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
       const int64_t row = tile * kTile + 16 * b + col;
-      if (row < a.N) a.y[(int64_t)m * a.N + row] = f2h(v[b]);
+      if (row < a.N) out.store(m, row, v[b], o[b]);
     }
     return;
   }
@@ -128,7 +133,7 @@ __device__ __forceinline__ void store_rows(const MxvArgs& a, int m, int64_t ltil
   for (int b = 0; b < kBlocks; ++b) {
     const int64_t row = tile * kTile + 16 * b + col;
     if (row < a.N)
-      finish_row(a.rw, m, ltile * kTile + 16 * b + col, a.P, old[b], term[b], a.y + (int64_t)m * a.N + row);
+      finish_row(a.rw, m, ltile * kTile + 16 * b + col, a.P, old[b], term[b], out, row, o[b]);
   }
 }
 
@@ -311,8 +316,8 @@ __device__ __forceinline__ int pq2_run_k0(int l16, int h) {
 // weight stream instead of waiting behind it (the vector memory path of a
 // CU serves requests in order, and a wave cannot run past a load it is
 // still trying to issue).
-template <int GSMAX>
-__global__ void __launch_bounds__(64 * kWaves) k_mxv_pq2(MxvArgs a) {
+template <int GSMAX, class Out>
+__device__ __forceinline__ void mxv_pq2_body(const MxvArgs& a, const Out& out) {
   static_assert(GSMAX <= kWaves, "one group per wave to encode");
   __shared__ __attribute__((aligned(16))) uint8_t sA[GSMAX][64 * 32];
   __shared__ uint8_t sSc[GSMAX][64];
@@ -447,7 +452,15 @@ __global__ void __launch_bounds__(64 * kWaves) k_mxv_pq2(MxvArgs a) {
   // 7. lane (token kg, rows 16 b + col)
 #pragma unroll
   for (int b = 0; b < kBlocks; ++b) pin(acc[b]);
-  if (live && kg < a.M) store_rows(a, kg, ltile, tile, col, acc);
+  if (live && kg < a.M) store_rows(a, out, kg, ltile, tile, col, acc);
+}
+template <int GSMAX>
+__global__ void __launch_bounds__(64 * kWaves) k_mxv_pq2(MxvArgs a) {
+  mxv_pq2_body<GSMAX>(a, PlainOut{a.y, a.N});
+}
+template <int GSMAX>
+__global__ void __launch_bounds__(64 * kWaves) k_mxv_pq2_ep(MxvArgs a, EpilogueOut out) {
+  mxv_pq2_body<GSMAX>(a, out);
 }
 
 // ---------------------------------------------------------------------------
@@ -460,8 +473,8 @@ __global__ void __launch_bounds__(64 * kWaves) k_mxv_pq2(MxvArgs a) {
 // fixed-order reduction in LDS.  With one K range per row range there is no
 // row word at all; else the ranges are added through the row words.
 // ---------------------------------------------------------------------------
-template <int GPW, int TPW>
-__global__ void __launch_bounds__(64 * kWaves) k_mxv1_pq2(MxvArgs a) {
+template <int GPW, int TPW, class Out>
+__device__ __forceinline__ void mxv1_pq2_body(const MxvArgs& a, const Out& out) {
   constexpr int kPasses = (GPW + 3) / 4;
   constexpr int kRows = TPW * kTile;
   // digit rows 0-2 of each group's A operand: [digit][lane group][32 bytes]
@@ -651,14 +664,23 @@ __global__ void __launch_bounds__(64 * kWaves) k_mxv1_pq2(MxvArgs a) {
     const int64_t lrow = lt * kTile + r % kTile;
     const int64_t row = a.tile0 * kTile + lrow;
     if (row >= a.N) continue;
+    const typename Out::Operands o = out.load(0, row);
     if (a.P == 1) {
-      a.y[row] = f2h(v);
+      out.store(0, row, v, o);
     } else {
       const uint64_t term = partial_term(a.rw, 0, lrow, v);
       const uint64_t old = arrive(a.rw, 0, lrow, term);
-      finish_row(a.rw, 0, lrow, a.P, old, term, a.y + row);
+      finish_row(a.rw, 0, lrow, a.P, old, term, out, row, o);
     }
   }
+}
+template <int GPW, int TPW>
+__global__ void __launch_bounds__(64 * kWaves) k_mxv1_pq2(MxvArgs a) {
+  mxv1_pq2_body<GPW, TPW>(a, PlainOut{a.y, a.N});
+}
+template <int GPW, int TPW>
+__global__ void __launch_bounds__(64 * kWaves) k_mxv1_pq2_ep(MxvArgs a, EpilogueOut out) {
+  mxv1_pq2_body<GPW, TPW>(a, out);
 }
 
 // ---------------------------------------------------------------------------
@@ -716,8 +738,8 @@ __device__ __forceinline__ uint32_t tok_addr(int m, int row) {
   return (uint32_t)(96 * m + row) * kLutRowBytes + 128u;
 }
 
-template <int NW, int MT>
-__global__ void __launch_bounds__(64 * NW) k_mxv_ptq1(MxvArgs a) {
+template <int NW, int MT, class Out>
+__device__ __forceinline__ void mxv_ptq1_body(const MxvArgs& a, const Out& out) {
   static_assert(NW >= 2 && NW <= 16, "2 to 16 waves");
   static_assert(MT >= 1 && MT <= kPtqMaxTokens, "one or two tokens");
   constexpr int kEnc = kPeriodGroups * MT;             // blocks to encode
@@ -973,12 +995,15 @@ __global__ void __launch_bounds__(64 * NW) k_mxv_ptq1(MxvArgs a) {
   const int64_t lrow = lt * kTile + 16 * kg + col;
   const int64_t row = a.tile0 * kTile + lrow;
   if (lt >= a.NTl || row >= a.N) return;
+  typename Out::Operands o[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) o[m] = out.load(m, row);
   float v[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) v[m] = kg == 0 ? acc[m][0] : kg == 1 ? acc[m][1] : kg == 2 ? acc[m][2] : acc[m][3];
   if (a.P == 1) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) a.y[(int64_t)m * a.N + row] = f2h(v[m]);
+    for (int m = 0; m < MT; ++m) out.store(m, row, v[m], o[m]);
     return;
   }
   uint64_t term[MT], old[MT];
@@ -987,7 +1012,15 @@ __global__ void __launch_bounds__(64 * NW) k_mxv_ptq1(MxvArgs a) {
 #pragma unroll
   for (int m = 0; m < MT; ++m) old[m] = arrive(a.rw, m, lrow, term[m]);
 #pragma unroll
-  for (int m = 0; m < MT; ++m) finish_row(a.rw, m, lrow, a.P, old[m], term[m], a.y + (int64_t)m * a.N + row);
+  for (int m = 0; m < MT; ++m) finish_row(a.rw, m, lrow, a.P, old[m], term[m], out, row, o[m]);
+}
+template <int NW, int MT>
+__global__ void __launch_bounds__(64 * NW) k_mxv_ptq1(MxvArgs a) {
+  mxv_ptq1_body<NW, MT>(a, PlainOut{a.y, a.N});
+}
+template <int NW, int MT>
+__global__ void __launch_bounds__(64 * NW) k_mxv_ptq1_ep(MxvArgs a, EpilogueOut out) {
+  mxv_ptq1_body<NW, MT>(a, out);
 }
 
 // ---------------------------------------------------------------------------
@@ -1043,22 +1076,30 @@ PtqPlan ptq1_plan(const bgg_weights_desc* d, int64_t M) {
   return PtqPlan{std::max(tw, kPtqMinWaves[M]), tw};
 }
 
+// KERN<...>, or with an epilogue KERN_ep<...>
+#define BGG_MXV_LAUNCH(KERN, ...)                                                    \
+  do {                                                                               \
+    if (ep)                                                                          \
+      hipLaunchKernelGGL((KERN##_ep<__VA_ARGS__>), grid, block, 0, st, a, *ep);      \
+    else                                                                             \
+      hipLaunchKernelGGL((KERN<__VA_ARGS__>), grid, block, 0, st, a);                \
+  } while (0)
 template <int NW>
-void launch_ptq1(int M, dim3 grid, hipStream_t st, const MxvArgs& a) {
+void launch_ptq1(int M, dim3 grid, hipStream_t st, const MxvArgs& a, const EpilogueOut* ep) {
   const dim3 block(64 * NW);
   if (M == 1) {
-    if constexpr (NW >= kPtqMinWaves[1]) hipLaunchKernelGGL((k_mxv_ptq1<NW, 1>), grid, block, 0, st, a);
+    if constexpr (NW >= kPtqMinWaves[1]) BGG_MXV_LAUNCH(k_mxv_ptq1, NW, 1);
   } else {
-    if constexpr (NW <= kPtqMaxWaves[2]) hipLaunchKernelGGL((k_mxv_ptq1<NW, 2>), grid, block, 0, st, a);
+    if constexpr (NW <= kPtqMaxWaves[2]) BGG_MXV_LAUNCH(k_mxv_ptq1, NW, 2);
   }
 }
 template <int NW>
-void launch_ptq1_nw(int nw, int M, dim3 grid, hipStream_t st, const MxvArgs& a) {
+void launch_ptq1_nw(int nw, int M, dim3 grid, hipStream_t st, const MxvArgs& a, const EpilogueOut* ep) {
   if constexpr (NW <= 16) {
     if (nw == NW)
-      launch_ptq1<NW>(M, grid, st, a);
+      launch_ptq1<NW>(M, grid, st, a, ep);
     else
-      launch_ptq1_nw<NW + 1>(nw, M, grid, st, a);
+      launch_ptq1_nw<NW + 1>(nw, M, grid, st, a, ep);
   }
 }
 
@@ -1082,7 +1123,7 @@ int mxv_kernel_name(const bgg_weights_desc* d, int64_t M, char* out, size_t cap)
 }
 
 bgg_status mxv_launch(const bgg_weights_desc* d, const void* packed, const void* x, void* y,
-                      int64_t M, int rotate, void* workspace, hipStream_t st) {
+                      int64_t M, int rotate, void* workspace, hipStream_t st, const EpilogueOut* ep) {
   MxvArgs a{};
   a.packed = (const uint8_t*)packed;
   a.scale_offset = d->scale_offset;
@@ -1113,7 +1154,7 @@ bgg_status mxv_launch(const bgg_weights_desc* d, const void* packed, const void*
       a.tile0 = r0 * a.TW;
       a.NTl = std::min<int64_t>(a.RR * a.TW, NT - a.tile0);
       const dim3 grid((unsigned)(a.RR * a.P));
-      launch_ptq1_nw<kPtqMinWaves[2]>(nw, (int)M, grid, st, a);
+      launch_ptq1_nw<kPtqMinWaves[2]>(nw, (int)M, grid, st, a, ep);
     }
     return hip_check("bgg_ternary_gemv");
   }
@@ -1135,9 +1176,9 @@ bgg_status mxv_launch(const bgg_weights_desc* d, const void* packed, const void*
       a.NTl = std::min<int64_t>(a.RR * tpw, NT - a.tile0);
       const dim3 grid((unsigned)(a.RR * a.P)), block(64 * kWaves);
       if (tpw == 2)
-        hipLaunchKernelGGL((k_mxv1_pq2<kGpw, 2>), grid, block, 0, st, a);
+        BGG_MXV_LAUNCH(k_mxv1_pq2, kGpw, 2);
       else
-        hipLaunchKernelGGL((k_mxv1_pq2<kGpw, 1>), grid, block, 0, st, a);
+        BGG_MXV_LAUNCH(k_mxv1_pq2, kGpw, 1);
     }
     return hip_check("bgg_ternary_gemv");
   }
@@ -1156,7 +1197,7 @@ bgg_status mxv_launch(const bgg_weights_desc* d, const void* packed, const void*
     a.tile0 = r0 * kWaves;
     a.NTl = std::min<int64_t>(a.RR * kWaves, NT - a.tile0);
     const dim3 grid((unsigned)(a.RR * a.P)), block(64 * kWaves);
-    hipLaunchKernelGGL((k_mxv_pq2<kPqGsMax>), grid, block, 0, st, a);
+    BGG_MXV_LAUNCH(k_mxv_pq2, kPqGsMax);
   }
   return hip_check("bgg_ternary_gemv");
 }

@@ -6,7 +6,7 @@
 // Every GEMV workspace starts with these words (fine words, then coarse
 // words, 8 MiB each); every launch leaves the words it used at zero.
 #pragma once
-#include "bgg_device.h"
+#include "bgg_epilogue.h"
 
 namespace bgg {
 
@@ -71,10 +71,12 @@ __device__ __forceinline__ uint64_t arrive(const RowWords& rw, int m, int64_t lr
   return __hip_atomic_fetch_add(rw.fine + (int64_t)m * kRowWordRows + lr, term, __ATOMIC_RELAXED,
                                 __HIP_MEMORY_SCOPE_AGENT);
 }
-// Phase 2: the arrival that saw P - 1 before it holds the whole row: store y
-// and clear the words.
+// Phase 2: the arrival that saw P - 1 before it holds the whole row: store
+// y[m][row] (operands o) and clear the words.
+template <class Out>
 __device__ __forceinline__ void finish_row(const RowWords& rw, int m, int64_t lr, int P, uint64_t old,
-                                           uint64_t term, uint16_t* __restrict__ yrow) {
+                                           uint64_t term, const Out& out, int64_t row,
+                                           const typename Out::Operands& o) {
   if ((int)(old >> kArriveShift) != P - 1) return;
   const uint64_t tot = old + term;
   float y;
@@ -90,18 +92,20 @@ __device__ __forceinline__ void finish_row(const RowWords& rw, int m, int64_t lr
     }
     y = (float)v;
   }
-  *yrow = f2h(y);
+  out.store(m, row, y, o);
   __hip_atomic_store(rw.fine + (int64_t)m * kRowWordRows + lr, 0ull, __ATOMIC_RELAXED,
                      __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // Partial p of (token slot m, local row lr) of a row cut into P slices, in
-// one go: add it; the arrival that completes the row stores y at *yrow.
+// one go: add it; the arrival that completes the row stores y[m][row].
+template <class Out>
 __device__ __forceinline__ void add_partial(const RowWords& rw, int m, int64_t lr, int P, float p,
-                                            uint16_t* __restrict__ yrow) {
+                                            const Out& out, int64_t row) {
   const uint64_t term = partial_term(rw, m, lr, p);
+  const typename Out::Operands o = out.load(m, row);
   const uint64_t old = arrive(rw, m, lr, term);
-  finish_row(rw, m, lr, P, old, term, yrow);
+  finish_row(rw, m, lr, P, old, term, out, row, o);
 }
 
 }  // namespace bgg

@@ -299,6 +299,52 @@ bgg_status bgg_gemv_prepare(const bgg_weights_desc* desc, const void* x_dev, int
 bgg_status bgg_gemv_run(const bgg_weights_desc* desc, const void* packed_dev, void* y_dev,
                         int64_t M, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Activations of an epilogue (no page passage): NONE v, RELU max(v, 0),
+ * RELU2 max(v, 0)^2, SILU v / (1 + e^-v), GELU v (1 + erf(v / sqrt 2)) / 2,
+ * GELU_TANH v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2. */
+typedef enum {
+  BGG_ACT_NONE = 0,
+  BGG_ACT_RELU = 1,
+  BGG_ACT_RELU2 = 2,
+  BGG_ACT_SILU = 3,
+  BGG_ACT_GELU = 4,
+  BGG_ACT_GELU_TANH = 5
+} bgg_activation;
+
+/* What becomes of a product before it is rounded:
+ *     y[m][n] = act(sum + bias[n]) * mul[m][n] + residual[m][n]
+ * in fp32, with one rounding to fp16.  Each pointer may be NULL (its step is
+ * left out).  Device fp16, 2-byte aligned; rows of mul and residual start
+ * every mul_stride or residual_stride values (at least N).  mul and residual
+ * may be the same buffer, and either may be y itself (its stride N then);
+ * they may not overlap y in any other way.  (The gated product of a decoder
+ * layer is act = SILU on the gate matrix with mul = the up projection; a
+ * layer's residual stream is residual = y = the stream.) */
+typedef struct bgg_epilogue {
+  int32_t activation; /* bgg_activation */
+  int32_t reserved;   /* 0 */
+  const void* bias_dev;
+  const void* mul_dev;
+  const void* residual_dev;
+  int64_t mul_stride; /* 0 without mul */
+  int64_t residual_stride; /* 0 without residual */
+} bgg_epilogue;
+
+/* bgg_ternary_gemv and bgg_gemv_run with an epilogue (no page passage): the
+ * same kernels and sums, the epilogue applied where a row's sum is complete,
+ * so y is written once and no other launch reads it.  A NaN or inf in a
+ * token's x makes its sums NaN, and the epilogue passes NaN on (RELU too).
+ * Other arguments and errors as without; BGG_ERR_NULL without epilogue,
+ * BGG_ERR_FORMAT (activation), BGG_ERR_SHAPE (strides, reserved),
+ * BGG_ERR_BUFFER (alignment). */
+bgg_status bgg_ternary_gemv_epilogue(const bgg_weights_desc* desc, const void* packed_dev,
+                                     const void* x_dev, void* y_dev, int64_t M, uint32_t flags,
+                                     const bgg_epilogue* epilogue, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+bgg_status bgg_gemv_run_epilogue(const bgg_weights_desc* desc, const void* packed_dev, void* y_dev,
+                                 int64_t M, const bgg_epilogue* epilogue, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
 /* The name under which a profiler lists the GEMV kernel that
  * bgg_ternary_gemv launches for M tokens (host only, bookkeeping of this
  * interface, no page passage; for matching profiles to calls): PQ2_0 with
@@ -343,6 +389,14 @@ size_t bgg_gemm_workspace_size(const bgg_weights_desc* desc, int64_t M);
 bgg_status bgg_ternary_gemm(const bgg_weights_desc* desc, const void* packed_dev,
                             const void* x_dev, void* y_dev, int64_t M, uint32_t flags,
                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* bgg_ternary_gemm with an epilogue (no page passage): as above, applied to
+ * the fp32 sums of the product kernel, or of the kernel that adds the
+ * partial sums where K is split. */
+bgg_status bgg_ternary_gemm_epilogue(const bgg_weights_desc* desc, const void* packed_dev,
+                                     const void* x_dev, void* y_dev, int64_t M, uint32_t flags,
+                                     const bgg_epilogue* epilogue, void* workspace,
+                                     size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * The rest of a decoder layer's attention: rotary positions with the append
