@@ -26,6 +26,9 @@ bgg_status epilogue_out(const char* who, const bgg_epilogue* ep, void* y, int64_
   out->mul_stride = ep->mul_stride;
   out->residual_stride = ep->residual_stride;
   out->act = ep->activation;
+  // (a missing operand has address and stride 0)
+  out->wide = N % 8 == 0 && ep->mul_stride % 8 == 0 && ep->residual_stride % 8 == 0 &&
+              (((uintptr_t)y | (uintptr_t)ep->bias_dev | (uintptr_t)ep->mul_dev | (uintptr_t)ep->residual_dev) & 15) == 0;
   return BGG_OK;
 }
 

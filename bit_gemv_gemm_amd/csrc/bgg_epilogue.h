@@ -18,6 +18,20 @@ struct PlainOut {
   }
 };
 
+// act(v).  1 / (1 + e) by the reciprocal instruction (one unit of fp32);
+// 1 + erf(u) = erfc(-u) and (1 + tanh(u)) / 2 = 1 / (1 + e^(-2 u)), which do
+// not cancel on the negative side.
+template <int ACT>
+__device__ __forceinline__ float activate(float v) {
+  if (ACT == BGG_ACT_RELU) return v < 0.0f ? 0.0f : v;  // (a NaN stays)
+  if (ACT == BGG_ACT_RELU2) return v < 0.0f ? 0.0f : v * v;
+  if (ACT == BGG_ACT_SILU) return v * __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+  if (ACT == BGG_ACT_GELU) return 0.5f * v * erfcf(v * -0.7071067811865475f);
+  if (ACT == BGG_ACT_GELU_TANH)
+    return v * __builtin_amdgcn_rcpf(1.0f + __expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
+  return v;
+}
+
 // The epilogue's operands of one value are loaded where its sum is about to
 // arrive (load), so that their latency passes beside the last atomics or
 // matrix operations, and applied when it has (store).  y may be mul or
@@ -30,6 +44,7 @@ struct EpilogueOut {
   const uint16_t *bias, *mul, *residual;
   int64_t mul_stride, residual_stride;
   int act;
+  int wide;  // every row of y and of the operands starts on 16 bytes, N % 8 == 0
   struct Operands {
     uint16_t bias, mul, residual;
   };
@@ -43,15 +58,11 @@ struct EpilogueOut {
   __device__ __forceinline__ float value(float v, const Operands& o) const {
     if (bias) v += h2f(o.bias);
     switch (act) {
-      case BGG_ACT_RELU: v = v < 0.0f ? 0.0f : v; break;  // (a NaN stays)
-      case BGG_ACT_RELU2: v = v < 0.0f ? 0.0f : v * v; break;
-      case BGG_ACT_SILU: v = v / (1.0f + __expf(-v)); break;
-      // (1 + erf(u) = erfc(-u) and (1 + tanh(u)) / 2 = 1 / (1 + e^(-2 u)),
-      // which do not cancel on the negative side)
-      case BGG_ACT_GELU: v = 0.5f * v * erfcf(v * -0.7071067811865475f); break;
-      case BGG_ACT_GELU_TANH:
-        v = v / (1.0f + __expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
-        break;
+      case BGG_ACT_RELU: v = activate<BGG_ACT_RELU>(v); break;
+      case BGG_ACT_RELU2: v = activate<BGG_ACT_RELU2>(v); break;
+      case BGG_ACT_SILU: v = activate<BGG_ACT_SILU>(v); break;
+      case BGG_ACT_GELU: v = activate<BGG_ACT_GELU>(v); break;
+      case BGG_ACT_GELU_TANH: v = activate<BGG_ACT_GELU_TANH>(v); break;
       default: break;
     }
     if (mul) v *= h2f(o.mul);

@@ -29,6 +29,7 @@
 
 #include <cmath>
 #include <cstdlib>
+#include <type_traits>
 
 #include "bgg_epilogue.h"
 
@@ -90,6 +91,98 @@ __device__ __forceinline__ void store_block(const f32x16& acc, int64_t m0, int64
   for (int r = 0; r < 16; ++r) {
     const int64_t m = m0 + 8 * (r / 4) + (r % 4);
     if (m < M) out.store(m, n, acc[r], o[r]);
+  }
+}
+
+// Eight values of a row, at.., through an epilogue: 16-byte loads and one
+// 16-byte store.
+struct Eight {
+  uint4 mul, residual;
+};
+__device__ __forceinline__ Eight load_eight(const bgg::EpilogueOut& out, int64_t m, int64_t n) {
+  Eight e{};
+  if (out.mul) e.mul = *reinterpret_cast<const uint4*>(out.mul + m * out.mul_stride + n);
+  if (out.residual) e.residual = *reinterpret_cast<const uint4*>(out.residual + m * out.residual_stride + n);
+  return e;
+}
+template <int ACT>
+__device__ __forceinline__ void store_eight(const bgg::EpilogueOut& out, int64_t m, int64_t n, float (&v)[8],
+                                            const float (&bias)[8], const Eight& e) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = bgg::activate<ACT>(v[i] + bias[i]);
+  if (out.mul) {
+    bgg::unpack8h(e.mul, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= x[i];
+  }
+  if (out.residual) {
+    bgg::unpack8h(e.residual, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += x[i];
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = (uint32_t)bgg::f2h(v[2 * i]) | ((uint32_t)bgg::f2h(v[2 * i + 1]) << 16);
+  *reinterpret_cast<uint4*>(out.y + m * out.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+// f(integral constant) for the epilogue's activation
+template <class F>
+__device__ __forceinline__ void with_activation(int act, F f) {
+  switch (act) {
+    case BGG_ACT_RELU: f(std::integral_constant<int, BGG_ACT_RELU>()); break;
+    case BGG_ACT_RELU2: f(std::integral_constant<int, BGG_ACT_RELU2>()); break;
+    case BGG_ACT_SILU: f(std::integral_constant<int, BGG_ACT_SILU>()); break;
+    case BGG_ACT_GELU: f(std::integral_constant<int, BGG_ACT_GELU>()); break;
+    case BGG_ACT_GELU_TANH: f(std::integral_constant<int, BGG_ACT_GELU_TANH>()); break;
+    default: f(std::integral_constant<int, BGG_ACT_NONE>()); break;
+  }
+}
+
+// The wave's 128 x 64 sums through an epilogue with wide rows: 32 rows at a
+// time through the wave's 8 KiB of the (now idle) activation buffer, so that
+// a lane has eight consecutive values of a row and the operands and y move
+// 16 bytes at a time, the operands of the next eight rows in flight.  (With
+// a value per load and store, two bytes each, 4096 x 17408 x 5120 with SILU
+// and a multiplier took 806 us, against 619 us for the product alone.)
+// Columns 32 .. 63 of the rows with bit 2 set change places with 0 .. 31,
+// so that the two half-waves of a store hit different banks.
+__device__ __forceinline__ void wide_epilogue(const f32x16 (&acc)[4][2], float* lds, int lane, int64_t m0,
+                                              int64_t n0, int64_t M, const bgg::EpilogueOut& out) {
+  const int li = lane & 31, h = lane >> 5, row0 = lane >> 3, c8 = 8 * (lane & 7);
+  const int64_t n = n0 + c8;
+  const bool col_ok = n < out.N;
+  float bias[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bias[i] = 0.0f;
+  if (out.bias && col_ok) bgg::load8h(out.bias + n, bias);
+  auto operands = [&](int row) {
+    return col_ok && m0 + row < M ? load_eight(out, m0 + row, n) : Eight{};
+  };
+  Eight e = operands(row0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int row = 8 * (r / 4) + 4 * h + (r % 4);
+        lds[row * 64 + ((j * 32 + li) ^ (32 * h))] = acc[i][j][r];
+      }
+    bgg::wave_lds_sync();
+    with_activation(out.act, [&](auto act) {
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        const int row = 8 * q + row0;
+        const Eight next = operands(32 * i + row + 8);
+        const float* src = lds + row * 64 + (c8 ^ (32 * ((row >> 2) & 1)));
+        const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
+        float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if (col_ok && m0 + 32 * i + row < M) store_eight<act.value>(out, m0 + 32 * i + row, n, v, bias, e);
+        e = next;
+      }
+    });
+    bgg::wave_lds_sync();
   }
 }
 
@@ -203,6 +296,12 @@ __device__ __forceinline__ void gemm_pq2_body(
 #undef BGG_STEP
 
   if (!w_ok) return;
+  if constexpr (std::is_same<Out, bgg::EpilogueOut>::value) {
+    if (out.wide && gridDim.z == 1) {  // (every wave is past its last read of As0: the steps' barrier)
+      wide_epilogue(acc, reinterpret_cast<float*>(As0) + wave * 2048, lane, m0, tw * kTileRows, M, out);
+      return;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -258,37 +357,33 @@ __global__ void __launch_bounds__(256) k_gemm_sum(const float* __restrict__ P, i
   }
 }
 
-// The same sums through an epilogue, four consecutive values of a row per
-// thread.
+// The same sums through an epilogue: eight consecutive values of a row per
+// thread where the rows are wide, else one.
 __global__ void __launch_bounds__(256) k_gemm_sum_ep(const float* __restrict__ P, int S, int64_t M, int64_t N,
                                                      bgg::EpilogueOut out) {
-  const int64_t per = (N + 3) / 4, MN = M * N;
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (idx >= M * per) return;
-  const int64_t m = idx / per, n0 = 4 * (idx % per);
-  const float* src = P + m * N + n0;
-  float a[4];
-  bgg::EpilogueOut::Operands o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = out.load(m, n0 + i < N ? n0 + i : N - 1);
-  if ((N & 3) == 0) {  // (then every row and partial is aligned)
-    float4 v = *reinterpret_cast<const float4*>(src);
-    for (int z = 1; z < S; ++z) {
-      const float4 b = *reinterpret_cast<const float4*>(src + z * MN);
-      v.x += b.x, v.y += b.y, v.z += b.z, v.w += b.w;
-    }
-    a[0] = v.x, a[1] = v.y, a[2] = v.z, a[3] = v.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = n0 + i < N ? i : 0;
-      a[i] = src[k];
-      for (int z = 1; z < S; ++z) a[i] += src[z * MN + k];
-    }
+  const int64_t MN = M * N, idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (!out.wide) {
+    if (idx >= MN) return;
+    const int64_t m = idx / N, n = idx % N;
+    const bgg::EpilogueOut::Operands o = out.load(m, n);
+    float a = P[idx];
+    for (int z = 1; z < S; ++z) a += P[z * MN + idx];
+    out.store(m, n, a, o);
+    return;
   }
+  if (8 * idx >= MN) return;
+  const int64_t m = 8 * idx / N, n = 8 * idx % N;  // (N % 8 == 0: one row)
+  const Eight e = load_eight(out, m, n);
+  float bias[8], v[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (n0 + i < N) out.store(m, n0 + i, a[i], o[i]);
+  for (int i = 0; i < 8; ++i) bias[i] = v[i] = 0.0f;
+  if (out.bias) bgg::load8h(out.bias + n, bias);
+  const float* src = P + 8 * idx;
+  for (int z = 0; z < S; ++z) {
+    const float4 a = *reinterpret_cast<const float4*>(src + z * MN), b = *reinterpret_cast<const float4*>(src + z * MN + 4);
+    v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+  }
+  with_activation(out.act, [&](auto act) { store_eight<act.value>(out, m, n, v, bias, e); });
 }
 
 // ---------------------------------------------------------------------------
@@ -693,7 +788,7 @@ bgg_status ternary_gemm(const char* who, const bgg_weights_desc* d, const void* 
                          d->row_tiles, kmid, P, y);
     }
     if (P && ep) {
-      hipLaunchKernelGGL(k_gemm_sum_ep, dim3((unsigned)ceil_div(mc * ceil_div(d->N, 4), 256)), dim3(256), 0, s,
+      hipLaunchKernelGGL(k_gemm_sum_ep, dim3((unsigned)ceil_div(out.wide ? mc * d->N / 8 : mc * d->N, 256)), dim3(256), 0, s,
                          (const float*)P, p.splits, mc, d->N, out);
     } else if (P) {
       const int64_t mn = mc * d->N;

@@ -7,7 +7,6 @@ bias, |act'| <= 1.13 (SILU 1.10, both GELUs 1.13) and, for RELU2, 2 |v| + ds,
 the epilogue in fp32 is off by at most ds |act'| |mul| and about ten roundings
 and function errors, 2^-20 of (|v| |mul| + |r|) in all (RELU2: v^2 |mul|), and
 y by half an fp16 step, 2^-11 |y| (at least 2^-25)."""
-import ctypes
 import itertools
 
 import numpy as np
@@ -33,7 +32,8 @@ def act64(v, name):
     if name == "relu2":
         return np.where(v < 0, 0, v) ** 2
     if name == "silu":
-        return v / (1 + np.exp(-v))
+        with np.errstate(over="ignore"):
+            return v / (1 + np.exp(-v))
     if name == "gelu":
         return 0.5 * v * (1 + erf(v / np.sqrt(2)))
     if name == "gelu_tanh":
@@ -124,18 +124,42 @@ def test_every_activation_and_operand(act, which):
 
 @pytest.mark.parametrize("fmt", ["PQ2_0", "PTQ1_0"])
 @pytest.mark.parametrize("M,N,K", [(1, 64, 128), (17, 100, 640), (77, 6100, 1280), (130, 1001, 256), (512, 320, 384),
-                                   (300, 17408, 256), (640, 5120, 512)])
-def test_gemm_sizes(fmt, M, N, K):
-    """Unsplit and split K, ragged tiles, rows off four-value alignment."""
-    c = Case(fmt, N, K, M, pad=3)
+                                   (300, 17408, 256), (640, 5120, 512), (129, 8, 128), (127, 264, 256)])
+@pytest.mark.parametrize("pad", [0, 3, 8])
+def test_gemm_sizes(fmt, M, N, K, pad):
+    """Unsplit and split K, ragged tiles, rows of operands on 16 bytes and
+    off them."""
+    c = Case(fmt, N, K, M, pad=pad)
     c.check(c.run("gelu", how="gemm"), "gelu")
-    y = torch.full((M, N), float("nan"), dtype=torch.float16, device="cuda")
     x = torch.empty((M, K), dtype=torch.float16, device="cuda")
     bgg.bgg_hadamard_rotate(c.x_d, x, M, K)
-    bgg.bgg_ternary_gemm_epilogue(c.d, c.packed, x, y, M, 0, None, activation="relu", bias=c.b_d, mul=c.mul_d,
-                                  residual=c.r_d)  # no workspace: unsplit, PTQ1_0 without the rewrite
-    torch.cuda.synchronize()
-    c.check(y, "relu")
+    for act in ("relu", "silu"):
+        guard = torch.full((M * N + 512,), 7.0, dtype=torch.float16, device="cuda")
+        y = guard[256:256 + M * N].view(M, N)
+        y.fill_(float("nan"))
+        bgg.bgg_ternary_gemm_epilogue(c.d, c.packed, x, y, M, 0, None, activation=act, bias=c.b_d, mul=c.mul_d,
+                                      residual=c.r_d)  # no workspace: unsplit, PTQ1_0 without the rewrite
+        torch.cuda.synchronize()
+        c.check(y, act)
+        assert torch.all(guard[:256] == 7.0) and torch.all(guard[-256:] == 7.0)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("which", ["b", "m", "r", "bmr"])
+def test_wide_rows_with_every_activation(act, which):
+    """Unsplit prompt products whose operands are all on 16 bytes."""
+    c = Case("PQ2_0", 520, 256, 140, which=which)
+    x = torch.empty((140, 256), dtype=torch.float16, device="cuda")
+    bgg.bgg_hadamard_rotate(c.x_d, x, 140, 256)
+    y = torch.full((140, 520), float("nan"), dtype=torch.float16, device="cuda")
+    bgg.bgg_ternary_gemm_epilogue(c.d, c.packed, x, y, 140, 0, None, activation=act, bias=c.b_d, mul=c.mul_d,
+                                  residual=c.r_d)
+    c.check(y, act)
+    # the same values a value at a time (y off 16 bytes)
+    odd = torch.full((140 * 520 + 1,), float("nan"), dtype=torch.float16, device="cuda")[1:].view(140, 520)
+    bgg.bgg_ternary_gemm_epilogue(c.d, c.packed, x, odd, 140, 0, None, activation=act, bias=c.b_d, mul=c.mul_d,
+                                  residual=c.r_d)
+    assert torch.equal(odd, y)
 
 
 def test_large_sums_pass_the_activations():
