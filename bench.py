@@ -45,6 +45,12 @@ Also in the same JSON line:
                 transform alone over 4 rotating buffer pairs, and a dense
                 fp16 GEMM on pre-dequantised weights (torch.matmul) as a
                 comparison, run only;
+  decoder_step  (only with --context N) the decode step of whole layers at
+                batch 1 over a paged cache of N tokens per layer: grouped
+                q|k|v product, rotary positions with the cache append,
+                attention, output product onto the residual stream, gate and
+                up with SILU, down product onto the residual stream (48 query
+                and 8 key heads of 128); and its attention part alone;
   cpu_baseline  the CPU oracle on a sample of the step, on all host threads
                 and on one (with the host CPU's model name);
   context       the pages' end-to-end model figures with their hardware.
@@ -325,6 +331,73 @@ def stack_breakdown(bgg, torch, stack, capture, reps_layers):
     return rows
 
 
+def decoder_bench(args, bgg, torch, dev, capture, fmt="PQ2_0"):
+    """The decode step of args.layers whole layers (norms left out) at batch
+    1, each with its own weights and its own cache of args.context tokens."""
+    import numpy as np
+    import synth
+    heads, kv_heads, dim, page, n = 48, 8, 128, 64, args.context
+    base = {m.name.split(".")[1]: m for m in synth.decode_stack(1)}
+    host = {}
+    for name, parts in (("qkv", ("q", "k", "v")), ("o", ("o",)), ("gate", ("gate",)), ("up", ("up",)), ("down", ("down",))):
+        Ts, Ss = zip(*(synth.workload_matrix(base[q], 0) for q in parts))
+        d = bgg.bgg_describe(fmt, sum(len(t) for t in Ts), Ts[0].shape[1])
+        host[name] = (d, bgg.bgg_pack_weights(d, np.concatenate(Ts), np.concatenate(Ss)))
+    layers = [{k: bgg.upload(p, dev) for k, (_, p) in host.items()} for _ in range(args.layers)]
+    desc = {k: d for k, (d, _) in host.items()}
+    hidden, nq, nk = int(desc["o"].N), heads * dim, kv_heads * dim
+    assert int(desc["qkv"].N) == nq + 2 * nk and int(desc["o"].K) == nq
+    pages = -(-n // page)
+    cache = bgg.bgg_cache_describe("f16", pages, page, kv_heads, dim)
+    caches = [[torch.randn((pages, kv_heads, page, dim), device=dev, dtype=torch.float16) for _ in range(2)]
+              for _ in range(args.layers)]
+    table = torch.randperm(pages, device=dev).int().view(1, pages)
+    length = torch.full((1,), n, dtype=torch.int32, device=dev)
+    pos = length - 1
+    slot = table[0, (n - 1) // page].long().view(1) * page + (n - 1) % page
+    freqs, mag = bgg.bgg_rotary_frequencies(dim, 1e6)
+    freqs = torch.from_numpy(freqs).to(dev)
+    f16 = dict(dtype=torch.float16, device=dev)
+    x = torch.randn((1, hidden), **f16)
+    y, qkv, q, att = (torch.empty((1, w), **f16) for w in (hidden, nq + 2 * nk, nq, nq))
+    up, act = (torch.empty((1, int(desc["up"].N)), **f16) for _ in range(2))
+    ws = bgg.workspace(max(bgg.bgg_gemv_workspace_size(d, 1) for d in desc.values()), dev)
+    wsa = bgg.workspace(bgg.bgg_attention_workspace_size(cache, heads, 1), dev)
+    rot = bgg.BGG_ROTATE_INPUT
+
+    def attention(st):
+        for kc, vc in caches:
+            bgg.bgg_rotary_append(cache, kc, vc, pos, slot, freqs, q=qkv[:, :nq], q_out=q, k=qkv[:, nq:nq + nk],
+                                  v=qkv[:, nq + nk:], magnitude=mag, stream=st)
+            bgg.bgg_paged_attention(cache, kc, vc, table, length, q, att, wsa, scale=dim ** -0.5, stream=st)
+
+    def step(st):
+        y.copy_(x)
+        for w, (kc, vc) in zip(layers, caches):
+            bgg.bgg_ternary_gemv(desc["qkv"], w["qkv"], y, qkv, 1, rot, ws, st)
+            bgg.bgg_rotary_append(cache, kc, vc, pos, slot, freqs, q=qkv[:, :nq], q_out=q, k=qkv[:, nq:nq + nk],
+                                  v=qkv[:, nq + nk:], magnitude=mag, stream=st)
+            bgg.bgg_paged_attention(cache, kc, vc, table, length, q, att, wsa, scale=dim ** -0.5, stream=st)
+            bgg.bgg_ternary_gemv_epilogue(desc["o"], w["o"], att, y, 1, rot, ws, residual=y, stream=st)
+            bgg.bgg_ternary_gemv(desc["up"], w["up"], y, up, 1, rot, ws, st)
+            bgg.bgg_ternary_gemv_epilogue(desc["gate"], w["gate"], y, act, 1, rot, ws, activation="silu", mul=up,
+                                          stream=st)
+            bgg.bgg_ternary_gemv_epilogue(desc["down"], w["down"], act, y, 1, rot, ws, residual=y, stream=st)
+    us = {}
+    for name, fn in (("step", step), ("attention", attention)):
+        g = capture(fn)
+        us[name] = replay_us(torch, g, args.stack_replays)
+        del g
+    kv = args.layers * 2 * n * kv_heads * dim * 2
+    packed = args.layers * sum(int(d.format_bytes) for d in desc.values())
+    log(f"decoder step, {args.layers} layers, {n} tokens of context: {us['step']:.0f} us, rotary and attention "
+        f"{us['attention']:.0f} us")
+    return dict(format=fmt, layers=args.layers, context=n, heads=heads, kv_heads=kv_heads, head_dim=dim, cache="f16",
+                us_per_step=round(us["step"], 1), us_attention=round(us["attention"], 1),
+                cache_bytes=kv, packed_bytes=packed, gbs=round((kv + packed) / us["step"] / 1e3, 1),
+                attention_gbs=round(kv / us["attention"] / 1e3, 1))
+
+
 def main() -> int:
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--gpus", type=int, default=1)
@@ -339,6 +412,8 @@ def main() -> int:
                     help="timed graph replays per decode-step variant (median reported)")
     ap.add_argument("--gemm-warmup", type=int, default=40,
                     help="untimed rotate + GEMM pairs before the timed prefill launches")
+    ap.add_argument("--context", type=int, default=0, metavar="TOKENS",
+                    help="also time the decode step of whole layers over a paged cache of TOKENS tokens per layer")
     ap.add_argument("--no-prefill", action="store_true")
     ap.add_argument("--no-variants", action="store_true",
                     help="skip the shared-transform, grouped and small-batch lines")
@@ -560,6 +635,10 @@ def main() -> int:
             torch.cuda.empty_cache()
     del stacks
     torch.cuda.empty_cache()
+
+    if args.context > 0:
+        out["decoder_step"] = decoder_bench(args, bgg, torch, dev, capture)
+        torch.cuda.empty_cache()
 
     # ---------------------------------------- single projection (gate_up, down)
     pw = synth.WORKLOADS["projection"]

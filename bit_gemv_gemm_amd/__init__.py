@@ -316,16 +316,17 @@ def bgg_ternary_gemm(desc, packed_dev, x_dev, y_dev, M: int, flags: int, workspa
                               M, flags, ws, wsb, _stream(stream)), "bgg_ternary_gemm")
 
 
-# the current stream's handle without building a torch.cuda.Stream (1 us of
-# a call's 8)
+# the current stream's handle and the current device without building
+# objects (1 us of a call's 8)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _run_on(dev, stream, where, call, *args):
     """call(*args, stream) with device dev current."""
     s = _raw_stream(dev) if stream is None else _stream(stream)
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         st = call(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -429,18 +430,18 @@ def bgg_attention_workspace_size(cache: bgg_cache_desc, q_heads: int, batch: int
 def _rows(t, rows, head_dim, dtype, dev, what):
     """(pointer, stride, heads) of row operand t: [rows, heads * head_dim] or
     [rows, heads, head_dim] on device dev, the values of a row side by side."""
-    shape = t.shape
     if t.dtype is not dtype or t.get_device() != dev:
         raise ValueError(f"{what} must be {dtype} on device {dev}")
+    shape, stride = t.shape, t.stride()
     if len(shape) == 2:
         n = shape[1]
-        ok = t.stride(1) == 1 and n % head_dim == 0
+        ok = stride[1] == 1 and n % head_dim == 0
     else:
         n = shape[1] * shape[2] if len(shape) == 3 else 0
-        ok = len(shape) == 3 and shape[2] == head_dim and t.stride(2) == 1 and (shape[1] == 1 or t.stride(1) == head_dim)
+        ok = len(shape) == 3 and shape[2] == head_dim and stride[2] == 1 and (shape[1] == 1 or stride[1] == head_dim)
     if not ok or shape[0] != rows:
         raise ValueError(f"{what} must be [{rows}, heads * {head_dim}] with contiguous rows, got {tuple(shape)}")
-    return t.data_ptr(), t.stride(0) if rows > 1 else n, n // head_dim
+    return t.data_ptr(), stride[0] if rows > 1 else n, n // head_dim
 
 
 def _vector(t, n, dtype, dev, what):
