@@ -122,8 +122,13 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item& 
   const int H = p.kv_heads * p.head_blocks;
   const int per = (p.batch + 63) / 64;
   const int b0 = lane * per, b1 = min(p.batch, b0 + per);
-  float tiles = 0.0f;
-  for (int b = b0; b < b1; ++b) {
+  // (the first sequence of the lane stays in registers: up to 64 sequences
+  // read their lengths once)
+  int lo0 = 0, n0 = 0;
+  if (b0 < b1) visible(p, b0, lo0, n0);
+  const int t0 = tiles_of(lo0, n0);
+  float tiles = (float)t0;
+  for (int b = b0 + 1; b < b1; ++b) {
     int lo, n;
     visible(p, b, lo, n);
     tiles += (float)tiles_of(lo, n);
@@ -134,8 +139,8 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item& 
   const float even = fminf(ceilf(all * (float)H / (float)p.target_items * 1.0001f), 1e8f);
   // chunks in the low half, those of sequences with several in the high half
   auto counts = [&](int size) {
-    int c = 0;
-    for (int b = b0; b < b1; ++b) {
+    int c = b0 < b1 ? both_counts(chunks_of(t0, size)) : 0;
+    for (int b = b0 + 1; b < b1; ++b) {
       int lo, n;
       visible(p, b, lo, n);
       c += both_counts(chunks_of(tiles_of(lo, n), size));
@@ -180,10 +185,13 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item& 
     const int o = __builtin_ctzll(__ballot((u & 0xFFFF) > seq_item));
     before = __builtin_amdgcn_readlane(u - c, o);
     b += o;
+    visible(p, b, lo0, n0);
+    it.lo = __builtin_amdgcn_readfirstlane(lo0);
+    it.n = __builtin_amdgcn_readfirstlane(n0);
+  } else {
+    it.lo = __builtin_amdgcn_readlane(lo0, owner);
+    it.n = __builtin_amdgcn_readlane(n0, owner);
   }
-  visible(p, b, it.lo, it.n);
-  it.lo = __builtin_amdgcn_readfirstlane(it.lo);
-  it.n = __builtin_amdgcn_readfirstlane(it.n);
   const int t = tiles_of(it.lo, it.n), first = it.lo / kTokens;
   it.b = b;
   it.head_block = index % H;
@@ -388,10 +396,14 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // maximum.
 constexpr float kSlack = 8.0f, kLift = 7.0f;
 
-// Floats of a part: accumulators [rows][D], maxima [rows], sums [rows].
+// Floats of a part: rows of D accumulators, the sum and three unused, then
+// the rows' maxima.
 __host__ __device__ constexpr int64_t part_floats(int64_t rows, int64_t D) {
-  return (rows * (D + 2) + 3) / 4 * 4;
+  return rows * (D + 4) + (rows + 3) / 4 * 4;
 }
+// Chunks of a sequence at most (the items of one sequence and head block,
+// about target_items of which there are kMaxItems at most).
+constexpr int kMaxItems = 256, kMaxChunks = kMaxItems + 1;
 
 // The parts pass from one workgroup to another, maybe on another die with
 // its own L2, by stores and loads that go through to the memory all dies
@@ -429,112 +441,101 @@ __device__ __forceinline__ void store_out(const AttnParams& p, int b, int h, int
 }
 
 // The parts of a sequence's chunks (at parts, parts + step, ...) into its
-// output: maxima and sums, then the accumulators weighted, four values per
-// thread; with fewer columns of four than threads the threads also share the
-// chunks out among them.  The loads that need nothing but addresses -- the
-// maxima and sums of the first 64 chunks and the first accumulators -- go
-// out together, so that up to 16 chunks cost one trip to memory.  `lds` holds
-// 16 * 64 + 16 D floats or more.
+// output: each chunk's weight 2^(m_c - m), then the weighted rows, four
+// values per thread (the sum is a column like the others); with fewer columns
+// of four than threads the threads also share the chunks out among them.  The
+// maxima and the first rows are loaded together, so that up to eight chunks
+// cost one trip to memory.  This code runs once, by one workgroup per
+// sequence and head block, so its instructions come from memory too: it is
+// kept short by loops (unrolled to 16 parts in flight and four columns it
+// took 9 us instead of 5 for 32 chunks of 8 x 128).  `lds` holds 16
+// kMaxChunks floats.
 template <class T, int D>
 __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, const float* parts,
                                            int64_t step, int rows, int heads, int h0, float vs,
                                            float* lds, float* lds16) {
   constexpr int kThreads = 64 * kWaves, kRows = kThreads / 16;  // threads of a head
-  constexpr int kBlock = 64;                                    // chunks weighted at a time
-  constexpr int kMine = kBlock / kRows;                         // of them by one thread
-  constexpr int kFlight = 16;                                   // a thread's parts in flight
-  constexpr int kCols = (kHeads * (D / 4) + kThreads - 1) / kThreads;
+  constexpr int kFlight = 8;                                    // a thread's parts in flight
+  constexpr int kHead = D / 4 + 1;                              // columns of a head
+  constexpr int kCols = (kHeads * kHead + kThreads - 1) / kThreads;
   const int tid = threadIdx.x, hr = tid & 15, cr = tid >> 4;
-  float* weight = lds;  // [kBlock][16]
-  const int columns = heads * (D / 4);
+  const int columns = heads * kHead;
   const int share = columns >= kThreads ? 1 : kThreads / columns;  // threads per column
   const int part_of = share > 1 ? tid / columns : 0, col0 = share > 1 ? tid % columns : tid;
 
-  // maxima and sums of head hr over the chunks c0 + cr, c0 + cr + kRows, ...
-  float mc[kMine], lc[kMine];
-  auto load_stats = [&](int c0) {
-#pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-      const int c = c0 + cr + kRows * j;
-      const bool in = c < it.chunks && hr < heads;
-      const float* x = parts + (in ? c : 0) * step + rows * D + (in ? hr : 0);
-      mc[j] = get1(x);
-      lc[j] = get1(x + rows);
-      if (!in) mc[j] = -FLT_MAX, lc[j] = 0.0f;
-    }
-  };
   uint64_t a[kFlight][2];
-  auto load_flight = [&](int col, int c0, int n, int cb) {
-    const float* x = parts + c0 * step + 4 * col;
+  auto load_flight = [&](int col, int cb) {
+    const float* x = parts + 4 * col;
 #pragma unroll
     for (int j = 0; j < kFlight; ++j) {
-      const int c = min(cb + j * share, n - 1);
+      const int64_t c = min(cb + j * share, it.chunks - 1);
       a[j][0] = get2(x + c * step);
       a[j][1] = get2(x + c * step + 2);
     }
   };
-  load_stats(0);
-  load_flight(min(col0, columns - 1), 0, min(kBlock, it.chunks), min(part_of, share - 1));
+  load_flight(min(col0, columns - 1), part_of);
 
-  float mh = -FLT_MAX, lh = 0.0f;
-#pragma unroll
-  for (int j = 0; j < kMine; ++j) mh = fmaxf(mh, mc[j]);
-  if (hr < heads)
-    for (int c = kBlock + cr; c < it.chunks; c += kRows) mh = fmaxf(mh, get1(parts + c * step + rows * D + hr));
-  weight[cr * 16 + hr] = mh;
+  float mh = -FLT_MAX;
+#pragma unroll 1
+  for (int c = cr; c < it.chunks; c += kRows) {
+    const float m = hr < heads ? get1(parts + c * step + rows * (D + 4) + hr) : -FLT_MAX;
+    lds[c * 16 + hr] = m;
+    mh = fmaxf(mh, m);
+  }
+  lds16[cr * 16 + hr] = mh;
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < kRows; ++j) mh = fmaxf(mh, weight[j * 16 + hr]);
+  for (int j = 0; j < kRows; ++j) mh = fmaxf(mh, lds16[j * 16 + hr]);
+#pragma unroll 1
+  for (int c = cr; c < it.chunks; c += kRows) lds[c * 16 + hr] = __builtin_amdgcn_exp2f(lds[c * 16 + hr] - mh);
+  __syncthreads();
+
   f32x4 o[kCols];
 #pragma unroll
   for (int k = 0; k < kCols; ++k) o[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int c0 = 0; c0 < it.chunks; c0 += kBlock) {
-    const int n = min(kBlock, it.chunks - c0);
-    if (c0) load_stats(c0);
-    __syncthreads();  // (the weights of the last block, and the maxima, are read)
 #pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-      const float w = __builtin_amdgcn_exp2f(mc[j] - mh);
-      lh += lc[j] * w;
-      weight[(cr + kRows * j) * 16 + hr] = w;
-    }
-    __syncthreads();
+  for (int k = 0; k < kCols; ++k) {
+    const int col = col0 + k * kThreads;
+    if (col >= columns || part_of >= share) continue;
+    const float* w = lds + col / kHead;
+#pragma unroll 1
+    for (int cb = part_of; cb < it.chunks; cb += kFlight * share) {
+      if (k > 0 || cb != part_of) load_flight(col, cb);
 #pragma unroll
-    for (int k = 0; k < kCols; ++k) {
-      const int col = col0 + k * kThreads;
-      if (col >= columns || part_of >= share) continue;
-      const int h = col / (D / 4);
-      for (int cb = part_of; cb < n; cb += kFlight * share) {
-        if (k > 0 || c0 > 0 || cb != part_of) load_flight(col, c0, n, cb);
+      for (int j = 0; j < kFlight; ++j) {
+        const int c = cb + j * share;
+        const float wc = c < it.chunks ? w[c * 16] : 0.0f;
+        // (a part past the last repeats it, with weight 0: an infinite value
+        // there would make it NaN)
 #pragma unroll
-        for (int j = 0; j < kFlight; ++j) {
-          if (cb + j * share >= n) continue;
-          const float w = weight[(cb + j * share) * 16 + h];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[k][i] += __uint_as_float((uint32_t)(a[j][i / 2] >> (32 * (i % 2)))) * w;
+        for (int i = 0; i < 4; ++i) {
+          const float v = __uint_as_float((uint32_t)(a[j][i / 2] >> (32 * (i % 2))));
+          o[k][i] = c < it.chunks ? fmaf(v, wc, o[k][i]) : o[k][i];
         }
       }
     }
   }
-  // the sums of the threads of a head, and the shares of a column
-  float* sums = lds + kBlock * 16;
+  // the shares of a column, and the sums
   __syncthreads();
-  weight[cr * 16 + hr] = lh;
+  if (part_of > 0 && part_of < share) *reinterpret_cast<f32x4*>(lds + 4 * (part_of * columns + col0)) = o[0];
   if (cr == 0) lds16[hr] = mh;
-  if (share > 1 && part_of > 0 && part_of < share)
-    *reinterpret_cast<f32x4*>(sums + 4 * (part_of * columns + col0)) = o[0];
+  __syncthreads();
+  if (part_of == 0) {
+#pragma unroll 1
+    for (int j = 1; j < share; ++j) o[0] += *reinterpret_cast<const f32x4*>(lds + 4 * (j * columns + col0));
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) {
+      const int col = col0 + k * kThreads;
+      if (col < columns && col % kHead == D / 4) lds16[16 + col / kHead] = o[k][0];
+    }
+  }
   __syncthreads();
   if (part_of > 0) return;
 #pragma unroll
   for (int k = 0; k < kCols; ++k) {
-    const int col = col0 + k * kThreads;
-    if (col >= columns) continue;
-    for (int j = 1; j < share; ++j) o[k] += *reinterpret_cast<const f32x4*>(sums + 4 * (j * columns + col));
-    const int h = col / (D / 4);
-    float l = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kRows; ++j) l += weight[j * 16 + h];
-    store_out<T>(p, it.b, h0 + h, D, 4 * (col % (D / 4)), o[k], lds16[h], l, vs);
+    const int col = col0 + k * kThreads, h = col / kHead;
+    if (col >= columns || col % kHead == D / 4) continue;
+    store_out<T>(p, it.b, h0 + h, D, 4 * (col % kHead), o[k], lds16[h], lds16[16 + h], vs);
   }
 }
 
@@ -548,8 +549,9 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
   using V = typename TL::V;
   constexpr int PL = TL::PL;
   constexpr int RowF = D + 4;  // floats between heads in LDS
-  __shared__ float red[kWaves][kHeads][RowF];
-  __shared__ float red_m[kWaves][kHeads], red_l[kWaves][kHeads];
+  __shared__ __attribute__((aligned(16))) float red[kWaves][kHeads][RowF];
+  __shared__ float red_m[kWaves][kHeads], red_l[kWaves][kHeads], red_j[4 * kWaves * 16];
+  static_assert(sizeof red >= 4 * 16 * kMaxChunks && sizeof red >= 4 * 4 * 64 * kWaves, "join_parts' weights and shares");
   __shared__ uint32_t arrived;
 
   Item it;
@@ -715,9 +717,10 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
     if (it.chunks == 1) {
       store_out<T>(p, it.b, h0 + h, D, d, o, mh, lh, vs);
     } else {
-      put2(part + h * D + d, o[0], o[1]);
-      put2(part + h * D + d + 2, o[2], o[3]);
-      if (d == 0) put1(part + rows * D + h, mh), put1(part + rows * D + rows + h, lh);
+      float* row = part + h * (D + 4);
+      put2(row + d, o[0], o[1]);
+      put2(row + d + 2, o[2], o[3]);
+      if (d == 0) put2(row + D, lh, 0.0f), put2(row + D + 2, 0.0f, 0.0f), put1(part + rows * (D + 4) + h, mh);
     }
   }
   if (it.chunks == 1) return;
@@ -734,7 +737,7 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
   if (arrived != (uint32_t)it.chunks - 1) return;
   if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   join_parts<T, D>(p, it, part - (int64_t)it.chunk * H * slot, H * slot, rows, heads, h0, vs,
-                   &red[0][0][0], &red_m[0][0]);
+                   &red[0][0][0], red_j);
 }
 
 // ---------------------------------------------------------------------------
@@ -754,6 +757,7 @@ struct AttnPlan {
 // call's shape, so that one workspace serves any sequence of calls: a
 // sequence of several chunks counts in the word of its first part.
 constexpr uint64_t kCounterBytes = BGG_ATTENTION_COUNTER_BYTES;
+static_assert(2 * kMaxItems * 4 <= kCounterBytes, "a counter per part");
 
 AttnPlan plan_attention(const bgg_cache_desc* c, int64_t q_heads, int64_t batch) {
   AttnPlan p;
@@ -761,7 +765,7 @@ AttnPlan plan_attention(const bgg_cache_desc* c, int64_t q_heads, int64_t batch)
   // one workgroup per CU: each one more per CU costs its own start and part
   // (1 x 262144 tokens f16: 1, 2, 3, 4 per CU 189, 193, 200, 208 us; 16
   // ragged sequences up to 8000 tokens of 4 x 256 bf16: 39, 44, 51, 59 us)
-  p.target = std::min<int64_t>(device_cus(), kCounterBytes / 8);
+  p.target = std::min<int64_t>(device_cus(), kMaxItems);
   p.items = p.target + batch * p.heads;
   // (a sequence of n > 1 chunks has more than (n - 1) >= n / 2 full ones)
   p.parts = 2 * p.target;
