@@ -39,7 +39,7 @@ struct AttnParams {
   float* parts;
   float scale;
   int max_tokens, pages, batch, q_heads, kv_heads, group, head_blocks, page_shift;
-  int target_items, min_tiles;
+  int target_items;
 };
 
 // ---------------------------------------------------------------------------
@@ -109,8 +109,18 @@ __device__ __forceinline__ void visible(const AttnParams& p, int b, int& lo, int
 __device__ __forceinline__ int tiles_of(int lo, int n) {
   return n > lo ? (n - 1) / kTokens - lo / kTokens + 1 : 0;
 }
+// A sequence of up to kOneChunk tiles stays whole: the join costs more than
+// the chunks gain (one sequence of 500 tokens, 8 x 128 f16: chunks of 4, 8,
+// 16 tiles 10.3, 11.2, 9.2 us).  A longer one is joined in any case; a wave's
+// tile costs about 1.2 us of latency and a part 0.15 us of the join, so a
+// chunk has at least about sqrt(tiles / 2) tiles (chunks of 4, 8, 16 tiles:
+// 1024 tokens 10.0, 10.8, 12.9 us; 2048 11.7, 11.3, 13.3; 8192 17.6, 17.4,
+// 15.8).
+constexpr int kOneChunk = 16;
 __device__ __forceinline__ int chunks_of(int tiles, int size) {
-  return tiles <= size ? 1 : (tiles + size - 1) / size;
+  if (tiles <= kOneChunk) return 1;
+  size = max(size, tiles <= 32 ? 4 : tiles <= 128 ? 8 : 16);
+  return (tiles + size - 1) / size;
 }
 
 __device__ __forceinline__ int both_counts(int chunks) {
@@ -156,13 +166,13 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item& 
   if (p.batch * H <= p.target_items) {
 #pragma unroll 1
     for (int k = 8; k <= 16; k += 2) {
-      size = max(p.min_tiles, (int)(even * (float)k * 0.125f));
+      size = max(1, (int)(even * (float)k * 0.125f));
       mine = counts(size);
       upto = scan_add(mine);
       if ((__builtin_amdgcn_readlane(upto, 63) & 0xFFFF) * H <= p.target_items) break;
     }
   } else {
-    size = max(p.min_tiles, (int)even);
+    size = max(1, (int)even);
     mine = counts(size);
     upto = scan_add(mine);
   }
@@ -743,10 +753,6 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
 // ---------------------------------------------------------------------------
 // plan and launch
 // ---------------------------------------------------------------------------
-// Tiles of a chunk at least: four for each wave.  Fewer gain less than the
-// join costs (one sequence of 500 tokens, 8 x 128 f16: chunks of 4, 8, 16
-// tiles 10.3, 11.2, 9.5 us).
-constexpr int kMinTiles = 16;
 
 struct AttnPlan {
   int64_t heads;  // head blocks of all key heads
@@ -831,7 +837,6 @@ bgg_status bgg_paged_attention(const bgg_cache_desc* c, const bgg_attention_args
   p.head_blocks = (int)ceil_div(p.group, kHeads);
   p.page_shift = __builtin_ctzll((unsigned long long)c->page_size);
   p.target_items = (int)plan.target;
-  p.min_tiles = kMinTiles;
   hipStream_t s = (hipStream_t)stream;
   const bool e4m3 = c->type == BGG_TYPE_E4M3;
   if (a->type == BGG_TYPE_F16) {
