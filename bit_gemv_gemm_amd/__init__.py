@@ -355,9 +355,12 @@ def _epilogue(N, M, dev, activation, bias, mul, residual):
                           _vector(bias, N, torch.float16, dev, "bias"), mp, rp, ms, rs)
 
 
-def _device_of(y, *others):
-    """y's device, which the others (or None) share."""
+def _device_of(x, y, *others):
+    """The device of y, which x and the others (or None) share; x (or None)
+    and y are float16."""
     dev = y.get_device()
+    if y.dtype is not torch.float16 or x is not None and (x.dtype is not torch.float16 or x.get_device() != dev):
+        raise ValueError(f"x and y must be float16 on one device, y is {y.dtype} on {dev}")
     for t in others:
         if t is not None and t.get_device() != dev:
             raise ValueError("the buffers of one call must be on one device")
@@ -368,7 +371,7 @@ def bgg_ternary_gemv_epilogue(desc, packed_dev, x_dev, y_dev, M: int, flags: int
                               bias=None, mul=None, residual=None, stream=None) -> None:
     """y = act(W x' + bias) * mul + residual, 1 <= M <= 16 tokens; bias [N],
     mul and residual [M, N], all float16 or None."""
-    dev, N = _device_of(y_dev, packed_dev, x_dev, workspace), desc.N
+    dev, N = _device_of(x_dev, y_dev, packed_dev, workspace), desc.N
     wsb = workspace.numel() * workspace.element_size()
     _run_on(dev, stream, "bgg_ternary_gemv_epilogue", _lib.bgg_ternary_gemv_epilogue, desc,
             _dev_ptr(packed_dev, desc.total_bytes, "packed"), _dev_ptr(x_dev, M * desc.K * 2, "x"),
@@ -379,7 +382,7 @@ def bgg_ternary_gemv_epilogue(desc, packed_dev, x_dev, y_dev, M: int, flags: int
 def bgg_gemv_run_epilogue(desc, packed_dev, y_dev, M: int, workspace, activation="none", bias=None, mul=None,
                           residual=None, stream=None) -> None:
     """bgg_gemv_run with an epilogue (see bgg_ternary_gemv_epilogue)."""
-    dev, N = _device_of(y_dev, packed_dev, workspace), desc.N
+    dev, N = _device_of(None, y_dev, packed_dev, workspace), desc.N
     wsb = workspace.numel() * workspace.element_size()
     _run_on(dev, stream, "bgg_gemv_run_epilogue", _lib.bgg_gemv_run_epilogue, desc,
             _dev_ptr(packed_dev, desc.total_bytes, "packed"), _dev_ptr(y_dev, M * N * 2, "y"), M,
@@ -389,7 +392,7 @@ def bgg_gemv_run_epilogue(desc, packed_dev, y_dev, M: int, workspace, activation
 def bgg_ternary_gemm_epilogue(desc, packed_dev, x_dev, y_dev, M: int, flags: int, workspace, activation="none",
                               bias=None, mul=None, residual=None, stream=None) -> None:
     """y = act(W x' + bias) * mul + residual for a prompt of M tokens."""
-    dev, N = _device_of(y_dev, packed_dev, x_dev, workspace), desc.N
+    dev, N = _device_of(x_dev, y_dev, packed_dev, workspace), desc.N
     wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _run_on(dev, stream, "bgg_ternary_gemm_epilogue", _lib.bgg_ternary_gemm_epilogue, desc,
             _dev_ptr(packed_dev, desc.total_bytes, "packed"), _dev_ptr(x_dev, M * desc.K * 2, "x"),

@@ -774,7 +774,7 @@ AttnPlan plan_attention(const bgg_cache_desc* c, int64_t q_heads, int64_t batch)
   p.target = std::min<int64_t>(device_cus(), kMaxItems);
   p.items = p.target + batch * p.heads;
   // (a sequence of n > 1 chunks has more than (n - 1) >= n / 2 full ones)
-  p.parts = 2 * p.target;
+  p.parts = 2 * kMaxItems;  // (whatever the device, so that the size does not depend on it)
   p.total_bytes = kCounterBytes + align256(
       4 * (uint64_t)(p.parts * part_floats(std::min<int64_t>(kHeads, q_heads / c->kv_heads), c->head_dim)));
   return p;

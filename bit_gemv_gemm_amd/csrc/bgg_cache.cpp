@@ -69,7 +69,7 @@ bgg_status check_rotary(const bgg_cache_desc* c, const bgg_rotary_args* a) {
   if (a->rotary_dim < 2 || a->rotary_dim > c->head_dim || a->rotary_dim % 2)
     return fail(BGG_ERR_SHAPE, "%s: rotary_dim %lld of a head of %lld", who,
                 (long long)a->rotary_dim, (long long)c->head_dim);
-  if (a->tokens < 0 || a->tokens > 0x7FFFFFFF)
+  if (a->tokens < 0 || a->tokens > kMaxTokens)
     return fail(BGG_ERR_SHAPE, "%s: %lld tokens", who, (long long)a->tokens);
   if ((st = check_type(who, a->type))) return st;
   if (!a->positions_dev || !a->freqs_dev) return fail(BGG_ERR_NULL, "%s: NULL buffer", who);

@@ -6,6 +6,7 @@
 namespace bgg {
 
 constexpr int64_t kMaxQHeads = 4096;
+constexpr int64_t kMaxTokens = int64_t(1) << 23;  // (a workgroup each, in a grid below 2^32 threads)
 constexpr int64_t kMaxBatch = 4096;  // (a wave looks through 64 sequences per lane)
 
 // BGG_OK iff `c` is exactly what bgg_cache_describe makes for its fields.

@@ -361,29 +361,32 @@ __global__ void __launch_bounds__(256) k_gemm_sum(const float* __restrict__ P, i
 // thread where the rows are wide, else one.
 __global__ void __launch_bounds__(256) k_gemm_sum_ep(const float* __restrict__ P, int S, int64_t M, int64_t N,
                                                      bgg::EpilogueOut out) {
-  const int64_t MN = M * N, idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t MN = M * N, step = (int64_t)gridDim.x * 256;
+  int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (!out.wide) {
-    if (idx >= MN) return;
-    const int64_t m = idx / N, n = idx % N;
-    const bgg::EpilogueOut::Operands o = out.load(m, n);
-    float a = P[idx];
-    for (int z = 1; z < S; ++z) a += P[z * MN + idx];
-    out.store(m, n, a, o);
+    for (; idx < MN; idx += step) {
+      const int64_t m = idx / N, n = idx % N;
+      const bgg::EpilogueOut::Operands o = out.load(m, n);
+      float a = P[idx];
+      for (int z = 1; z < S; ++z) a += P[z * MN + idx];
+      out.store(m, n, a, o);
+    }
     return;
   }
-  if (8 * idx >= MN) return;
-  const int64_t m = 8 * idx / N, n = 8 * idx % N;  // (N % 8 == 0: one row)
-  const Eight e = load_eight(out, m, n);
-  float bias[8], v[8];
+  for (; 8 * idx < MN; idx += step) {
+    const int64_t m = 8 * idx / N, n = 8 * idx % N;  // (N % 8 == 0: one row)
+    const Eight e = load_eight(out, m, n);
+    float bias[8], v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) bias[i] = v[i] = 0.0f;
-  if (out.bias) bgg::load8h(out.bias + n, bias);
-  const float* src = P + 8 * idx;
-  for (int z = 0; z < S; ++z) {
-    const float4 a = *reinterpret_cast<const float4*>(src + z * MN), b = *reinterpret_cast<const float4*>(src + z * MN + 4);
-    v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+    for (int i = 0; i < 8; ++i) bias[i] = v[i] = 0.0f;
+    if (out.bias) bgg::load8h(out.bias + n, bias);
+    const float* src = P + 8 * idx;
+    for (int z = 0; z < S; ++z) {
+      const float4 a = *reinterpret_cast<const float4*>(src + z * MN), b = *reinterpret_cast<const float4*>(src + z * MN + 4);
+      v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+    }
+    with_activation(out.act, [&](auto act) { store_eight<act.value>(out, m, n, v, bias, e); });
   }
-  with_activation(out.act, [&](auto act) { store_eight<act.value>(out, m, n, v, bias, e); });
 }
 
 // ---------------------------------------------------------------------------
@@ -788,7 +791,10 @@ bgg_status ternary_gemm(const char* who, const bgg_weights_desc* d, const void* 
                          d->row_tiles, kmid, P, y);
     }
     if (P && ep) {
-      hipLaunchKernelGGL(k_gemm_sum_ep, dim3((unsigned)ceil_div(out.wide ? mc * d->N / 8 : mc * d->N, 256)), dim3(256), 0, s,
+      // (a grid holds less than 2^32 threads: each takes several values of
+      // the largest outputs)
+      const int64_t blocks = ceil_div(out.wide ? mc * d->N / 8 : mc * d->N, 256);
+      hipLaunchKernelGGL(k_gemm_sum_ep, dim3((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20)), dim3(256), 0, s,
                          (const float*)P, p.splits, mc, d->N, out);
     } else if (P) {
       const int64_t mn = mc * d->N;

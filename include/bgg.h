@@ -485,7 +485,7 @@ typedef struct bgg_rotary_args {
   int32_t type;             /* BGG_TYPE_F16 or BGG_TYPE_BF16: q, q_out, k, v */
   int32_t layout;           /* bgg_rotary_layout */
   int64_t rotary_dim;       /* first values of a head that turn: even, 2 .. head_dim */
-  int64_t tokens;           /* T >= 0 */
+  int64_t tokens;           /* 0 <= T <= 2^23 */
   int64_t q_heads;          /* 1 .. 4096 with q, else 0 */
   const void* q_dev;        /* [T][q_heads][head_dim]; NULL: keys and values only */
   void* q_out_dev;          /* same shape; may be q_dev with the same stride */

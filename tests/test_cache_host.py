@@ -115,7 +115,7 @@ def attention(desc, **change):
 @pytest.mark.parametrize("change,status", [
     (dict(type=3), FORMAT), (dict(type=0), FORMAT), (dict(type=2), FORMAT), (dict(layout=2), FORMAT),
     (dict(ksc=P, vsc=P), FORMAT), (dict(reserved=1), SHAPE), (dict(rotary_dim=0), SHAPE), (dict(rotary_dim=63), SHAPE),
-    (dict(rotary_dim=66), SHAPE), (dict(tokens=-1), SHAPE), (dict(tokens=1 << 31), SHAPE), (dict(q_heads=0), SHAPE),
+    (dict(rotary_dim=66), SHAPE), (dict(tokens=-1), SHAPE), (dict(tokens=(1 << 23) + 1), SHAPE), (dict(q_heads=0), SHAPE),
     (dict(q_heads=4097, qs=1 << 20, qos=1 << 20), SHAPE), (dict(qs=248), SHAPE), (dict(qos=260), SHAPE),
     (dict(ks=120), SHAPE), (dict(vs=129), SHAPE), (dict(qos=264), SHAPE), (dict(q=0), NULL), (dict(q_out=0), NULL),
     (dict(k=0), NULL), (dict(v=0), NULL), (dict(q=0, q_heads=0, k=0, v=0), NULL), (dict(positions=0), NULL),

@@ -154,6 +154,67 @@ def test_ragged_batch():
     run_check(case(lengths, hq=12, hk=4, D=128, dtype="bf16", kv="bf16", page=64))
 
 
+def test_large_batch_with_a_few_long_sequences():
+    """More than 64 sequences (several per lane of the schedule), some cut in
+    chunks."""
+    lengths = [1 + (i * 13) % 40 for i in range(150)]
+    for b in (0, 63, 64, 149):
+        lengths[b] = 3000 + b
+    lengths[77] = 0
+    run_check(case(lengths, hq=8, hk=1, D=64, page=32, seed=31))
+
+
+def test_largest_batch():
+    lengths = [(i * 7) % 4 for i in range(4096)]
+    lengths[2048], lengths[4095] = 900, 700
+    run_check(case(lengths, hq=2, hk=1, D=64, kv="e4m3", seed=32))
+
+
+@pytest.mark.parametrize("hq,hk", [(4096, 1), (1024, 1024), (4096, 512)])
+def test_largest_head_counts(hq, hk):
+    run_check(case([40, 3], hq=hq, hk=hk, D=64, seed=33))
+
+
+def test_largest_page_and_one_wide_table():
+    run_check(case([70000, 5], hq=2, hk=1, D=64, page=65536, seed=34))
+    run_check(case([40], hq=2, hk=1, D=64, page=16, width=(1 << 31) // 16 - 1, seed=34))
+
+
+def test_subnormal_keys_and_values_count():
+    """fp16 values below 2^-14 are not flushed."""
+    c = case([300], hq=4, hk=1, D=64, seed=35)
+    for x in c["caches"]:
+        x *= 2.0 ** -22
+    c["scale"] = 2.0 ** 20
+    assert (c["caches"][0].abs() < 2.0 ** -14).all() and c["caches"][0].any()
+    d = Device(c)
+    d.step()
+    torch.cuda.synchronize()
+    out, lse, tol, ltol = formula(c)
+    got = d.out.double().cpu().numpy().reshape(out.shape)
+    assert np.all(np.abs(got - out) <= tol) and np.abs(got).max() > 2.0 ** -24
+    assert np.all(np.abs(d.lse.double().cpu().numpy() - lse) <= ltol)
+
+
+def test_two_streams_with_their_own_workspaces():
+    """Calls that overlap in time."""
+    cs = [case([5000, 40], hq=12, hk=2, seed=41), case([3000] * 3, hq=8, hk=4, D=64, seed=42)]
+    ds = [Device(c) for c in cs]
+    for d in ds:
+        d.step()
+    torch.cuda.synchronize()
+    want = [d.out.clone() for d in ds]
+    streams = [torch.cuda.Stream() for _ in ds]
+    for d in ds:
+        d.out.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for d, s in zip(ds, streams):
+            d.step(stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(d.out, w) for d, w in zip(ds, want))
+
+
 def test_many_short_sequences():
     run_check(case([1 + (i * 7) % 50 for i in range(300)], hq=4, hk=2, D=64))
 

@@ -130,6 +130,12 @@ def test_far_and_negative_positions(far):
     check_case(c, *run(c))
 
 
+@pytest.mark.parametrize("T,hq,hk,layout", [(2, 4096, 1024, "half"), (20001, 2, 1, "interleaved"), (1, 1, 1024, "half")])
+def test_many_heads_and_tokens(T, hq, hk, layout):
+    c = case(T=T, hq=hq, hk=hk, D=64, R=32, layout=layout, seed=T)
+    check_case(c, *run(c))
+
+
 def test_in_place_queries():
     c = case(T=20, seed=5)
     check_case(c, *run(c, in_place=True))
