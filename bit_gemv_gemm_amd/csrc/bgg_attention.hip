@@ -138,6 +138,7 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item& 
   if (b0 < b1) visible(p, b0, lo0, n0);
   const int t0 = tiles_of(lo0, n0);
   float tiles = (float)t0;
+#pragma unroll 1
   for (int b = b0 + 1; b < b1; ++b) {
     int lo, n;
     visible(p, b, lo, n);
@@ -147,34 +148,27 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item& 
   // more than target_items + batch * H workgroups)
   const float all = wave_add(tiles);
   const float even = fminf(ceilf(all * (float)H / (float)p.target_items * 1.0001f), 1e8f);
-  // chunks in the low half, those of sequences with several in the high half
-  auto counts = [&](int size) {
-    int c = b0 < b1 ? both_counts(chunks_of(t0, size)) : 0;
-    for (int b = b0 + 1; b < b1; ++b) {
-      int lo, n;
-      visible(p, b, lo, n);
-      c += both_counts(chunks_of(tiles_of(lo, n), size));
-    }
-    return c;
-  };
   // The last chunk of every sequence is a full workgroup too, so the even
   // size gives a few workgroups more than the GPU takes at once, and they
   // would run alone at the end: a larger size that gives target_items at
   // most, if one up to twice the even size does (16 ragged sequences up to
   // 8000 tokens of 4 x 256 bf16: 280 workgroups 39.8 us, 256 29.7 us).
-  int size = 0, mine = 0, upto = 0;
-  if (p.batch * H <= p.target_items) {
+  // Chunks are counted in the low half, those of sequences with several in
+  // the high half.
+  int size = 0, upto = 0, mine = 0;
 #pragma unroll 1
-    for (int k = 8; k <= 16; k += 2) {
-      size = max(1, (int)(even * (float)k * 0.125f));
-      mine = counts(size);
-      upto = scan_add(mine);
-      if ((__builtin_amdgcn_readlane(upto, 63) & 0xFFFF) * H <= p.target_items) break;
+  for (int k = 8; k <= 16; k += 2) {
+    size = max(1, (int)(even * (float)k * 0.125f));
+    mine = b0 < b1 ? both_counts(chunks_of(t0, size)) : 0;
+#pragma unroll 1
+    for (int b = b0 + 1; b < b1; ++b) {
+      int lo, n;
+      visible(p, b, lo, n);
+      mine += both_counts(chunks_of(tiles_of(lo, n), size));
     }
-  } else {
-    size = max(1, (int)even);
-    mine = counts(size);
     upto = scan_add(mine);
+    if (p.batch * H > p.target_items) break;
+    if ((__builtin_amdgcn_readlane(upto, 63) & 0xFFFF) * H <= p.target_items) break;
   }
   size = __builtin_amdgcn_readfirstlane(size);
   const int seq_item = index / H;  // chunks before this one, over all sequences
@@ -406,10 +400,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // maximum.
 constexpr float kSlack = 8.0f, kLift = 7.0f;
 
-// Floats of a part: rows of D accumulators, the sum and three unused, then
-// the rows' maxima.
+// Floats of a part: rows of D accumulators, then each row's maximum and sum.
 __host__ __device__ constexpr int64_t part_floats(int64_t rows, int64_t D) {
-  return rows * (D + 4) + (rows + 3) / 4 * 4;
+  return (rows * (D + 2) + 3) / 4 * 4;
 }
 // Chunks of a sequence at most (the items of one sequence and head block,
 // about target_items of which there are kMaxItems at most).
@@ -424,13 +417,6 @@ __device__ __forceinline__ void put2(float* p, float a, float b) {
   const uint64_t v = (uint64_t)__float_as_uint(a) | ((uint64_t)__float_as_uint(b) << 32);
   __hip_atomic_store(reinterpret_cast<uint64_t*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ void put1(float* p, float a) {
-  __hip_atomic_store(reinterpret_cast<uint32_t*>(p), __float_as_uint(a), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float get1(const float* p) {
-  return __uint_as_float(
-      __hip_atomic_load(reinterpret_cast<const uint32_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-}
 __device__ __forceinline__ uint64_t get2(const float* p) {
   return __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -440,42 +426,42 @@ template <class T>
 __device__ __forceinline__ void store_out(const AttnParams& p, int b, int h, int D, int d, f32x4 o, float m,
                                           float l, float vs) {
   const bool none = l == 0.0f;
+  const float f = none ? 0.0f : vs / l;
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    w[i] = (uint32_t)T::bits(none ? 0.0f : o[2 * i] * vs / l) |
-           ((uint32_t)T::bits(none ? 0.0f : o[2 * i + 1] * vs / l) << 16);
+    w[i] = (uint32_t)T::bits(o[2 * i] * f) | ((uint32_t)T::bits(o[2 * i + 1] * f) << 16);
   *reinterpret_cast<u32x2*>(p.out + b * p.out_stride + (int64_t)h * D + d) = u32x2{w[0], w[1]};
   if (d == 0 && p.lse)
-    p.lse[(int64_t)b * p.q_heads + h] = none ? -INFINITY : (m + (log2f(l) - kLift)) * kLn2;
+    p.lse[(int64_t)b * p.q_heads + h] = none ? -INFINITY : (m + (__builtin_amdgcn_logf(l) - kLift)) * kLn2;
 }
 
 // The parts of a sequence's chunks (at parts, parts + step, ...) into its
 // output: each chunk's weight 2^(m_c - m), then the weighted rows, four
-// values per thread (the sum is a column like the others); with fewer columns
-// of four than threads the threads also share the chunks out among them.  The
-// maxima and the first rows are loaded together, so that up to eight chunks
-// cost one trip to memory.  This code runs once, by one workgroup per
-// sequence and head block, so its instructions come from memory too: it is
-// kept short by loops (unrolled to 16 parts in flight and four columns it
-// took 9 us instead of 5 for 32 chunks of 8 x 128).  `lds` holds 16
-// kMaxChunks floats.
+// values (a column) per thread and step; with fewer columns than threads the
+// threads also share the chunks out among them.  The maxima and sums and the
+// first columns are loaded together, so that up to eight chunks cost one trip
+// to memory.  This code runs once, by one workgroup per sequence and head
+// block, so its instructions come from memory too: it is kept short by loops
+// (unrolled to 16 parts in flight and three columns per thread it took 9 us
+// for 32 chunks of 6 x 128).  `lds` holds 32 kMaxChunks floats.
 template <class T, int D>
 __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, const float* parts,
                                            int64_t step, int rows, int heads, int h0, float vs,
                                            float* lds, float* lds16) {
   constexpr int kThreads = 64 * kWaves, kRows = kThreads / 16;  // threads of a head
   constexpr int kFlight = 8;                                    // a thread's parts in flight
-  constexpr int kHead = D / 4 + 1;                              // columns of a head
-  constexpr int kCols = (kHeads * kHead + kThreads - 1) / kThreads;
   const int tid = threadIdx.x, hr = tid & 15, cr = tid >> 4;
-  const int columns = heads * kHead;
+  const int columns = heads * (D / 4);
   const int share = columns >= kThreads ? 1 : kThreads / columns;  // threads per column
-  const int part_of = share > 1 ? tid / columns : 0, col0 = share > 1 ? tid % columns : tid;
+  const int part_of = share > 1 ? tid / columns : 0;
+  int col = share > 1 ? tid % columns : tid;
+  float* weight = lds;                     // [chunks][16]
+  float* sum = lds + 16 * kMaxChunks;      // [chunks][16]
 
   uint64_t a[kFlight][2];
-  auto load_flight = [&](int col, int cb) {
-    const float* x = parts + 4 * col;
+  auto load_flight = [&](int c0, int cb) {
+    const float* x = parts + 4 * c0;
 #pragma unroll
     for (int j = 0; j < kFlight; ++j) {
       const int64_t c = min(cb + j * share, it.chunks - 1);
@@ -483,70 +469,80 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
       a[j][1] = get2(x + c * step + 2);
     }
   };
-  load_flight(min(col0, columns - 1), part_of);
+  load_flight(min(col, columns - 1), part_of);
 
-  float mh = -FLT_MAX;
+  float mh = -FLT_MAX, lh = 0.0f;
 #pragma unroll 1
   for (int c = cr; c < it.chunks; c += kRows) {
-    const float m = hr < heads ? get1(parts + c * step + rows * (D + 4) + hr) : -FLT_MAX;
-    lds[c * 16 + hr] = m;
-    mh = fmaxf(mh, m);
+    const uint64_t x = get2(parts + c * step + rows * D + 2 * min(hr, heads - 1));
+    weight[c * 16 + hr] = __uint_as_float((uint32_t)x);
+    sum[c * 16 + hr] = __uint_as_float((uint32_t)(x >> 32));
+    mh = fmaxf(mh, __uint_as_float((uint32_t)x));
   }
   lds16[cr * 16 + hr] = mh;
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < kRows; ++j) mh = fmaxf(mh, lds16[j * 16 + hr]);
 #pragma unroll 1
-  for (int c = cr; c < it.chunks; c += kRows) lds[c * 16 + hr] = __builtin_amdgcn_exp2f(lds[c * 16 + hr] - mh);
+  for (int c = cr; c < it.chunks; c += kRows) {
+    const float w = __builtin_amdgcn_exp2f(weight[c * 16 + hr] - mh);
+    lh += sum[c * 16 + hr] * w;
+    weight[c * 16 + hr] = w;
+  }
+  float* heads_m = lds16 + 16 * kRows;
+  float* heads_l = heads_m + 16;
+  if (cr == 0) heads_m[hr] = mh;
+  __syncthreads();  // (every maximum is read)
+  lds16[cr * 16 + hr] = lh;
+  __syncthreads();
+  if (cr == 0) {
+    lh = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) lh += lds16[j * 16 + hr];
+    heads_l[hr] = lh;
+  }
   __syncthreads();
 
-  f32x4 o[kCols];
-#pragma unroll
-  for (int k = 0; k < kCols; ++k) o[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int k = 0; k < kCols; ++k) {
-    const int col = col0 + k * kThreads;
-    if (col >= columns || part_of >= share) continue;
-    const float* w = lds + col / kHead;
+  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  int cb = part_of;
+  const bool works = part_of < share;
 #pragma unroll 1
-    for (int cb = part_of; cb < it.chunks; cb += kFlight * share) {
-      if (k > 0 || cb != part_of) load_flight(col, cb);
+  while (works && col < columns) {
+    const float* w = weight + col / (D / 4);
+    // (a part past the last repeats it with weight 0; the select keeps an
+    // infinite value there from making a NaN)
 #pragma unroll
-      for (int j = 0; j < kFlight; ++j) {
-        const int c = cb + j * share;
-        const float wc = c < it.chunks ? w[c * 16] : 0.0f;
-        // (a part past the last repeats it, with weight 0: an infinite value
-        // there would make it NaN)
+    for (int j = 0; j < kFlight; ++j) {
+      const int c = cb + j * share;
+      const bool in = c < it.chunks;
+      const float wc = w[(in ? c : 0) * 16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float v = __uint_as_float((uint32_t)(a[j][i / 2] >> (32 * (i % 2))));
-          o[k][i] = c < it.chunks ? fmaf(v, wc, o[k][i]) : o[k][i];
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float v = __uint_as_float((uint32_t)(a[j][i / 2] >> (32 * (i % 2))));
+        o[i] = in ? fmaf(v, wc, o[i]) : o[i];
       }
     }
-  }
-  // the shares of a column, and the sums
-  __syncthreads();
-  if (part_of > 0 && part_of < share) *reinterpret_cast<f32x4*>(lds + 4 * (part_of * columns + col0)) = o[0];
-  if (cr == 0) lds16[hr] = mh;
-  __syncthreads();
-  if (part_of == 0) {
-#pragma unroll 1
-    for (int j = 1; j < share; ++j) o[0] += *reinterpret_cast<const f32x4*>(lds + 4 * (j * columns + col0));
-#pragma unroll
-    for (int k = 0; k < kCols; ++k) {
-      const int col = col0 + k * kThreads;
-      if (col < columns && col % kHead == D / 4) lds16[16 + col / kHead] = o[k][0];
+    cb += kFlight * share;
+    if (cb >= it.chunks) {
+      if (share > 1) break;
+      const int h = col / (D / 4);
+      store_out<T>(p, it.b, h0 + h, D, 4 * (col % (D / 4)), o, heads_m[h], heads_l[h], vs);
+      o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      cb = 0;
+      col += kThreads;
+      if (col >= columns) break;
     }
+    load_flight(col, cb);
   }
+  if (share == 1) return;
+  __syncthreads();  // (the sums are done with: their place takes the shares)
+  if (part_of > 0 && works) *reinterpret_cast<f32x4*>(sum + 4 * (part_of * columns + col)) = o;
   __syncthreads();
   if (part_of > 0) return;
-#pragma unroll
-  for (int k = 0; k < kCols; ++k) {
-    const int col = col0 + k * kThreads, h = col / kHead;
-    if (col >= columns || col % kHead == D / 4) continue;
-    store_out<T>(p, it.b, h0 + h, D, 4 * (col % kHead), o[k], lds16[h], lds16[16 + h], vs);
-  }
+#pragma unroll 1
+  for (int j = 1; j < share; ++j) o += *reinterpret_cast<const f32x4*>(sum + 4 * (j * columns + col));
+  const int h = col / (D / 4);
+  store_out<T>(p, it.b, h0 + h, D, 4 * (col % (D / 4)), o, heads_m[h], heads_l[h], vs);
 }
 
 // One workgroup per item: its waves take the chunk's tiles in turn, each
@@ -559,9 +555,12 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
   using V = typename TL::V;
   constexpr int PL = TL::PL;
   constexpr int RowF = D + 4;  // floats between heads in LDS
-  __shared__ __attribute__((aligned(16))) float red[kWaves][kHeads][RowF];
-  __shared__ float red_m[kWaves][kHeads], red_l[kWaves][kHeads], red_j[4 * kWaves * 16];
-  static_assert(sizeof red >= 4 * 16 * kMaxChunks && sizeof red >= 4 * 4 * 64 * kWaves, "join_parts' weights and shares");
+  // the waves' accumulators, then join_parts' weights and sums
+  constexpr int kRed = kWaves * kHeads * RowF, kJoin = 32 * kMaxChunks;
+  __shared__ __attribute__((aligned(16))) float lds[kRed > kJoin ? kRed : kJoin];
+  __shared__ float red_m[kWaves][kHeads], red_l[kWaves][kHeads], red_j[64 * kWaves + 32];
+  static_assert(4 * 64 * kWaves <= 16 * kMaxChunks, "the shares of the columns fit");
+  float(*red)[kHeads][RowF] = reinterpret_cast<float(*)[kHeads][RowF]>(lds);
   __shared__ uint32_t arrived;
 
   Item it;
@@ -727,10 +726,9 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
     if (it.chunks == 1) {
       store_out<T>(p, it.b, h0 + h, D, d, o, mh, lh, vs);
     } else {
-      float* row = part + h * (D + 4);
-      put2(row + d, o[0], o[1]);
-      put2(row + d + 2, o[2], o[3]);
-      if (d == 0) put2(row + D, lh, 0.0f), put2(row + D + 2, 0.0f, 0.0f), put1(part + rows * (D + 4) + h, mh);
+      put2(part + h * D + d, o[0], o[1]);
+      put2(part + h * D + d + 2, o[2], o[3]);
+      if (d == 0) put2(part + rows * D + 2 * h, mh, lh);
     }
   }
   if (it.chunks == 1) return;
@@ -747,7 +745,7 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
   if (arrived != (uint32_t)it.chunks - 1) return;
   if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   join_parts<T, D>(p, it, part - (int64_t)it.chunk * H * slot, H * slot, rows, heads, h0, vs,
-                   &red[0][0][0], red_j);
+                   lds, red_j);
 }
 
 // ---------------------------------------------------------------------------
