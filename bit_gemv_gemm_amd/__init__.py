@@ -30,6 +30,11 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
+try:
+    from . import _marshal
+except ImportError as e:
+    raise ImportError(f"{e}; build the package as above (its _marshal module is missing or of another torch)") from e
+
 BGG_FMT_PQ2_0 = 1
 BGG_FMT_PTQ1_0 = 2
 BGG_FMT_Q1_0 = 3
@@ -93,9 +98,8 @@ class bgg_cache_desc(ctypes.Structure):
         return "bgg_cache_desc(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
-# the argument structs of the epilogue and of the calls on a cache (field
-# order of bgg.h), packed in one go: a ctypes.Structure takes longer to fill
-# than its kernel takes to run
+# the argument structs of the epilogue and of the calls on a cache, in the
+# field order of bgg.h
 _EPILOGUE = struct.Struct("@iiPPPqq")
 _ROTARY_ARGS = struct.Struct("@iiqqqPPPPqqqqPPPfiPPPP")
 _ATTENTION_ARGS = struct.Struct("@ifqqqPPqqPPPPPPqqPPN")
@@ -322,15 +326,21 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
+# The calls below check and marshal their tensors in _marshal (C++: in Python
+# that takes longer than most of the kernels) and then call libbgg.so.
+_marshal.bind(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in (
+    "bgg_paged_attention", "bgg_rotary_append", "bgg_ternary_gemv_epilogue", "bgg_gemv_run_epilogue",
+    "bgg_ternary_gemm_epilogue")))
 
-def _run_on(dev, stream, where, call, *args):
-    """call(*args, stream) with device dev current."""
-    s = _raw_stream(dev) if stream is None else _stream(stream)
-    if _current_device() == dev:
-        st = call(*args, s)
+
+def _run_on(where, on, stream, call, *args):
+    """call(*args, stream) with the device of tensor `on` current."""
+    dev = on.get_device()
+    if dev < 0 or _current_device() == dev:
+        st = call(*args, (_raw_stream(dev) if dev >= 0 else 0) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(dev):
-            st = call(*args, s)
+            st = call(*args, _raw_stream(dev) if stream is None else _stream(stream))
     if st != 0:
         raise BggError(st, where)
 
@@ -338,76 +348,31 @@ def _run_on(dev, stream, where, call, *args):
 # ---------------------------------------------------------------------------
 # products with an epilogue
 # ---------------------------------------------------------------------------
-def _operand(t, M, N, dev, what):
-    """(pointer, stride) of epilogue operand t: float16 [M, N], rows of any
-    stride (None: 0, 0)."""
-    if t is None:
-        return 0, 0
-    if t.dtype is not torch.float16 or t.get_device() != dev or t.shape != (M, N) or (N > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what} must be float16 [{M}, {N}] with contiguous rows on device {dev}")
-    return t.data_ptr(), t.stride(0) if M > 1 else N
-
-
-def _epilogue(N, M, dev, activation, bias, mul, residual):
-    mp, ms = _operand(mul, M, N, dev, "mul")
-    rp, rs = _operand(residual, M, N, dev, "residual")
-    return _EPILOGUE.pack(ACTIVATIONS[activation] if isinstance(activation, str) else activation, 0,
-                          _vector(bias, N, torch.float16, dev, "bias"), mp, rp, ms, rs)
-
-
-def _device_of(x, y, *others):
-    """The device of y, which x and the others (or None) share; x (or None)
-    and y are float16."""
-    dev = y.get_device()
-    if y.dtype is not torch.float16 or x is not None and (x.dtype is not torch.float16 or x.get_device() != dev):
-        raise ValueError(f"x and y must be float16 on one device, y is {y.dtype} on {dev}")
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("the buffers of one call must be on one device")
-    return dev
-
-
 def bgg_ternary_gemv_epilogue(desc, packed_dev, x_dev, y_dev, M: int, flags: int, workspace, activation="none",
                               bias=None, mul=None, residual=None, stream=None) -> None:
     """y = act(W x' + bias) * mul + residual, 1 <= M <= 16 tokens; bias [N],
-    mul and residual [M, N], all float16 or None."""
-    dev, N = _device_of(x_dev, y_dev, packed_dev, workspace), desc.N
-    wsb = workspace.numel() * workspace.element_size()
-    _run_on(dev, stream, "bgg_ternary_gemv_epilogue", _lib.bgg_ternary_gemv_epilogue, desc,
-            _dev_ptr(packed_dev, desc.total_bytes, "packed"), _dev_ptr(x_dev, M * desc.K * 2, "x"),
-            _dev_ptr(y_dev, M * N * 2, "y"), M, flags, _epilogue(N, M, dev, activation, bias, mul, residual),
-            _dev_ptr(workspace, 0, "workspace"), wsb)
+    mul and residual [M, N] (rows of any stride), all float16 or None."""
+    _run_on("bgg_ternary_gemv_epilogue", y_dev, stream, _marshal.product, 0, desc, packed_dev, x_dev, y_dev, M, flags,
+            workspace, ACTIVATIONS[activation] if isinstance(activation, str) else activation, bias, mul, residual)
 
 
 def bgg_gemv_run_epilogue(desc, packed_dev, y_dev, M: int, workspace, activation="none", bias=None, mul=None,
                           residual=None, stream=None) -> None:
     """bgg_gemv_run with an epilogue (see bgg_ternary_gemv_epilogue)."""
-    dev, N = _device_of(None, y_dev, packed_dev, workspace), desc.N
-    wsb = workspace.numel() * workspace.element_size()
-    _run_on(dev, stream, "bgg_gemv_run_epilogue", _lib.bgg_gemv_run_epilogue, desc,
-            _dev_ptr(packed_dev, desc.total_bytes, "packed"), _dev_ptr(y_dev, M * N * 2, "y"), M,
-            _epilogue(N, M, dev, activation, bias, mul, residual), _dev_ptr(workspace, 0, "workspace"), wsb)
+    _run_on("bgg_gemv_run_epilogue", y_dev, stream, _marshal.product, 1, desc, packed_dev, None, y_dev, M, 0, workspace,
+            ACTIVATIONS[activation] if isinstance(activation, str) else activation, bias, mul, residual)
 
 
 def bgg_ternary_gemm_epilogue(desc, packed_dev, x_dev, y_dev, M: int, flags: int, workspace, activation="none",
                               bias=None, mul=None, residual=None, stream=None) -> None:
     """y = act(W x' + bias) * mul + residual for a prompt of M tokens."""
-    dev, N = _device_of(x_dev, y_dev, packed_dev, workspace), desc.N
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _run_on(dev, stream, "bgg_ternary_gemm_epilogue", _lib.bgg_ternary_gemm_epilogue, desc,
-            _dev_ptr(packed_dev, desc.total_bytes, "packed"), _dev_ptr(x_dev, M * desc.K * 2, "x"),
-            _dev_ptr(y_dev, M * N * 2, "y"), M, flags, _epilogue(N, M, dev, activation, bias, mul, residual),
-            _dev_ptr(workspace, 0, "workspace"), wsb)
+    _run_on("bgg_ternary_gemm_epilogue", y_dev, stream, _marshal.product, 2, desc, packed_dev, x_dev, y_dev, M, flags,
+            workspace, ACTIVATIONS[activation] if isinstance(activation, str) else activation, bias, mul, residual)
 
 
 # ---------------------------------------------------------------------------
 # the paged cache, rotary positions and attention
 # ---------------------------------------------------------------------------
-_TORCH_TYPES = {BGG_TYPE_F16: torch.float16, BGG_TYPE_BF16: torch.bfloat16,
-                BGG_TYPE_E4M3: torch.float8_e4m3fn}
-_TYPE_OF = {v: k for k, v in _TORCH_TYPES.items()}
-
-
 def bgg_cache_describe(type, pages: int, page_size: int, kv_heads: int, head_dim: int) -> bgg_cache_desc:
     d = bgg_cache_desc()
     _ok(_lib.bgg_cache_describe(TYPES[type] if isinstance(type, str) else int(type), pages, page_size, kv_heads,
@@ -430,109 +395,24 @@ def bgg_attention_workspace_size(cache: bgg_cache_desc, q_heads: int, batch: int
     return int(_lib.bgg_attention_workspace_size(ctypes.byref(cache), q_heads, batch))
 
 
-def _rows(t, rows, head_dim, dtype, dev, what):
-    """(pointer, stride, heads) of row operand t: [rows, heads * head_dim] or
-    [rows, heads, head_dim] on device dev, the values of a row side by side."""
-    if t.dtype is not dtype or t.get_device() != dev:
-        raise ValueError(f"{what} must be {dtype} on device {dev}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 2:
-        n = shape[1]
-        ok = stride[1] == 1 and n % head_dim == 0
-    else:
-        n = shape[1] * shape[2] if len(shape) == 3 else 0
-        ok = len(shape) == 3 and shape[2] == head_dim and stride[2] == 1 and (shape[1] == 1 or stride[1] == head_dim)
-    if not ok or shape[0] != rows:
-        raise ValueError(f"{what} must be [{rows}, heads * {head_dim}] with contiguous rows, got {tuple(shape)}")
-    return t.data_ptr(), stride[0] if rows > 1 else n, n // head_dim
-
-
-def _vector(t, n, dtype, dev, what):
-    """Pointer of the contiguous vector t of at least n values (None: 0)."""
-    if t is None:
-        return 0
-    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"{what} must be contiguous {dtype} on device {dev} with {n} values")
-    return t.data_ptr()
-
-
-def _cache_ptrs(cache, k_cache, v_cache, dev):
-    dt = _TORCH_TYPES[cache.type]
-    n = cache.total_bytes // dt.itemsize
-    return _vector(k_cache, n, dt, dev, "k_cache"), _vector(v_cache, n, dt, dev, "v_cache")
-
-
 def bgg_rotary_append(cache: bgg_cache_desc, k_cache, v_cache, positions, slots, freqs, q=None, q_out=None, k=None,
                       v=None, layout="half", magnitude: float = 1.0, k_scale=None, v_scale=None, stream=None) -> None:
     """Rotate q into q_out, and k and v into their slots of the cache.  The
     rotated part of a head is 2 * len(freqs) values.  q, k and v: [T, heads *
-    head_dim] (or [T, heads, head_dim]), rows of any stride."""
-    dev, D, T = positions.get_device(), cache.head_dim, positions.numel()
-    if dev < 0:
-        raise ValueError("positions must be a device tensor")
-    ref = q if q is not None else k
-    if ref is None:
-        raise ValueError("neither q nor k")
-    if (k is None) != (v is None):
-        raise ValueError("k and v come together")
-    dt = ref.dtype
-    if dt is not torch.float16 and dt is not torch.bfloat16:
-        raise ValueError(f"q, k and v must be float16 or bfloat16, not {dt}")
-    qp = qs = op = os_ = hq = kp = ks = vp = vs = kc = vc = sl = 0
-    if q is not None:
-        qp, qs, hq = _rows(q, T, D, dt, dev, "q")
-        op, os_, ho = _rows(q_out, T, D, dt, dev, "q_out")
-        if ho != hq:
-            raise ValueError("q_out must have q's heads")
-    if k is not None:
-        kp, ks, hk = _rows(k, T, D, dt, dev, "k")
-        vp, vs, hv = _rows(v, T, D, dt, dev, "v")
-        if hk != cache.kv_heads or hv != cache.kv_heads:
-            raise ValueError(f"k and v must have {cache.kv_heads} heads")
-        kc, vc = _cache_ptrs(cache, k_cache, v_cache, dev)
-        sl = _vector(slots, T, torch.int64, dev, "slots")
-    if T == 0:  # (empty tensors have no pointers)
-        return
-    args = _ROTARY_ARGS.pack(
-        _TYPE_OF[dt], ROTARY_LAYOUTS[layout] if isinstance(layout, str) else layout, 2 * freqs.numel(), T, hq, qp, op,
-        kp, vp, qs, os_, ks, vs, _vector(positions, T, torch.int32, dev, "positions"), sl,
-        _vector(freqs, 1, torch.float32, dev, "freqs"), magnitude, 0, kc, vc,
-        _vector(k_scale, cache.kv_heads, torch.float32, dev, "k_scale"),
-        _vector(v_scale, cache.kv_heads, torch.float32, dev, "v_scale"))
-    _run_on(dev, stream, "bgg_rotary_append", _lib.bgg_rotary_append, cache, args)
+    head_dim] (or [T, heads, head_dim]), rows of any stride; positions int32
+    [T]; slots int64 [T]; freqs float32."""
+    _run_on("bgg_rotary_append", positions, stream, _marshal.rotary_append, cache, k_cache, v_cache, positions, slots,
+            freqs, q, q_out, k, v, ROTARY_LAYOUTS[layout] if isinstance(layout, str) else layout, magnitude, k_scale,
+            v_scale)
 
 
 def bgg_paged_attention(cache: bgg_cache_desc, k_cache, v_cache, page_table, lengths, q, out, workspace,
                         scale: float, window: int = 0, lse=None, k_scale=None, v_scale=None, stream=None) -> None:
     """Attention of one new token per sequence.  q and out: [B, heads *
-    head_dim] (or [B, heads, head_dim]); page_table int32 [B, pages]; lengths
-    int32 [B]; lse None or float32 [B, heads]."""
-    dev, B = q.get_device(), q.shape[0]
-    if dev < 0:
-        raise ValueError("q must be a device tensor")
-    dt = q.dtype
-    if dt is not torch.float16 and dt is not torch.bfloat16:
-        raise ValueError(f"q must be float16 or bfloat16, not {dt}")
-    qp, qs, hq = _rows(q, B, cache.head_dim, dt, dev, "q")
-    op, os_, ho = _rows(out, B, cache.head_dim, dt, dev, "out")
-    if ho != hq:
-        raise ValueError("out must have q's heads")
-    kc, vc = _cache_ptrs(cache, k_cache, v_cache, dev)
-    if (page_table.dtype is not torch.int32 or page_table.get_device() != dev or page_table.dim() != 2
-            or page_table.shape[0] != B or page_table.stride(1) != 1 and page_table.shape[1] != 1):
-        raise ValueError(f"page_table must be int32 [{B}, pages] with contiguous rows on device {dev}")
-    width = page_table.shape[1]
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on device {dev}")
-    if B == 0:  # (empty tensors have no pointers)
-        return
-    args = _ATTENTION_ARGS.pack(
-        _TYPE_OF[dt], scale, B, hq, window, qp, op, qs, os_, _vector(lse, B * hq, torch.float32, dev, "lse"), kc, vc,
-        _vector(k_scale, cache.kv_heads, torch.float32, dev, "k_scale"),
-        _vector(v_scale, cache.kv_heads, torch.float32, dev, "v_scale"), page_table.data_ptr(), width,
-        page_table.stride(0) if B > 1 else width, _vector(lengths, B, torch.int32, dev, "lengths"),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _run_on(dev, stream, "bgg_paged_attention", _lib.bgg_paged_attention, cache, args)
+    head_dim] (or [B, heads, head_dim]), rows of any stride; page_table int32
+    [B, pages]; lengths int32 [B]; lse None or float32 [B, heads]."""
+    _run_on("bgg_paged_attention", q, stream, _marshal.paged_attention, cache, k_cache, v_cache, page_table, lengths, q,
+            out, workspace, scale, window, lse, k_scale, v_scale)
 
 
 # ---------------------------------------------------------------------------
