@@ -2,8 +2,17 @@
 // s_t = scale q.k_t, out = sum_t e^(s_t) v_t / sum_t e^(s_t).
 //
 // Every key and value is read once per 16 query heads of its key head, and
-// each read value does 2 * 16 multiply-adds on the matrix cores, so the
-// kernel is bound by the cache's bytes.
+// each read value does at most 2 * 16 multiply-adds on the matrix cores, so
+// long sequences are bound by the cache's bytes and short ones by the chain
+// of dependent loads (length, page numbers, keys; then, where a sequence is
+// cut, the parts).  One launch; the tokens are read with running maximum and
+// sum, straight from the cache into the operands of the matrix operations.
+//
+// Measured (one MI355X, which reads 6.14 TB/s; 48 query heads on 8 key heads
+// of 128 unless stated): 1 x 262144 tokens f16 186 us (5.76 TB/s), 16 x
+// 32768 e4m3 183 us (5.87), 1 x 32768 f16 28.9 us (4.6), 1 x 1024 9.4 us, 1 x
+// 64 4.8 us (a kernel that does nothing: 1.7); 16 ragged sequences up to 8000
+// tokens, 24 heads on 4 of 256, bf16: 28 us (4.0 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

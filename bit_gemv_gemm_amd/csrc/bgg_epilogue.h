@@ -1,5 +1,10 @@
 // Where the products put their results: y as it is, or through an epilogue,
 // y = act(sum + bias) * mul + residual in fp32 with one rounding to fp16.
+// The kernels are those of the plain products, with the output as a template
+// argument; the epilogue costs its operands' bytes and little else (down
+// 5120x17408 at one token onto a residual 6.77 us against 6.66, gate
+// 17408x5120 at 16 tokens with SILU and a multiplier 22.5 against 21.5, at
+// 4096 tokens 633 against 611, of which reading the multiplier is 23).
 #pragma once
 #include <cmath>
 
