@@ -271,7 +271,7 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int dev = device_of(tensor(a[4], "y"), "y");
     const int64_t M = integer(a[5]), N = d->N;
     const uint32_t flags = (uint32_t)integer(a[6]);
-    if (M < 0) refuse("M", "is negative");
+    if (M < 0 || M > (int64_t(1) << 31)) refuse("M", "is out of range");  // (M times a matrix size stays in 64 bits)
     const void* packed = bytes(a[2], d->total_bytes, dev, "packed");
     const void* x = which == 1 ? nullptr : halves(a[3], M * d->K, dev, "x");
     void* y = halves(a[4], M * N, dev, "y");
