@@ -60,19 +60,23 @@ struct EpilogueOut {
     if (residual) o.residual = residual[m * residual_stride + n];
     return o;
   }
-  __device__ __forceinline__ float value(float v, const Operands& o) const {
+  template <int ACT>
+  __device__ __forceinline__ float value_of(float v, const Operands& o) const {
     if (bias) v += h2f(o.bias);
-    switch (act) {
-      case BGG_ACT_RELU: v = activate<BGG_ACT_RELU>(v); break;
-      case BGG_ACT_RELU2: v = activate<BGG_ACT_RELU2>(v); break;
-      case BGG_ACT_SILU: v = activate<BGG_ACT_SILU>(v); break;
-      case BGG_ACT_GELU: v = activate<BGG_ACT_GELU>(v); break;
-      case BGG_ACT_GELU_TANH: v = activate<BGG_ACT_GELU_TANH>(v); break;
-      default: break;
-    }
+    v = activate<ACT>(v);
     if (mul) v *= h2f(o.mul);
     if (residual) v += h2f(o.residual);
     return v;
+  }
+  __device__ __forceinline__ float value(float v, const Operands& o) const {
+    switch (act) {
+      case BGG_ACT_RELU: return value_of<BGG_ACT_RELU>(v, o);
+      case BGG_ACT_RELU2: return value_of<BGG_ACT_RELU2>(v, o);
+      case BGG_ACT_SILU: return value_of<BGG_ACT_SILU>(v, o);
+      case BGG_ACT_GELU: return value_of<BGG_ACT_GELU>(v, o);
+      case BGG_ACT_GELU_TANH: return value_of<BGG_ACT_GELU_TANH>(v, o);
+      default: return value_of<BGG_ACT_NONE>(v, o);
+    }
   }
   __device__ __forceinline__ void store(int64_t m, int64_t n, float v, const Operands& o) const {
     y[m * N + n] = f2h(value(v, o));

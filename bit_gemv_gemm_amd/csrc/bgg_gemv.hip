@@ -1033,19 +1033,32 @@ __device__ __forceinline__ void mx_gemv_body(const uint8_t* __restrict__ packed,
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       red[wave][(4 * kg + e) * kMmaRedStride + 16 * rb + col] = acc[rb][e];
+  // (an epilogue's operands, in flight over the barrier)
+  constexpr int kMine = kMmaSlots * kTile / (64 * W);
+  typename Out::Operands o[kMine];
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int t = W * k + wave;
+    if (t < Mreal && tile * kTile + lane < N) o[k] = out.load(t, tile * kTile + lane);
+  }
   __syncthreads();
-  for (int it = threadIdx.x; it < kMmaSlots * kTile; it += 64 * W) {
-    const int t = it >> 6, r = it & 63;
-    if (t >= Mreal) break;  // t only grows with it
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int t = W * k + wave, r = lane;
+    if (t >= Mreal) break;
     float v = red[0][t * kMmaRedStride + r];
 #pragma unroll
     for (int q = 1; q < W; ++q) v += red[q][t * kMmaRedStride + r];
     const int64_t row = tile * kTile + r;
+    if (row >= N) break;
     if (ws.Sg == 1) {
-      if (row < N) out.store(t, row, v, out.load(t, row));
+      out.store(t, row, v, o[k]);
       continue;
     }
-    if (row < N) add_partial(row_words_of(sums), t, ws.local * kTile + r, ws.Sg, v, out, row);
+    const RowWords rw = row_words_of(sums);
+    const uint64_t term = partial_term(rw, t, ws.local * kTile + r, v);
+    const uint64_t old = arrive(rw, t, ws.local * kTile + r, term);
+    finish_row(rw, t, ws.local * kTile + r, ws.Sg, old, term, out, row, o[k]);
   }
 }
 
@@ -1221,19 +1234,32 @@ __device__ __forceinline__ void gemv_ptq1_mx_body(
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       red[wave * kRedWave + (4 * kg + e) * kMmaRedStride + 16 * rb + col] = acc[rb][e];
+  // (an epilogue's operands, in flight over the barrier)
+  constexpr int kMine = kMmaSlots * kTile / (64 * W);
+  typename Out::Operands o[kMine];
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int t = W * k + wave;
+    if (t < Mreal && tile * kTile + lane < N) o[k] = out.load(t, tile * kTile + lane);
+  }
   __syncthreads();
-  for (int it = threadIdx.x; it < kMmaSlots * kTile; it += 64 * W) {
-    const int t = it >> 6, r = it & 63;
-    if (t >= Mreal) break;  // t only grows with it
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int t = W * k + wave, r = lane;
+    if (t >= Mreal) break;
     float v = red[t * kMmaRedStride + r];
 #pragma unroll
     for (int q = 1; q < W; ++q) v += red[q * kRedWave + t * kMmaRedStride + r];
     const int64_t row = tile * kTile + r;
+    if (row >= N) break;
     if (ws.Sg == 1) {
-      if (row < N) out.store(t, row, v, out.load(t, row));
+      out.store(t, row, v, o[k]);
       continue;
     }
-    if (row < N) add_partial(row_words_of(sums), t, ws.local * kTile + r, ws.Sg, v, out, row);
+    const RowWords rw = row_words_of(sums);
+    const uint64_t term = partial_term(rw, t, ws.local * kTile + r, v);
+    const uint64_t old = arrive(rw, t, ws.local * kTile + r, term);
+    finish_row(rw, t, ws.local * kTile + r, ws.Sg, old, term, out, row, o[k]);
   }
 }
 template <int W>
