@@ -186,14 +186,22 @@ __device__ __forceinline__ void wide_epilogue(const f32x16 (&acc)[4][2], float* 
   }
 }
 
-template <class Out>
+// MI: 32-token blocks of the tile.  Four, and as few as hold the tokens for
+// prompts of up to 96, whose time went into reading, multiplying and waiting
+// for rows that are not there: 17408x5120 (PQ2_0, MI against four) 32 tokens
+// 19.3 / 31.6 us, 64 tokens 25.4 / 34.0, 96 tokens 32.8 / 37.3.  A row's
+// operations do not depend on the others: the same sums, bit for bit.  Short
+// tiles store a value at a time also with an epilogue (a tile moved through
+// LDS would raise the register count and the code of prompts that store
+// little).
+template <int MI, class Out>
 __device__ __forceinline__ void gemm_pq2_body(
     const uint16_t* __restrict__ X, const uint8_t* __restrict__ packed,
                const uint16_t* __restrict__ scales, int64_t M, int64_t N, int64_t K, int64_t C,
                int64_t G,
                int64_t NT, int64_t kmid, float* __restrict__ P, const Out& out) {
-  __shared__ __attribute__((aligned(16))) uint4 As0[kBM * 16];
-  __shared__ __attribute__((aligned(16))) uint4 As1[kBM * 16];
+  __shared__ __attribute__((aligned(16))) uint4 As0[MI * 32 * 16];
+  __shared__ __attribute__((aligned(16))) uint4 As1[MI * 32 * 16];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -201,12 +209,12 @@ __device__ __forceinline__ void gemm_pq2_body(
   const int64_t m0 = (int64_t)blockIdx.y * kBM, n0 = (int64_t)blockIdx.x * kBN;
 
   // activation loader: load instruction i of this wave fills slots
-  // (8 wave + i) * 64 + lane, i.e. row (8 wave + i) * 4 + lane / 16, piece
+  // (2 MI wave + i) * 64 + lane, i.e. row (2 MI wave + i) * 4 + lane / 16, piece
   // (lane % 16) ^ (row & 15); rows past M re-read row M-1 (never stored)
-  const uint16_t* a_src[8];
+  const uint16_t* a_src[2 * MI];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = (8 * wave + i) * 4 + (lane >> 4);
+  for (int i = 0; i < 2 * MI; ++i) {
+    const int r = (2 * MI * wave + i) * 4 + (lane >> 4);
     const int q = (lane & 15) ^ (r & 15);
     const int64_t am = m0 + r < M ? m0 + r : M - 1;
     a_src[i] = X + am * K + 8 * q;
@@ -221,9 +229,9 @@ __device__ __forceinline__ void gemm_pq2_body(
   const uint4* b_src = reinterpret_cast<const uint4*>(packed) + tcl * C * kTileRows + li;
   const uint16_t* s_src = scales + tcl * G * kTileRows + li;
 
-  f32x16 acc[4][2];
+  f32x16 acc[MI][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -244,10 +252,10 @@ __device__ __forceinline__ void gemm_pq2_body(
   uint16_t s0, s1;
 #define BGG_LOAD_A(KS, BUF)                                                   \
   do {                                                                        \
-    _Pragma("unroll") for (int i = 0; i < 8; ++i)                             \
+    _Pragma("unroll") for (int i = 0; i < 2 * MI; ++i)                        \
       __builtin_amdgcn_global_load_lds(                                       \
           a_src[i] + (KS) * 128,                                              \
-          (__attribute__((address_space(3))) void*)&BUF[(8 * wave + i) * 64], \
+          (__attribute__((address_space(3))) void*)&BUF[(2 * MI * wave + i) * 64], \
           16, 0, 0);                                                          \
   } while (0)
 #define BGG_LOAD_B(KS)                                                        \
@@ -266,8 +274,8 @@ __device__ __forceinline__ void gemm_pq2_body(
     BGG_LOAD_B((KS) + 1);                                                     \
     __builtin_amdgcn_sched_barrier(0);                                        \
     _Pragma("unroll") for (int kk = 0; kk < 8; ++kk) {                        \
-      f16x8 a[4], b[2];                                                       \
-      _Pragma("unroll") for (int i = 0; i < 4; ++i) a[i] =                    \
+      f16x8 a[MI], b[2];                                                      \
+      _Pragma("unroll") for (int i = 0; i < MI; ++i) a[i] =                   \
           *reinterpret_cast<const f16x8*>(&CUR[a_slot(i * 32 + li, 2 * kk + h)]); \
       _Pragma("unroll") for (int j = 0; j < 2; ++j) {                         \
         const uint4 c_ = bw[kk >> 2][j];                                      \
@@ -275,7 +283,7 @@ __device__ __forceinline__ void gemm_pq2_body(
         const uint32_t w_ = k4_ == 0 ? c_.x : k4_ == 1 ? c_.y : k4_ == 2 ? c_.z : c_.w; \
         b[j] = decode8_pq2(w_, 16 * h, tb[j]);                                \
       }                                                                       \
-      _Pragma("unroll") for (int i = 0; i < 4; ++i)                           \
+      _Pragma("unroll") for (int i = 0; i < MI; ++i)                          \
           _Pragma("unroll") for (int j = 0; j < 2; ++j) acc[i][j] =            \
           __builtin_amdgcn_mfma_f32_32x32x16_f16(a[i], b[j], acc[i][j], 0, 0, 0); \
     }                                                                         \
@@ -296,14 +304,14 @@ __device__ __forceinline__ void gemm_pq2_body(
 #undef BGG_STEP
 
   if (!w_ok) return;
-  if constexpr (std::is_same<Out, bgg::EpilogueOut>::value) {
+  if constexpr (MI == 4 && std::is_same<Out, bgg::EpilogueOut>::value) {
     if (out.wide && gridDim.z == 1) {  // (every wave is past its last read of As0: the steps' barrier)
       wide_epilogue(acc, reinterpret_cast<float*>(As0) + wave * 2048, lane, m0, tw * kTileRows, M, out);
       return;
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       store_block(acc[i][j], m0 + i * 32 + 4 * h, tw * kTileRows + j * 32 + li, M, N, P, out);
@@ -314,14 +322,31 @@ __global__ void __launch_bounds__(256, 2)
                const uint16_t* __restrict__ scales, int64_t M, int64_t N, int64_t K, int64_t C,
                int64_t G,
                int64_t NT, int64_t kmid, float* __restrict__ P, uint16_t* __restrict__ Y) {
-  gemm_pq2_body(X, packed, scales, M, N, K, C, G, NT, kmid, P, bgg::PlainOut{Y, N});
+  gemm_pq2_body<4>(X, packed, scales, M, N, K, C, G, NT, kmid, P, bgg::PlainOut{Y, N});
 }
 __global__ void __launch_bounds__(256, 2)
     k_gemm_pq2_ep(const uint16_t* __restrict__ X, const uint8_t* __restrict__ packed,
                const uint16_t* __restrict__ scales, int64_t M, int64_t N, int64_t K, int64_t C,
                int64_t G,
                int64_t NT, int64_t kmid, float* __restrict__ P, bgg::EpilogueOut out) {
-  gemm_pq2_body(X, packed, scales, M, N, K, C, G, NT, kmid, P, out);
+  gemm_pq2_body<4>(X, packed, scales, M, N, K, C, G, NT, kmid, P, out);
+}
+// up to 32 MI tokens
+template <int MI>
+__global__ void __launch_bounds__(256, 2)
+    k_gemm_pq2_short(const uint16_t* __restrict__ X, const uint8_t* __restrict__ packed,
+               const uint16_t* __restrict__ scales, int64_t M, int64_t N, int64_t K, int64_t C,
+               int64_t G,
+               int64_t NT, int64_t kmid, float* __restrict__ P, uint16_t* __restrict__ Y) {
+  gemm_pq2_body<MI>(X, packed, scales, M, N, K, C, G, NT, kmid, P, bgg::PlainOut{Y, N});
+}
+template <int MI>
+__global__ void __launch_bounds__(256, 2)
+    k_gemm_pq2_short_ep(const uint16_t* __restrict__ X, const uint8_t* __restrict__ packed,
+               const uint16_t* __restrict__ scales, int64_t M, int64_t N, int64_t K, int64_t C,
+               int64_t G,
+               int64_t NT, int64_t kmid, float* __restrict__ P, bgg::EpilogueOut out) {
+  gemm_pq2_body<MI>(X, packed, scales, M, N, K, C, G, NT, kmid, P, out);
 }
 
 // The sums P[0] + P[1] + ... of V values at src (partials MN values apart),
@@ -766,6 +791,13 @@ GemmPlan gemm_plan(const bgg_weights_desc* d, int64_t M, bool rotate, uint64_t a
   return p;
 }
 
+// The PQ2_0 kernel of M tokens: the fewest 32-token blocks that hold them
+// (gemm_pq2_body has the times of both sides), or the 128-token tile.
+template <class K>
+K kernel_for(int64_t M, K whole, K one, K two, K three) {
+  return M <= 32 ? one : M <= 64 ? two : M <= 96 ? three : whole;
+}
+
 bgg_status ternary_gemm(const char* who, const bgg_weights_desc* d, const void* packed_dev, const void* x_dev,
                         void* y_dev, int64_t M, uint32_t flags, const bgg::EpilogueOut* ep,
                         void* workspace, size_t workspace_bytes, void* stream) {
@@ -823,11 +855,14 @@ bgg_status ternary_gemm(const char* who, const bgg_weights_desc* d, const void* 
       out.y = y;
       if (out.mul) out.mul += m0 * out.mul_stride;
       if (out.residual) out.residual += m0 * out.residual_stride;
-      hipLaunchKernelGGL(pq2 ? k_gemm_pq2_ep : k_gemm_ptq1_ep, grid, dim3(256), 0, s,
+      hipLaunchKernelGGL(pq2 ? kernel_for(M, k_gemm_pq2_ep, k_gemm_pq2_short_ep<1>, k_gemm_pq2_short_ep<2>,
+                                          k_gemm_pq2_short_ep<3>)
+                             : k_gemm_ptq1_ep, grid, dim3(256), 0, s,
                          (const uint16_t*)xr + m0 * d->K, wts, scales, mc, d->N, d->K, C, d->groups,
                          d->row_tiles, kmid, P, out);
     } else {
-      hipLaunchKernelGGL(pq2 ? k_gemm_pq2 : k_gemm_ptq1, grid, dim3(256), 0, s,
+      hipLaunchKernelGGL(pq2 ? kernel_for(M, k_gemm_pq2, k_gemm_pq2_short<1>, k_gemm_pq2_short<2>, k_gemm_pq2_short<3>)
+                             : k_gemm_ptq1, grid, dim3(256), 0, s,
                          (const uint16_t*)xr + m0 * d->K, wts, scales, mc, d->N, d->K, C, d->groups,
                          d->row_tiles, kmid, P, y);
     }

@@ -144,6 +144,30 @@ def test_gemm_sizes(fmt, M, N, K, pad):
         assert torch.all(guard[:256] == 7.0) and torch.all(guard[-256:] == 7.0)
 
 
+@pytest.mark.parametrize("fmt", ["PQ2_0", "PTQ1_0"])
+@pytest.mark.parametrize("M", [17, 31, 32, 33, 63, 64, 65, 95, 96, 97, 127, 128])
+def test_prompts_of_one_tile(fmt, M):
+    """Every height of the product's tile, split with an epilogue and unsplit
+    without; a token's sums do not depend on how many come with it."""
+    N, K = 333, 1408
+    c = Case(fmt, N, K, M)
+    c.check(c.run("silu", how="gemm"), "silu")
+    # the same tokens and more, K in one range in both: PQ2_0 without a
+    # workspace, PTQ1_0 with one that holds the weights rewritten and no more
+    ws = None if fmt == "PQ2_0" else bgg.workspace(c.d.row_tiles * 64 * K // 4)
+    more = torch.cat([c.x_d, torch.zeros((128 - M, K), dtype=torch.float16, device="cuda")])
+    got = []
+    for x in (c.x_d, more):
+        guard = torch.full((len(x) * N + 512,), 7.0, dtype=torch.float16, device="cuda")
+        y = guard[256:256 + len(x) * N].view(len(x), N)
+        y.fill_(float("nan"))
+        bgg.bgg_ternary_gemm(c.d, c.packed, x, y, len(x), 0, ws)
+        torch.cuda.synchronize()
+        assert torch.all(guard[:256] == 7.0) and torch.all(guard[-256:] == 7.0)
+        got.append(y[:M])
+    assert torch.equal(*got)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("which", ["b", "m", "r", "bmr"])
 def test_wide_rows_with_every_activation(act, which):
