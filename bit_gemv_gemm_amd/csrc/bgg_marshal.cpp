@@ -82,6 +82,7 @@ struct Rows {
 };
 // [rows, heads * dim] or [rows, heads, dim], the values of a row side by side.
 Rows rows(PyObject* o, int64_t n, int64_t dim, at::ScalarType type, int dev, const char* what) {
+  if (dim < 1) refuse("cache", "describes no valid cache");  // (a descriptor nobody filled; the library checks the rest)
   const at::Tensor& t = tensor(o, what);
   if (!t.is_cuda() || t.get_device() != dev) refuse(what, "must be on the device of the call's other tensors");
   if (t.scalar_type() != type) refuse(what, "has the wrong type");

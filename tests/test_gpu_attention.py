@@ -451,3 +451,20 @@ def test_binding_refusals():
             call(i, x, **kw)
     bgg.bgg_paged_attention(d.d, d.k, d.v, d.table[:0], d.n[:0], d.q[:0], d.out[:0], d.ws, scale=0.1)
     torch.cuda.synchronize()
+
+
+def test_unfilled_descriptors_are_refused():
+    """A descriptor that bgg_cache_describe never filled (a head dimension of
+    zero), or one changed afterwards, is an error."""
+    d = Device(case([20, 30], seed=2))
+    T = len(d.q)
+    pos, slots = torch.zeros(T, dtype=torch.int32, device="cuda"), torch.zeros(T, dtype=torch.int64, device="cuda")
+    freqs = torch.ones(d.d.head_dim // 2, device="cuda")
+    changed = bgg.bgg_cache_desc.from_buffer_copy(d.d)
+    changed.page_size *= 2
+    for c, error in ((bgg.bgg_cache_desc(), ValueError), (changed, bgg.BggError)):
+        with pytest.raises(error):
+            bgg.bgg_paged_attention(c, d.k, d.v, d.table, d.n, d.q, d.out, d.ws, scale=0.1)
+        with pytest.raises(error):
+            bgg.bgg_rotary_append(c, None, None, pos, slots, freqs, q=d.q, q_out=torch.empty_like(d.q))
+    torch.cuda.synchronize()
