@@ -4,12 +4,15 @@ Every function has the name of the C entry point it calls.  Host buffers are
 numpy arrays; device buffers are torch tensors on the ROCm device (PyTorch is
 used for device memory and streams, nothing else).  A non-OK status raises
 BggError carrying the library's message.  There is no fallback: if
-libbgg.so is missing, importing this package fails.
+libbgg.so is missing, importing this package fails; without the module that
+marshals the decoder-layer calls (_marshal, built against one torch) those
+calls raise ImportError, and the others, which need libbgg.so alone, work.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import re
 import struct
 
 import numpy as np
@@ -30,10 +33,27 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
+
+class _Missing:
+    """Stands for the marshalling module that could not be taken: any use
+    raises an ImportError with the reason."""
+
+    def __init__(self, why):
+        self.why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"the _marshal module of {__name__} is needed for this call: {self.why}; build it with "
+                          "`python -c 'import __graft_entry__ as g; g.build()'` or `python bit_gemv_gemm_amd/build.py`")
+
+
 try:
     from . import _marshal
+    # (it reads torch's tensors through that torch's own headers)
+    _built_with = getattr(_marshal, "torch_version", "?")
+    if _built_with != re.match(r"[\d.]*", torch.__version__)[0]:
+        _marshal = _Missing(f"it was built with torch {_built_with}, this is {torch.__version__}")
 except ImportError as e:
-    raise ImportError(f"{e}; build the package as above (its _marshal module is missing or of another torch)") from e
+    _marshal = _Missing(str(e))
 
 BGG_FMT_PQ2_0 = 1
 BGG_FMT_PTQ1_0 = 2
@@ -328,9 +348,10 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 
 # The calls below check and marshal their tensors in _marshal (C++: in Python
 # that takes longer than most of the kernels) and then call libbgg.so.
-_marshal.bind(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in (
-    "bgg_paged_attention", "bgg_rotary_append", "bgg_ternary_gemv_epilogue", "bgg_gemv_run_epilogue",
-    "bgg_ternary_gemm_epilogue")))
+if not isinstance(_marshal, _Missing):
+    _marshal.bind(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in (
+        "bgg_paged_attention", "bgg_rotary_append", "bgg_ternary_gemv_epilogue", "bgg_gemv_run_epilogue",
+        "bgg_ternary_gemm_epilogue")))
 
 
 def _run_on(where, on, stream, call, *args):

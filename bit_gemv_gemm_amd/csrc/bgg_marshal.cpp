@@ -5,6 +5,7 @@
 // No arithmetic and no GPU work of its own.
 #include <Python.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <exception>
 
@@ -318,4 +319,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__marshal() {
+  PyObject* m = PyModule_Create(&module);
+  // the torch whose tensors this code can read
+  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION)) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
