@@ -430,16 +430,18 @@ __device__ __forceinline__ uint64_t get2(const float* p) {
   return __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Values d .. d + 3 of query head h: the accumulator over the sum, rounded.
+// Values d .. d + 3 of query head h: the accumulator over the sum, rounded
+// (0 where no score was above -inf, also if the values there were NaN or inf
+// and the accumulator is NaN).
 template <class T>
 __device__ __forceinline__ void store_out(const AttnParams& p, int b, int h, int D, int d, f32x4 o, float m,
                                           float l, float vs) {
   const bool none = l == 0.0f;
-  const float f = none ? 0.0f : vs / l;
+  const float f = vs / l;
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    w[i] = (uint32_t)T::bits(o[2 * i] * f) | ((uint32_t)T::bits(o[2 * i + 1] * f) << 16);
+    w[i] = none ? 0u : (uint32_t)T::bits(o[2 * i] * f) | ((uint32_t)T::bits(o[2 * i + 1] * f) << 16);
   *reinterpret_cast<u32x2*>(p.out + b * p.out_stride + (int64_t)h * D + d) = u32x2{w[0], w[1]};
   if (d == 0 && p.lse)
     p.lse[(int64_t)b * p.q_heads + h] = none ? -INFINITY : (m + (__builtin_amdgcn_logf(l) - kLift)) * kLn2;
