@@ -226,6 +226,9 @@ struct Mma;
 template <>
 struct Mma<F16> {
   using op = f16x8;
+  // a probability is at most 2^(7 + kSlack) = 2^15, inside fp16, and fp16's
+  // subnormals begin at 2^-21 of the maximum
+  static constexpr float lift = 7.0f;
   static __device__ __forceinline__ f32x4 mul(op a, op b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
   }
@@ -247,6 +250,9 @@ struct Mma<F16> {
 template <>
 struct Mma<BF16> {
   using op = bf16x8;
+  // a probability is at most 1, so that the largest bfloat16 values stay
+  // inside fp32
+  static constexpr float lift = -8.0f;
   static __device__ __forceinline__ f32x4 mul(op a, op b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
@@ -404,10 +410,9 @@ struct Tile {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // A maximum is raised only where a score passes it by more than kSlack (in
 // powers of two), so most tiles need no lane moves and no rescaling.
-// Probabilities are kept 2^kLift times their value: at most 2^(kLift +
-// kSlack) = 2^15, inside fp16, and its subnormals begin at 2^-21 of the
-// maximum.
-constexpr float kSlack = 8.0f, kLift = 7.0f;
+// Probabilities are kept 2^lift times their value, at most 2^(lift + kSlack)
+// (Mma::lift).
+constexpr float kSlack = 8.0f;
 
 // Floats of a part: rows of D accumulators, then each row's maximum and sum.
 __host__ __device__ constexpr int64_t part_floats(int64_t rows, int64_t D) {
@@ -433,7 +438,7 @@ __device__ __forceinline__ uint64_t get2(const float* p) {
 // Values d .. d + 3 of query head h: the accumulator over the sum, rounded
 // (0 where no score was above -inf, also if the values there were NaN or inf
 // and the accumulator is NaN).
-template <class T>
+template <class T, class V>
 __device__ __forceinline__ void store_out(const AttnParams& p, int b, int h, int D, int d, f32x4 o, float m,
                                           float l, float vs) {
   const bool none = l == 0.0f;
@@ -444,7 +449,7 @@ __device__ __forceinline__ void store_out(const AttnParams& p, int b, int h, int
     w[i] = none ? 0u : (uint32_t)T::bits(o[2 * i] * f) | ((uint32_t)T::bits(o[2 * i + 1] * f) << 16);
   *reinterpret_cast<u32x2*>(p.out + b * p.out_stride + (int64_t)h * D + d) = u32x2{w[0], w[1]};
   if (d == 0 && p.lse)
-    p.lse[(int64_t)b * p.q_heads + h] = none ? -INFINITY : (m + (__builtin_amdgcn_logf(l) - kLift)) * kLn2;
+    p.lse[(int64_t)b * p.q_heads + h] = none ? -INFINITY : (m + (__builtin_amdgcn_logf(l) - Mma<V>::lift)) * kLn2;
 }
 
 // The parts of a sequence's chunks (at parts, parts + step, ...) into its
@@ -456,7 +461,7 @@ __device__ __forceinline__ void store_out(const AttnParams& p, int b, int h, int
 // block, so its instructions come from memory too: it is kept short by loops
 // (unrolled to 16 parts in flight and three columns per thread it took 9 us
 // for 32 chunks of 6 x 128).  `lds` holds 32 kMaxChunks floats.
-template <class T, int D>
+template <class T, class V, int D>
 __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, const float* parts,
                                            int64_t step, int rows, int heads, int h0, float vs,
                                            float* lds, float* lds16) {
@@ -537,7 +542,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
     if (cb >= it.chunks) {
       if (share > 1) break;
       const int h = col / (D / 4);
-      store_out<T>(p, it.b, h0 + h, D, 4 * (col % (D / 4)), o, heads_m[h], heads_l[h], vs);
+      store_out<T, V>(p, it.b, h0 + h, D, 4 * (col % (D / 4)), o, heads_m[h], heads_l[h], vs);
       o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       cb = 0;
       col += kThreads;
@@ -553,7 +558,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
 #pragma unroll 1
   for (int j = 1; j < share; ++j) o += *reinterpret_cast<const f32x4*>(sum + 4 * (j * columns + col));
   const int h = col / (D / 4);
-  store_out<T>(p, it.b, h0 + h, D, 4 * (col % (D / 4)), o, heads_m[h], heads_l[h], vs);
+  store_out<T, V>(p, it.b, h0 + h, D, 4 * (col % (D / 4)), o, heads_m[h], heads_l[h], vs);
 }
 
 // One workgroup per item: its waves take the chunk's tiles in turn, each
@@ -683,7 +688,7 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
     float pr[8], rest[8], none[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      pr[e] = __builtin_amdgcn_exp2f(x[e] - m + kLift);
+      pr[e] = __builtin_amdgcn_exp2f(x[e] - m + Mma<V>::lift);
       l += pr[e];
     }
     const typename Mma<V>::op hi = Mma<V>::split(pr, rest), lo = Mma<V>::split(rest, none);
@@ -735,7 +740,7 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
       o += *reinterpret_cast<const f32x4*>(&red[w][h][d]);
     }
     if (it.chunks == 1) {
-      store_out<T>(p, it.b, h0 + h, D, d, o, mh, lh, vs);
+      store_out<T, V>(p, it.b, h0 + h, D, d, o, mh, lh, vs);
     } else {
       put2(part + h * D + d, o[0], o[1]);
       put2(part + h * D + d + 2, o[2], o[3]);
@@ -755,7 +760,7 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
   __syncthreads();
   if (arrived != (uint32_t)it.chunks - 1) return;
   if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  join_parts<T, D>(p, it, part - (int64_t)it.chunk * H * slot, H * slot, rows, heads, h0, vs,
+  join_parts<T, V, D>(p, it, part - (int64_t)it.chunk * H * slot, H * slot, rows, heads, h0, vs,
                    lds, red_j);
 }
 
