@@ -435,6 +435,56 @@ __device__ __forceinline__ uint64_t get2(const float* p) {
   return __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// Infinite values.  A visible one makes its element infinite (NaN where both
+// signs or a NaN meet), but times a 16-bit term that is zero or negative, or
+// a weight that has become zero, it is NaN.  So an element that came out NaN
+// from scores that are numbers is decided again, from the infinite and NaN
+// values alone: their sum is what the element is.  (1 x 500 tokens: 9.10 us
+// without, 9.28 with the pass over the values inlined among the code that
+// every launch fetches, 9.15 with it called.)
+__device__ __forceinline__ bool any_nan(const f32x4& o) {
+  return __builtin_isunordered(o[0], o[1]) | __builtin_isunordered(o[2], o[3]);
+}
+__device__ __forceinline__ float not_finite(float v) { return fabsf(v) < INFINITY ? 0.0f : v; }
+__device__ __forceinline__ void take_infinite(f32x4& o, const f32x4& s) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (o[i] != o[i] && fabsf(s[i]) == INFINITY) o[i] = s[i];
+}
+// Values d .. d + 3 of the visible tokens first .. end - 1 (16-bit caches:
+// E4M3 has no infinity), by one thread.
+template <class C, int D>
+__device__ __attribute__((noinline)) f32x4 infinite_values(const int32_t* table, const uint16_t* v_cache, int pages,
+                                                           int kv_heads, int kh, int page_shift, int first, int end,
+                                                           int d) {
+  f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+  for (int t = first; t < end; ++t) {
+    const int page = table[t >> page_shift];
+    if (page < 0 || page >= pages) continue;
+    const int64_t cell = (((int64_t)page * kv_heads + kh) << page_shift) + (t & ((1 << page_shift) - 1));
+    const u32x2 v = *reinterpret_cast<const u32x2*>(v_cache + cell * D + d);
+    s[0] += not_finite(C::value((uint16_t)v.x));
+    s[1] += not_finite(C::value((uint16_t)(v.x >> 16)));
+    s[2] += not_finite(C::value((uint16_t)v.y));
+    s[3] += not_finite(C::value((uint16_t)(v.y >> 16)));
+  }
+  return s;
+}
+// Four accumulators of every part of a sequence.
+__device__ __forceinline__ f32x4 infinite_parts(const float* at, int64_t step, int chunks) {
+  f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    const uint64_t a = get2(at + c * step), b = get2(at + c * step + 2);
+    s[0] += not_finite(__uint_as_float((uint32_t)a));
+    s[1] += not_finite(__uint_as_float((uint32_t)(a >> 32)));
+    s[2] += not_finite(__uint_as_float((uint32_t)b));
+    s[3] += not_finite(__uint_as_float((uint32_t)(b >> 32)));
+  }
+  return s;
+}
+
 // Values d .. d + 3 of query head h: the accumulator over the sum, rounded
 // (0 where no score was above -inf, also if the values there were NaN or inf
 // and the accumulator is NaN).
@@ -519,6 +569,16 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
   }
   __syncthreads();
 
+  // the column of the output, its shares added
+  auto store_column = [&](f32x4 o) {
+    const int h = col / (D / 4);
+    if (__builtin_expect(__any(any_nan(o)), false)) {
+      const f32x4 inf = infinite_parts(parts + 4 * col, step, it.chunks);
+      if (heads_l[h] == heads_l[h]) take_infinite(o, inf);
+    }
+    store_out<T, V>(p, it.b, h0 + h, D, 4 * (col % (D / 4)), o, heads_m[h], heads_l[h], vs);
+  };
+
   f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
   int cb = part_of;
   const bool works = part_of < share;
@@ -541,8 +601,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
     cb += kFlight * share;
     if (cb >= it.chunks) {
       if (share > 1) break;
-      const int h = col / (D / 4);
-      store_out<T, V>(p, it.b, h0 + h, D, 4 * (col % (D / 4)), o, heads_m[h], heads_l[h], vs);
+      store_column(o);
       o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       cb = 0;
       col += kThreads;
@@ -557,8 +616,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
   if (part_of > 0) return;
 #pragma unroll 1
   for (int j = 1; j < share; ++j) o += *reinterpret_cast<const f32x4*>(sum + 4 * (j * columns + col));
-  const int h = col / (D / 4);
-  store_out<T, V>(p, it.b, h0 + h, D, 4 * (col % (D / 4)), o, heads_m[h], heads_l[h], vs);
+  store_column(o);
 }
 
 // One workgroup per item: its waves take the chunk's tiles in turn, each
@@ -739,6 +797,13 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
       lh += red_l[w][h] * __builtin_amdgcn_exp2f(red_m[w][h] - mh);
       o += *reinterpret_cast<const f32x4*>(&red[w][h][d]);
     }
+    if constexpr (sizeof(typename C::bits_t) == 2)
+      if (__builtin_expect(__any(any_nan(o)), false)) {
+        const int end = (int)min((int64_t)it.n, (int64_t)it.tile_end * kTokens);
+        const f32x4 inf = infinite_values<C, D>(table, reinterpret_cast<const uint16_t*>(p.v_cache), p.pages, p.kv_heads,
+                                                kh, p.page_shift, max(it.lo, it.tile * kTokens), end, d);
+        if (lh == lh) take_infinite(o, inf);
+      }
     if (it.chunks == 1) {
       store_out<T, V>(p, it.b, h0 + h, D, d, o, mh, lh, vs);
     } else {

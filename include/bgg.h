@@ -572,7 +572,9 @@ size_t bgg_attention_workspace_size(const bgg_cache_desc* cache, int64_t q_heads
  * tokens (length 0 or below, or every score -inf) gets out = 0 and
  * lse = -inf.  A page number outside 0 .. pages - 1 (say -1 for a page that
  * a window has left behind) hides its tokens.  What the cache holds at
- * hidden tokens, NaN included, has no influence.
+ * hidden tokens, NaN included, has no influence.  An infinite value of a
+ * visible token makes its element of out infinite, NaN where both signs or a
+ * NaN meet, whatever the token's probability.
  * Products q.k are exact in fp32 sums; softmax statistics and sums are
  * fp32; the probabilities enter their product with the values as a sum of
  * two 16-bit terms; out is rounded once.  The cache is read once per 16
