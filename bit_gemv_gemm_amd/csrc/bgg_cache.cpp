@@ -130,6 +130,8 @@ bgg_status check_attention(const bgg_cache_desc* c, const bgg_attention_args* a)
     return fail(BGG_ERR_BUFFER, "%s: misaligned buffer", who);
   if ((st = check_rows(who, "q", a->q_dev, a->q_stride, a->q_heads * c->head_dim))) return st;
   if ((st = check_rows(who, "out", a->out_dev, a->out_stride, a->q_heads * c->head_dim))) return st;
+  if (a->out_dev == a->q_dev && a->out_stride != a->q_stride && a->batch > 1)
+    return fail(BGG_ERR_SHAPE, "%s: out in the place of q with two strides", who);
   return BGG_OK;
 }
 

@@ -538,7 +538,7 @@ typedef struct bgg_attention_args {
   int64_t q_heads;         /* a multiple of kv_heads, at most 4096 */
   int64_t window;          /* > 0: only the last `window` tokens are visible; 0: all */
   const void* q_dev;       /* [B][q_heads][head_dim] */
-  void* out_dev;           /* same shape */
+  void* out_dev;           /* same shape; overlaps no input, but may be q_dev with the same stride */
   int64_t q_stride;
   int64_t out_stride;
   float* lse_dev;          /* [B][q_heads], or NULL */
