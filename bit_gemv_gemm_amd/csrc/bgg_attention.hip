@@ -10,8 +10,8 @@
 //
 // Measured (one MI355X, which reads 6.14 TB/s; 48 query heads on 8 key heads
 // of 128 unless stated): 1 x 262144 tokens f16 186 us (5.76 TB/s), 16 x
-// 32768 e4m3 183 us (5.87), 1 x 32768 f16 28.9 us (4.6), 1 x 1024 9.4 us, 1 x
-// 64 4.8 us (a kernel that does nothing: 1.7); 16 ragged sequences up to 8000
+// 32768 e4m3 183 us (5.87), 1 x 32768 f16 28.6 us (4.7), 1 x 1024 8.9 us, 1 x
+// 64 4.6 us (a kernel that does nothing: 1.7); 16 ragged sequences up to 8000
 // tokens, 24 heads on 4 of 256, bf16: 28 us (4.0 TB/s).
 #include <hip/hip_runtime.h>
 
@@ -100,7 +100,13 @@ __device__ __forceinline__ float column_sum(float v) {
 // fills the GPU evenly whatever its longest sequence; every sequence has one
 // chunk at least, and its chunks are equal but for rounding.  The lengths
 // are on the device, so each wave works this out by itself: lane l sums over
-// the sequences [l per, (l + 1) per).
+// the sequences [l per, (l + 1) per).  Up to 64 sequences that is one read of
+// the lengths; beyond, each wave reads them all several times over, one after
+// the other in a lane, and there is a workgroup per sequence and head block
+// at least: the schedule's time grows with the square of the batch (40 tokens
+// each, 48 heads on 8 of 128 f16: 256 sequences 24 us, 1024 182 us, 4096 2.06
+// ms, where their bytes take 8, 31 and 126 us; 500 tokens each: 104 us, 447
+// us and 3.0 ms against 86, 346 and 1383).
 // ---------------------------------------------------------------------------
 struct Item {
   int b, head_block;  // head_block = key head * head_blocks + block of 16 of its query heads
@@ -121,10 +127,14 @@ __device__ __forceinline__ int tiles_of(int lo, int n) {
 // A sequence of up to kOneChunk tiles stays whole: the join costs more than
 // the chunks gain (one sequence of 500 tokens, 8 x 128 f16: chunks of 4, 8,
 // 16 tiles 10.3, 11.2, 9.2 us).  A longer one is joined in any case; a wave's
-// tile costs about 1.2 us of latency and a part 0.15 us of the join, so a
-// chunk has at least about sqrt(tiles / 2) tiles (chunks of 4, 8, 16 tiles:
-// 1024 tokens 10.0, 10.8, 12.9 us; 2048 11.7, 11.3, 13.3; 8192 17.6, 17.4,
-// 15.8).
+// tile costs about 1.2 us of latency and a part 0.15 us of the join, so up to
+// 128 tiles a chunk has at least about sqrt(tiles / 2) of them (chunks of 4,
+// 8, 16 tiles: 1024 tokens 10.0, 10.8, 12.9 us; 2048 11.7, 11.3, 13.3; 8192
+// 17.6, 17.4, 15.8).  The floor stays at 16 for longer sequences, whose even
+// share is more than that with eight head blocks; with one or two it is not,
+// and longer chunks are not measured there (1 x 65536 tokens: 16 heads on one
+// key head, 128 parts, 36 us; 8 on two 26; 1 x 262144: 68 and 54, their bytes
+// 22 and 44).
 constexpr int kOneChunk = 16;
 __device__ __forceinline__ int chunks_of(int tiles, int size) {
   if (tiles <= kOneChunk) return 1;

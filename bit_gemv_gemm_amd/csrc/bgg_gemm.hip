@@ -731,7 +731,10 @@ constexpr int kMaxSplits = 32;
 //    CU; short prompts): S ranges with S * wgs within the slots, S chosen to
 //    minimise T / S steps of about 3.2 us plus the fp32 partials (S M N
 //    floats written and read once more, at about 5 TB/s, and the adding
-//    launch).  A 64-token gate/up product runs 7 ranges, k/v 32.
+//    launch).  A 64-token gate/up product runs 7 ranges, k/v 32.  The step's
+//    time and the two workgroups per CU are those of the 128-token tile; the
+//    shorter tiles' steps are shorter (32 tokens of gate/up: 27 us by this
+//    rule, 18.4 measured), so it may give them more ranges than they need.
 //  * Otherwise two ranges when the blocks fill the slots much less evenly
 //    than twice as many would (the last, partly empty round of workgroups,
 //    e.g. 640 blocks on 512 slots for 4096 tokens x 5120 rows, costs nearly

@@ -198,7 +198,10 @@ __global__ void __launch_bounds__(kThreads) k_rotary_append(RotaryParams p) {
 }
 
 // Any even rotary_dim: one pair or value per thread and step, two bytes at a
-// time (4095 tokens as above with all of the head rotated but two values: 32 us, in 16-byte units 21.5).
+// time (4095 tokens as above with all of the head rotated but two values: 32
+// us, in 16-byte units 21.5).  For rotated parts whose halves, or whose end,
+// lie inside a 16-byte unit: a thread's pairs are then spread over other
+// threads' units.  Multiples of 16 (interleaved: of 8) never come here.
 template <class T, class C>
 __global__ void __launch_bounds__(kThreads) k_rotary_append_any(RotaryParams p) {
   __shared__ float cs[kMaxPairs], sn[kMaxPairs];

@@ -578,11 +578,16 @@ size_t bgg_attention_workspace_size(const bgg_cache_desc* cache, int64_t q_heads
  * Products q.k are exact in fp32 sums; softmax statistics and sums are
  * fp32; the probabilities enter their product with the values as a sum of
  * two 16-bit terms; out is rounded once.  The cache is read once per 16
- * query heads of a key head.  The same inputs give the same bits.
+ * query heads of a key head.  The same call gives the same bits; how a
+ * sequence is cut, and so its last bits, follows the lengths of all
+ * sequences of the call.
  * `workspace`: its first BGG_ATTENTION_COUNTER_BYTES count the parts of a
  * sequence and must be zero when a call starts: zero-fill a new workspace
  * once (or call bgg_gemv_workspace_reset); every successful call, of any
  * shape, leaves them zero.  Calls that share a workspace must not overlap.
+ * The rest of it is scratch: a workspace shared with the products must be
+ * reset before a GEMV call that follows this one, and before this one where
+ * a bgg_ternary_gemm call came last.
  * batch == 0 is a no-op.
  * Errors: BGG_ERR_NULL, BGG_ERR_DESC, BGG_ERR_FORMAT (types: a 16-bit cache
  * has the type of q), BGG_ERR_SHAPE, BGG_ERR_BUFFER (alignment, workspace
