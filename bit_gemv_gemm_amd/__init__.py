@@ -119,7 +119,8 @@ class bgg_cache_desc(ctypes.Structure):
 
 
 # the argument structs of the epilogue and of the calls on a cache, in the
-# field order of bgg.h
+# field order of bgg.h, for calls of libbgg.so past _marshal (which fills the
+# C structs themselves)
 _EPILOGUE = struct.Struct("@iiPPPqq")
 _ROTARY_ARGS = struct.Struct("@iiqqqPPPPqqqqPPPfiPPPP")
 _ATTENTION_ARGS = struct.Struct("@ifqqqPPqqPPPPPPqqPPN")
