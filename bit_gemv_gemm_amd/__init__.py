@@ -88,6 +88,10 @@ BGG_ROTARY_BASE = 2
 BGG_ROTARY_PARTS = 3
 ROTARY_SCALINGS = {"none": BGG_ROTARY_NONE, "linear": BGG_ROTARY_LINEAR, "base": BGG_ROTARY_BASE,
                    "parts": BGG_ROTARY_PARTS}
+BGG_AXES_BLOCKS = 0
+BGG_AXES_CYCLIC = 1
+AXES_ARRANGEMENTS = {"blocks": BGG_AXES_BLOCKS, "cyclic": BGG_AXES_CYCLIC}
+BGG_MAX_AXES = 4
 STATUS = {0: "BGG_OK", 1: "BGG_ERR_NULL", 2: "BGG_ERR_FORMAT", 3: "BGG_ERR_SHAPE",
           4: "BGG_ERR_TRIT", 5: "BGG_ERR_PACKED_BYTE", 6: "BGG_ERR_BUFFER", 7: "BGG_ERR_DESC",
           8: "BGG_ERR_HIP", 9: "BGG_ERR_SCALE"}
@@ -124,6 +128,8 @@ class bgg_cache_desc(ctypes.Structure):
 _EPILOGUE = struct.Struct("@iiPPPqq")
 _ROTARY_ARGS = struct.Struct("@iiqqqPPPPqqqqPPPfiPPPP")
 _ATTENTION_ARGS = struct.Struct("@ifqqqPPqqPPPPPPqqPPN")
+_ROTARY_AXES_ARGS = struct.Struct("@qqP")
+_ASSIGN_ARGS = struct.Struct("@qqPPPPqqPqPPPPPPP")
 
 
 class BggError(RuntimeError):
@@ -160,6 +166,9 @@ _SIGS = {
     "bgg_cache_describe": ([_i32, _i64, _i64, _i64, _i64, _PC], _i32),
     "bgg_rotary_frequencies": ([_i64, _f64, _i32, _f64, _f64, _f64, _f64, _vp, _vp], _i32),
     "bgg_rotary_append": ([_PC, _vp, _vp], _i32),
+    "bgg_rotary_axes": ([_vp, _i64, _i32, _vp], _i32),
+    "bgg_rotary_append_axes": ([_PC, _vp, _vp, _vp], _i32),
+    "bgg_cache_assign": ([_PC, _vp, _vp], _i32),
     "bgg_attention_workspace_size": ([_PC, _i64, _i64], _sz),
     "bgg_paged_attention": ([_PC, _vp, _vp], _i32),
     "bgg_status_string": ([_i32], ctypes.c_char_p),
@@ -352,7 +361,7 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 if not isinstance(_marshal, _Missing):
     _marshal.bind(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in (
         "bgg_paged_attention", "bgg_rotary_append", "bgg_ternary_gemv_epilogue", "bgg_gemv_run_epilogue",
-        "bgg_ternary_gemm_epilogue")))
+        "bgg_ternary_gemm_epilogue", "bgg_rotary_append_axes", "bgg_cache_assign")))
 
 
 def _run_on(where, on, stream, call, *args):
@@ -426,6 +435,43 @@ def bgg_rotary_append(cache: bgg_cache_desc, k_cache, v_cache, positions, slots,
     _run_on("bgg_rotary_append", positions, stream, _marshal.rotary_append, cache, k_cache, v_cache, positions, slots,
             freqs, q, q_out, k, v, ROTARY_LAYOUTS[layout] if isinstance(layout, str) else layout, magnitude, k_scale,
             v_scale)
+
+
+def bgg_rotary_axes(sections, arrangement="blocks") -> np.ndarray:
+    """uint8 [pairs]: the axis whose position turns each pair, with
+    sections[a] pairs for axis a."""
+    s = np.ascontiguousarray(sections, dtype=np.int64)
+    if s.ndim != 1:
+        raise ValueError("sections must be one number per axis")
+    out = np.zeros(128, dtype=np.uint8)
+    kind = AXES_ARRANGEMENTS[arrangement] if isinstance(arrangement, str) else int(arrangement)
+    _ok(_lib.bgg_rotary_axes(s.ctypes.data, s.size, kind, out.ctypes.data), "bgg_rotary_axes")
+    return out[:int(s.sum())].copy()
+
+
+def bgg_rotary_append_axes(cache: bgg_cache_desc, k_cache, v_cache, positions, axes, slots, freqs, q=None, q_out=None,
+                           k=None, v=None, layout="half", magnitude: float = 1.0, k_scale=None, v_scale=None,
+                           stream=None) -> None:
+    """bgg_rotary_append for tokens with several positions: positions int32
+    [A, T] (rows of any stride; one row expanded to A is one position on every
+    axis), axes uint8 [len(freqs)], the row whose position turns each pair
+    (bgg_rotary_axes)."""
+    _run_on("bgg_rotary_append_axes", positions, stream, _marshal.rotary_append_axes, cache, k_cache, v_cache, positions,
+            axes, slots, freqs, q, q_out, k, v, ROTARY_LAYOUTS[layout] if isinstance(layout, str) else layout, magnitude,
+            k_scale, v_scale)
+
+
+def bgg_cache_assign(cache: bgg_cache_desc, lengths, counts, page_table, free_pages, free_count, lengths_out,
+                     free_count_out, past, starts, positions, slots, shared_pages=None, stream=None) -> None:
+    """The bookkeeping of a batch's step: counts[b] new tokens for sequence b
+    (below 0: that many given back) get pages from the stack free_pages, and
+    every row of the step its position and slot.  lengths, counts,
+    lengths_out, past, shared_pages: int32 [B]; page_table int32 [B, pages];
+    free_pages int32; free_count, free_count_out int32 [1]; starts int32
+    [B + 1]; positions int32 [T]; slots int64 [T].  lengths_out may be
+    lengths, and free_count_out free_count."""
+    _run_on("bgg_cache_assign", lengths, stream, _marshal.cache_assign, cache, lengths, counts, page_table, free_pages,
+            free_count, lengths_out, free_count_out, past, starts, positions, slots, shared_pages)
 
 
 def bgg_paged_attention(cache: bgg_cache_desc, k_cache, v_cache, page_table, lengths, q, out, workspace,

@@ -1,10 +1,12 @@
 // Host side of the paged cache and of the rotary positions: descriptor,
-// frequency tables and the argument checks of the two device calls
-// (bgg_rotary.hip, bgg_attention.hip).  No GPU work happens here.
+// frequency and axis tables and the argument checks of the device calls
+// (bgg_assign.hip, bgg_rotary.hip, bgg_attention.hip).  No GPU work happens
+// here.
 #include "bgg_cache.h"
 
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 
 namespace bgg {
 
@@ -56,8 +58,7 @@ static bgg_status check_rows(const char* who, const char* what, const void* p, i
   return BGG_OK;
 }
 
-bgg_status check_rotary(const bgg_cache_desc* c, const bgg_rotary_args* a) {
-  const char* who = "bgg_rotary_append";
+static bgg_status check_rotary(const char* who, const bgg_cache_desc* c, const bgg_rotary_args* a) {
   bgg_status st = check_cache(c);
   if (st) return st;
   if (!a) return fail(BGG_ERR_NULL, "%s: NULL arguments", who);
@@ -95,6 +96,56 @@ bgg_status check_rotary(const bgg_cache_desc* c, const bgg_rotary_args* a) {
     if ((st = check_rows(who, "k", a->k_dev, a->k_stride, c->kv_heads * c->head_dim))) return st;
     if ((st = check_rows(who, "v", a->v_dev, a->v_stride, c->kv_heads * c->head_dim))) return st;
   }
+  return BGG_OK;
+}
+
+bgg_status check_rotary(const bgg_cache_desc* c, const bgg_rotary_args* a) {
+  return check_rotary("bgg_rotary_append", c, a);
+}
+
+bgg_status check_rotary_axes(const bgg_cache_desc* c, const bgg_rotary_args* a,
+                             const bgg_rotary_axes_args* x) {
+  const char* who = "bgg_rotary_append_axes";
+  bgg_status st = check_rotary(who, c, a);
+  if (st) return st;
+  if (!x || !x->axis_of_pair_dev) return fail(BGG_ERR_NULL, "%s: NULL axes", who);
+  if (x->axes < 1 || x->axes > BGG_MAX_AXES)
+    return fail(BGG_ERR_SHAPE, "%s: %lld axes", who, (long long)x->axes);
+  if (x->stride != 0 && (x->stride < a->tokens || x->stride > (int64_t(1) << 40)))
+    return fail(BGG_ERR_SHAPE, "%s: rows of %lld positions %lld apart", who, (long long)a->tokens,
+                (long long)x->stride);
+  return BGG_OK;
+}
+
+bgg_status check_assign(const bgg_cache_desc* c, const bgg_assign_args* a) {
+  const char* who = "bgg_cache_assign";
+  bgg_status st = check_cache(c);
+  if (st) return st;
+  if (!a) return fail(BGG_ERR_NULL, "%s: NULL arguments", who);
+  if (a->batch < 0 || a->batch > kMaxBatch)
+    return fail(BGG_ERR_SHAPE, "%s: batch of %lld", who, (long long)a->batch);
+  if (a->rows < 0 || a->rows > kMaxTokens)
+    return fail(BGG_ERR_SHAPE, "%s: %lld rows", who, (long long)a->rows);
+  if (a->table_width < 1 || a->table_width > 0x7FFFFFFF / c->page_size ||
+      a->batch * a->table_width > (int64_t(1) << 31))
+    return fail(BGG_ERR_SHAPE, "%s: %lld pages of %lld tokens for each of %lld sequences", who,
+                (long long)a->table_width, (long long)c->page_size, (long long)a->batch);
+  if (a->table_stride < a->table_width || a->table_stride > (int64_t(1) << 40))
+    return fail(BGG_ERR_SHAPE, "%s: table stride %lld below its width %lld", who,
+                (long long)a->table_stride, (long long)a->table_width);
+  if (a->free_capacity < 1 || a->free_capacity > 0x7FFFFFFF)
+    return fail(BGG_ERR_SHAPE, "%s: room for %lld free pages", who, (long long)a->free_capacity);
+  if (!a->free_pages_dev || !a->free_count_dev || !a->free_count_out_dev || !a->starts_dev)
+    return fail(BGG_ERR_NULL, "%s: NULL buffer", who);
+  if (a->batch && (!a->lengths_dev || !a->counts_dev || !a->page_table_dev || !a->lengths_out_dev || !a->past_dev))
+    return fail(BGG_ERR_NULL, "%s: NULL buffer", who);
+  if (a->rows && (!a->positions_dev || !a->slots_dev)) return fail(BGG_ERR_NULL, "%s: NULL buffer", who);
+  for (const void* p : {(const void*)a->lengths_dev, (const void*)a->counts_dev, (const void*)a->shared_pages_dev,
+                        (const void*)a->page_table_dev, (const void*)a->free_pages_dev, (const void*)a->free_count_dev,
+                        (const void*)a->lengths_out_dev, (const void*)a->free_count_out_dev, (const void*)a->past_dev,
+                        (const void*)a->starts_dev, (const void*)a->positions_dev})
+    if (!aligned(p, 4)) return fail(BGG_ERR_BUFFER, "%s: misaligned buffer", who);
+  if (!aligned(a->slots_dev, 8)) return fail(BGG_ERR_BUFFER, "%s: misaligned slots", who);
   return BGG_OK;
 }
 
@@ -204,6 +255,36 @@ bgg_status bgg_rotary_frequencies(int64_t rotary_dim, double base, int32_t scali
     freqs[i] = (float)f;
   }
   *magnitude = scaling == BGG_ROTARY_PARTS ? (float)(1.0 + 0.1 * std::log(factor)) : 1.0f;
+  clear_error();
+  return BGG_OK;
+}
+
+bgg_status bgg_rotary_axes(const int64_t* sections, int64_t axes, int32_t arrangement,
+                           uint8_t* axis_of_pair) {
+  const char* who = "bgg_rotary_axes";
+  if (!sections || !axis_of_pair) return fail(BGG_ERR_NULL, "%s: NULL argument", who);
+  if (arrangement != BGG_AXES_BLOCKS && arrangement != BGG_AXES_CYCLIC)
+    return fail(BGG_ERR_FORMAT, "%s: unknown arrangement %d", who, (int)arrangement);
+  if (axes < 1 || axes > BGG_MAX_AXES) return fail(BGG_ERR_SHAPE, "%s: %lld axes", who, (long long)axes);
+  int64_t pairs = 0;
+  for (int64_t a = 0; a < axes; ++a) {
+    if (sections[a] < 0 || sections[a] > 128)
+      return fail(BGG_ERR_SHAPE, "%s: %lld pairs of axis %lld", who, (long long)sections[a], (long long)a);
+    pairs += sections[a];
+  }
+  if (pairs < 1 || pairs > 128) return fail(BGG_ERR_SHAPE, "%s: %lld pairs", who, (long long)pairs);
+  if (arrangement == BGG_AXES_BLOCKS) {
+    int64_t i = 0;
+    for (int64_t a = 0; a < axes; ++a)
+      for (int64_t k = 0; k < sections[a]; ++k) axis_of_pair[i++] = (uint8_t)a;
+  } else {
+    for (int64_t a = 1; a < axes; ++a)  // its last pair is a + axes * (sections[a] - 1)
+      if (sections[a] > 0 && a + axes * (sections[a] - 1) >= pairs)
+        return fail(BGG_ERR_SHAPE, "%s: %lld pairs of axis %lld do not lie among %lld in turn", who,
+                    (long long)sections[a], (long long)a, (long long)pairs);
+    for (int64_t i = 0; i < pairs; ++i)
+      axis_of_pair[i] = (uint8_t)(i < axes * sections[i % axes] ? i % axes : 0);
+  }
   clear_error();
   return BGG_OK;
 }

@@ -12,6 +12,10 @@ constexpr int64_t kMaxBatch = 4096;  // (a wave looks through 64 sequences per l
 // BGG_OK iff `c` is exactly what bgg_cache_describe makes for its fields.
 bgg_status check_cache(const bgg_cache_desc* c);
 bgg_status check_rotary(const bgg_cache_desc* c, const bgg_rotary_args* a);
+// The same, and the positions of several axes.
+bgg_status check_rotary_axes(const bgg_cache_desc* c, const bgg_rotary_args* a,
+                             const bgg_rotary_axes_args* x);
+bgg_status check_assign(const bgg_cache_desc* c, const bgg_assign_args* a);
 bgg_status check_attention(const bgg_cache_desc* c, const bgg_attention_args* a);
 
 }  // namespace bgg

@@ -23,6 +23,8 @@ struct Refused {};
 
 decltype(&bgg_paged_attention) p_attention;
 decltype(&bgg_rotary_append) p_rotary;
+decltype(&bgg_rotary_append_axes) p_rotary_axes;
+decltype(&bgg_cache_assign) p_assign;
 decltype(&bgg_ternary_gemv_epilogue) p_gemv;
 decltype(&bgg_gemv_run_epilogue) p_run;
 decltype(&bgg_ternary_gemm_epilogue) p_gemm;
@@ -205,45 +207,103 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (cache, k_cache, v_cache, positions, slots, freqs, q, q_out, k, v, layout, magnitude, k_scale, v_scale, stream)
+// (cache, k_cache, v_cache, positions, slots, freqs, q, q_out, k, v, layout, magnitude, k_scale, v_scale, stream),
+// with several axes their table after the positions
+PyObject* rotary(PyObject* const* a, bool several) {
+  Cache c(a[0], "cache");
+  const at::Tensor& pos = tensor(a[3], "positions");
+  const int dev = device_of(pos, "positions");
+  bgg_rotary_axes_args x{};
+  int64_t T = pos.numel();
+  if (several) {
+    if (pos.dim() != 2 || (pos.size(1) > 1 && pos.stride(1) != 1) || pos.scalar_type() != at::kInt || pos.stride(0) < 0)
+      refuse("positions", "must be int32 [axes, tokens] with contiguous rows");
+    T = pos.size(1);
+    x.axes = pos.size(0);
+    x.stride = x.axes > 1 ? pos.stride(0) : 0;
+    const at::Tensor& of = tensor(a[4], "axes");
+    x.axis_of_pair_dev = (const uint8_t*)vector(a[4], 1, at::kByte, dev, "axes");
+    if (of.numel() != tensor(a[6], "freqs").numel()) refuse("axes", "must have an entry per frequency");
+  }
+  PyObject* const* r = a + several;  // (slots and what follows)
+  const int64_t D = c->head_dim;
+  const bool with_q = !is_none(r[6]), with_k = !is_none(r[8]);
+  if (!with_q && !with_k) refuse("q and k", "one of them is needed");
+  if (with_k != !is_none(r[9])) refuse("k and v", "come together");
+  const at::Tensor& ref = tensor(r[with_q ? 6 : 8], with_q ? "q" : "k");
+  bgg_rotary_args g{};
+  g.type = type_of(ref, with_q ? "q" : "k");
+  const at::ScalarType st = ref.scalar_type();
+  if (with_q) {
+    const Rows rq = rows(r[6], T, D, st, dev, "q"), ro = rows(r[7], T, D, st, dev, "q_out");
+    if (ro.heads != rq.heads) refuse("q_out", "must have q's heads");
+    g.q_dev = rq.data, g.q_stride = rq.stride, g.q_heads = rq.heads;
+    g.q_out_dev = ro.data, g.q_out_stride = ro.stride;
+  }
+  if (with_k) {
+    const Rows rk = rows(r[8], T, D, st, dev, "k"), rv = rows(r[9], T, D, st, dev, "v");
+    if (rk.heads != c->kv_heads || rv.heads != c->kv_heads) refuse("k and v", "must have the cache's heads");
+    g.k_dev = rk.data, g.k_stride = rk.stride;
+    g.v_dev = rv.data, g.v_stride = rv.stride;
+    cache_buffers(c, a[1], a[2], dev, &g.k_cache_dev, &g.v_cache_dev);
+    g.slots_dev = (const int64_t*)vector(r[4], T, at::kLong, dev, "slots");
+  }
+  g.layout = (int32_t)integer(r[10]);
+  g.positions_dev = several ? (const int32_t*)pos.data_ptr() : (const int32_t*)vector(a[3], T, at::kInt, dev, "positions");
+  g.freqs_dev = (const float*)vector(r[5], 1, at::kFloat, dev, "freqs");
+  g.rotary_dim = 2 * tensor(r[5], "freqs").numel();
+  g.tokens = T;
+  g.magnitude = (float)number(r[11]);
+  g.k_scale_dev = (const float*)vector(r[12], c->kv_heads, at::kFloat, dev, "k_scale");
+  g.v_scale_dev = (const float*)vector(r[13], c->kv_heads, at::kFloat, dev, "v_scale");
+  if (T == 0) return PyLong_FromLong(0);  // (empty tensors have no pointers)
+  void* stream = (void*)(uintptr_t)integer(r[14]);
+  if (several) return status_of([&] { return p_rotary_axes(c.get(), &g, &x, stream); });
+  return status_of([&] { return p_rotary(c.get(), &g, stream); });
+}
 PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded("rotary_append", n, 15, [&]() -> PyObject* {
+  return guarded("rotary_append", n, 15, [&] { return rotary(a, false); });
+}
+PyObject* rotary_append_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("rotary_append_axes", n, 16, [&] { return rotary(a, true); });
+}
+
+// (cache, lengths, counts, page_table, free_pages, free_count, lengths_out, free_count_out, past, starts, positions,
+// slots, shared_pages, stream)
+PyObject* cache_assign(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("cache_assign", n, 14, [&]() -> PyObject* {
     Cache c(a[0], "cache");
-    const at::Tensor& pos = tensor(a[3], "positions");
-    const int dev = device_of(pos, "positions");
-    const int64_t T = pos.numel(), D = c->head_dim;
-    const bool with_q = !is_none(a[6]), with_k = !is_none(a[8]);
-    if (!with_q && !with_k) refuse("q and k", "one of them is needed");
-    if (with_k != !is_none(a[9])) refuse("k and v", "come together");
-    const at::Tensor& ref = tensor(a[with_q ? 6 : 8], with_q ? "q" : "k");
-    bgg_rotary_args g{};
-    g.type = type_of(ref, with_q ? "q" : "k");
-    const at::ScalarType st = ref.scalar_type();
-    if (with_q) {
-      const Rows rq = rows(a[6], T, D, st, dev, "q"), ro = rows(a[7], T, D, st, dev, "q_out");
-      if (ro.heads != rq.heads) refuse("q_out", "must have q's heads");
-      g.q_dev = rq.data, g.q_stride = rq.stride, g.q_heads = rq.heads;
-      g.q_out_dev = ro.data, g.q_out_stride = ro.stride;
-    }
-    if (with_k) {
-      const Rows rk = rows(a[8], T, D, st, dev, "k"), rv = rows(a[9], T, D, st, dev, "v");
-      if (rk.heads != c->kv_heads || rv.heads != c->kv_heads) refuse("k and v", "must have the cache's heads");
-      g.k_dev = rk.data, g.k_stride = rk.stride;
-      g.v_dev = rv.data, g.v_stride = rv.stride;
-      cache_buffers(c, a[1], a[2], dev, &g.k_cache_dev, &g.v_cache_dev);
-      g.slots_dev = (const int64_t*)vector(a[4], T, at::kLong, dev, "slots");
-    }
-    g.layout = (int32_t)integer(a[10]);
-    g.positions_dev = (const int32_t*)vector(a[3], T, at::kInt, dev, "positions");
-    g.freqs_dev = (const float*)vector(a[5], 1, at::kFloat, dev, "freqs");
-    g.rotary_dim = 2 * tensor(a[5], "freqs").numel();
-    g.tokens = T;
-    g.magnitude = (float)number(a[11]);
-    g.k_scale_dev = (const float*)vector(a[12], c->kv_heads, at::kFloat, dev, "k_scale");
-    g.v_scale_dev = (const float*)vector(a[13], c->kv_heads, at::kFloat, dev, "v_scale");
-    if (T == 0) return PyLong_FromLong(0);  // (empty tensors have no pointers)
-    void* stream = (void*)(uintptr_t)integer(a[14]);
-    return status_of([&] { return p_rotary(c.get(), &g, stream); });
+    const at::Tensor& len = tensor(a[1], "lengths");
+    const int dev = device_of(len, "lengths");
+    auto ints = [&](int i, int64_t n, const char* what) {
+      tensor(a[i], what);  // (None is refused)
+      return (int32_t*)vector(a[i], n, at::kInt, dev, what);
+    };
+    bgg_assign_args g{};
+    g.batch = len.numel();
+    g.lengths_dev = ints(1, g.batch, "lengths");
+    g.counts_dev = ints(2, g.batch, "counts");
+    const at::Tensor& t = tensor(a[3], "page_table");
+    if (!t.is_cuda() || t.get_device() != dev || t.scalar_type() != at::kInt || t.dim() != 2 ||
+        t.size(0) != g.batch || (t.size(1) > 1 && t.stride(1) != 1))
+      refuse("page_table", "must be int32 [batch, pages] with contiguous rows on the device of lengths");
+    g.page_table_dev = (int32_t*)t.data_ptr();
+    g.table_width = t.size(1);
+    g.table_stride = g.batch > 1 ? t.stride(0) : t.size(1);
+    g.free_pages_dev = ints(4, 1, "free_pages");
+    g.free_capacity = tensor(a[4], "free_pages").numel();
+    g.free_count_dev = ints(5, 1, "free_count");
+    g.lengths_out_dev = ints(6, g.batch, "lengths_out");
+    g.free_count_out_dev = ints(7, 1, "free_count_out");
+    g.past_dev = ints(8, g.batch, "past");
+    g.starts_dev = ints(9, g.batch + 1, "starts");
+    g.rows = tensor(a[10], "positions").numel();
+    g.positions_dev = ints(10, g.rows, "positions");
+    if (tensor(a[11], "slots").numel() != g.rows) refuse("slots", "must have an entry per position");
+    g.slots_dev = (int64_t*)vector(a[11], g.rows, at::kLong, dev, "slots");
+    g.shared_pages_dev = (const int32_t*)vector(a[12], g.batch, at::kInt, dev, "shared_pages");
+    void* stream = (void*)(uintptr_t)integer(a[13]);
+    return status_of([&] { return p_assign(c.get(), &g, stream); });
   });
 }
 
@@ -292,16 +352,18 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // The addresses of bgg_paged_attention, bgg_rotary_append, bgg_ternary_gemv_epilogue,
-// bgg_gemv_run_epilogue and bgg_ternary_gemm_epilogue.
+// bgg_gemv_run_epilogue, bgg_ternary_gemm_epilogue, bgg_rotary_append_axes and bgg_cache_assign.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded("bind", n, 5, [&]() -> PyObject* {
-    void* p[5];
-    for (int i = 0; i < 5; ++i) p[i] = (void*)(uintptr_t)integer(a[i]);
+  return guarded("bind", n, 7, [&]() -> PyObject* {
+    void* p[7];
+    for (int i = 0; i < 7; ++i) p[i] = (void*)(uintptr_t)integer(a[i]);
     p_attention = (decltype(p_attention))p[0];
     p_rotary = (decltype(p_rotary))p[1];
     p_gemv = (decltype(p_gemv))p[2];
     p_run = (decltype(p_run))p[3];
     p_gemm = (decltype(p_gemm))p[4];
+    p_rotary_axes = (decltype(p_rotary_axes))p[5];
+    p_assign = (decltype(p_assign))p[6];
     Py_RETURN_NONE;
   });
 }
@@ -313,6 +375,8 @@ PyCFunction entry() {
 PyMethodDef methods[] = {{"bind", entry<bind>(), METH_FASTCALL, nullptr},
                          {"paged_attention", entry<paged_attention>(), METH_FASTCALL, nullptr},
                          {"rotary_append", entry<rotary_append>(), METH_FASTCALL, nullptr},
+                         {"rotary_append_axes", entry<rotary_append_axes>(), METH_FASTCALL, nullptr},
+                         {"cache_assign", entry<cache_assign>(), METH_FASTCALL, nullptr},
                          {"product", entry<product>(), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

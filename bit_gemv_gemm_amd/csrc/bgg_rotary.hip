@@ -29,6 +29,9 @@ struct RotaryParams {
   void *k_cache, *v_cache;
   const float *k_scale, *v_scale;
   int64_t all_slots;
+  const uint8_t* axis_of_pair;  // nullptr: one position per token
+  int64_t axis_stride;
+  int last_axis;
   int q_heads, kv_heads, head_dim, pairs, interleaved, page_shift, rows_per_group;
 };
 
@@ -45,7 +48,9 @@ __device__ __forceinline__ void angle_of(int32_t position, float freq, float* c,
 __device__ __forceinline__ void angles_to_lds(const RotaryParams& p, int64_t t, float* cs, float* sn) {
   if ((int)threadIdx.x < p.pairs) {
     float c, s;
-    angle_of(p.positions[t], p.freqs[threadIdx.x], &c, &s);
+    const int32_t* positions = p.positions;
+    if (p.axis_of_pair) positions += min((int)p.axis_of_pair[threadIdx.x], p.last_axis) * p.axis_stride;
+    angle_of(positions[t], p.freqs[threadIdx.x], &c, &s);
     cs[threadIdx.x] = c * p.magnitude;
     sn[threadIdx.x] = s * p.magnitude;
   }
@@ -253,14 +258,16 @@ void launch_rotary(const RotaryParams& p, dim3 grid, hipStream_t s) {
     hipLaunchKernelGGL((k_rotary_append<T, C, true>), grid, block, 0, s, p);
 }
 
-}  // namespace
-
-extern "C" bgg_status bgg_rotary_append(const bgg_cache_desc* c, const bgg_rotary_args* a,
-                                        void* stream) {
-  bgg_status st = check_rotary(c, a);
-  if (st) return st;
+// The call, its arguments checked.
+bgg_status append(const char* who, const bgg_cache_desc* c, const bgg_rotary_args* a, const bgg_rotary_axes_args* x,
+                  void* stream) {
   if (a->tokens == 0) return BGG_OK;
   RotaryParams p{};
+  if (x) {
+    p.axis_of_pair = x->axis_of_pair_dev;
+    p.axis_stride = x->stride;
+    p.last_axis = (int)x->axes - 1;
+  }
   p.q = (const uint16_t*)a->q_dev;
   p.k = (const uint16_t*)a->k_dev;
   p.v = (const uint16_t*)a->v_dev;
@@ -302,5 +309,22 @@ extern "C" bgg_status bgg_rotary_append(const bgg_cache_desc* c, const bgg_rotar
     else
       launch_rotary<BF16, BF16>(p, grid, s);
   }
-  return hip_check("bgg_rotary_append");
+  return hip_check(who);
 }
+
+}  // namespace
+
+extern "C" {
+
+bgg_status bgg_rotary_append(const bgg_cache_desc* c, const bgg_rotary_args* a, void* stream) {
+  const bgg_status st = check_rotary(c, a);
+  return st ? st : append("bgg_rotary_append", c, a, nullptr, stream);
+}
+
+bgg_status bgg_rotary_append_axes(const bgg_cache_desc* c, const bgg_rotary_args* a, const bgg_rotary_axes_args* x,
+                                  void* stream) {
+  const bgg_status st = check_rotary_axes(c, a, x);
+  return st ? st : append("bgg_rotary_append_axes", c, a, x, stream);
+}
+
+}  // extern "C"

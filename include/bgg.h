@@ -529,6 +529,105 @@ typedef struct bgg_rotary_args {
 bgg_status bgg_rotary_append(const bgg_cache_desc* cache, const bgg_rotary_args* args,
                              void* stream);
 
+/* Which axis turns which pair in a model whose tokens have several positions
+ * (time, height and width of an image's or video's patches; no page
+ * passage), with sections[a] pairs for axis a of A:
+ *   BLOCKS  the first sections[0] pairs turn by axis 0, the next sections[1]
+ *           by axis 1, ...
+ *   CYCLIC  pair i turns by axis i mod A as long as i < A sections[i mod A],
+ *           else by axis 0 */
+typedef enum { BGG_AXES_BLOCKS = 0, BGG_AXES_CYCLIC = 1 } bgg_axes_arrangement;
+
+#define BGG_MAX_AXES 4
+
+/* The table of axes that bgg_rotary_append_axes takes: axis_of_pair[i] (host
+ * bytes), i < the sum of the sections (rotary_dim / 2).  CYCLIC needs
+ * sections that the rule above gives each axis in full: the first sections[a]
+ * pairs of axis a > 0 lie among the pairs, and axis 0 has the rest.  Host
+ * only, no page passage.
+ * Errors: BGG_ERR_NULL, BGG_ERR_FORMAT (arrangement), BGG_ERR_SHAPE (axes
+ * outside 1..BGG_MAX_AXES; a section below 0; no pair, or more than 128). */
+bgg_status bgg_rotary_axes(const int64_t* sections, int64_t axes, int32_t arrangement,
+                           uint8_t* axis_of_pair);
+
+/* The positions of bgg_rotary_append_axes: args->positions_dev holds axes
+ * rows of T positions, stride apart (in values; 0: every axis reads the same
+ * row, as text does), and pair i turns by row axis_of_pair[i] (a row past the
+ * last counts as the last). */
+typedef struct bgg_rotary_axes_args {
+  int64_t axes;                    /* 1 .. BGG_MAX_AXES */
+  int64_t stride;                  /* 0, or at least T */
+  const uint8_t* axis_of_pair_dev; /* [rotary_dim / 2] */
+} bgg_rotary_axes_args;
+
+/* bgg_rotary_append for tokens with several positions (no page passage): the
+ * angle of pair i is positions[axis_of_pair[i]][t] * freqs[i], everything
+ * else is as there.  (freqs is the caller's: a tower that starts each axis
+ * anew puts the tables of its sections one after the other.  Rows without a
+ * cache, as an image tower's: queries and keys side by side are q alone.)
+ * Errors: as bgg_rotary_append. */
+bgg_status bgg_rotary_append_axes(const bgg_cache_desc* cache, const bgg_rotary_args* args,
+                                  const bgg_rotary_axes_args* axes, void* stream);
+
+/* Arguments of bgg_cache_assign.  int32 arrays are 4-byte aligned, slots
+ * 8-byte. */
+typedef struct bgg_assign_args {
+  int64_t batch;                   /* 0 <= B <= 4096 sequences */
+  int64_t rows;                    /* 0 <= T <= 2^23 rows for new tokens */
+  const int32_t* lengths_dev;      /* [B]: tokens in the cache */
+  const int32_t* counts_dev;       /* [B]: new tokens; below 0: tokens given back */
+  const int32_t* shared_pages_dev; /* [B]: first pages of a sequence that are not its own,
+                                      or NULL (none) */
+  int32_t* page_table_dev;         /* [B][table_stride] */
+  int64_t table_width;             /* >= 1; table_width * page_size < 2^31, B * table_width <= 2^31 */
+  int64_t table_stride;            /* >= table_width */
+  int32_t* free_pages_dev;         /* [free_capacity]: a stack of free pages, the next one last */
+  int64_t free_capacity;           /* 1 .. 2^31 - 1 */
+  const int32_t* free_count_dev;   /* [1]: pages on the stack (cut to 0 .. free_capacity) */
+  int32_t* lengths_out_dev;        /* [B]; may be lengths_dev */
+  int32_t* free_count_out_dev;     /* [1]; may be free_count_dev */
+  int32_t* past_dev;               /* [B] */
+  int32_t* starts_dev;             /* [B + 1] */
+  int32_t* positions_dev;          /* [T] */
+  int64_t* slots_dev;              /* [T] */
+} bgg_assign_args;
+
+/*
+ * The bookkeeping of one step of a serving batch (no page passage): pages
+ * for the new tokens of each sequence from a stack of free ones, back to it
+ * from sequences that end or give tokens back, and for each row of the step
+ * the position and the slot that bgg_rotary_append takes.  With W =
+ * table_width, ps = page_size, held(x) = ceil(x / ps), n = lengths[b] cut to
+ * 0 .. W ps and c = counts[b], in this order:
+ *  1. c < 0: past[b] = max(n + c, shared_pages[b] ps), at most n (INT32_MIN:
+ *     all that is not shared).  The pages of table entries held(past[b]) ..
+ *     held(n) - 1 go onto the stack, the last sequence's last entry first
+ *     (what a step took and the next gives back is where it was); entries
+ *     outside 0 .. pages - 1 are left out, and so is what the stack has no
+ *     room for.  The entries themselves stay.  c >= 0: past[b] = n.
+ *  2. The rows of the new tokens lie one sequence after the other:
+ *     starts[b] = the sum of the counts above 0 before b, cut to T, and
+ *     starts[B] the sum of all.
+ *  3. A sequence with c > 0 is served if its rows end within T, past[b] + c
+ *     <= W ps, and the stack has its held(past[b] + c) - held(past[b]) pages
+ *     left after those of every sequence before it that meets the first two
+ *     conditions (served or not: no sequence overtakes another one; one that
+ *     needs no page is served).  Its pages come off the stack in order of
+ *     sequence and entry, into its table entries from held(past[b]) on.
+ *  4. lengths_out[b] = past[b] + c if served, else past[b];
+ *     free_count_out = pages left on the stack.
+ *  5. Row starts[b] + i of a served sequence: positions = past[b] + i, slots
+ *     = the slot of that token, -1 if its page lies outside 0 .. pages - 1.
+ *     Every other row: position 0, slot -1 (stores nothing).
+ * The rest of table and stack is left as it was.  Only the cache's pages and
+ * page_size matter.  No buffers overlap except where noted; the same call
+ * gives the same result.  With lengths_out = lengths and free_count_out =
+ * free_count a captured step can be replayed.
+ * Errors: BGG_ERR_NULL (buffers of no elements may be NULL), BGG_ERR_DESC,
+ * BGG_ERR_SHAPE, BGG_ERR_BUFFER (alignment), BGG_ERR_HIP.
+ */
+bgg_status bgg_cache_assign(const bgg_cache_desc* cache, const bgg_assign_args* args, void* stream);
+
 /* Arguments of bgg_paged_attention; rows, strides and alignment as in
  * bgg_rotary_args. */
 typedef struct bgg_attention_args {
