@@ -129,6 +129,7 @@ _EPILOGUE = struct.Struct("@iiPPPqq")
 _ROTARY_ARGS = struct.Struct("@iiqqqPPPPqqqqPPPfiPPPP")
 _ATTENTION_ARGS = struct.Struct("@ifqqqPPqqPPPPPPqqPPN")
 _ROTARY_AXES_ARGS = struct.Struct("@qqP")
+_SHARED_ARGS = struct.Struct("@qPP")
 _ASSIGN_ARGS = struct.Struct("@qqPPPPqqPqPPPPPPP")
 
 
@@ -171,6 +172,8 @@ _SIGS = {
     "bgg_cache_assign": ([_PC, _vp, _vp], _i32),
     "bgg_attention_workspace_size": ([_PC, _i64, _i64], _sz),
     "bgg_paged_attention": ([_PC, _vp, _vp], _i32),
+    "bgg_shared_attention_workspace_size": ([_PC, _i64, _i64], _sz),
+    "bgg_shared_attention": ([_PC, _vp, _vp, _vp], _i32),
     "bgg_status_string": ([_i32], ctypes.c_char_p),
     "bgg_last_error": ([], ctypes.c_char_p),
     "bgg_abi_version": ([], _u32),
@@ -361,7 +364,7 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 if not isinstance(_marshal, _Missing):
     _marshal.bind(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in (
         "bgg_paged_attention", "bgg_rotary_append", "bgg_ternary_gemv_epilogue", "bgg_gemv_run_epilogue",
-        "bgg_ternary_gemm_epilogue", "bgg_rotary_append_axes", "bgg_cache_assign")))
+        "bgg_ternary_gemm_epilogue", "bgg_rotary_append_axes", "bgg_cache_assign", "bgg_shared_attention")))
 
 
 def _run_on(where, on, stream, call, *args):
@@ -481,6 +484,22 @@ def bgg_paged_attention(cache: bgg_cache_desc, k_cache, v_cache, page_table, len
     [B, pages]; lengths int32 [B]; lse None or float32 [B, heads]."""
     _run_on("bgg_paged_attention", q, stream, _marshal.paged_attention, cache, k_cache, v_cache, page_table, lengths, q,
             out, workspace, scale, window, lse, k_scale, v_scale)
+
+
+def bgg_shared_attention_workspace_size(cache: bgg_cache_desc, q_heads: int, batch: int) -> int:
+    return int(_lib.bgg_shared_attention_workspace_size(ctypes.byref(cache), q_heads, batch))
+
+
+def bgg_shared_attention(cache: bgg_cache_desc, k_cache, v_cache, page_table, lengths, group_starts, shared_pages, q, out,
+                         workspace, scale: float, window: int = 0, lse=None, k_scale=None, v_scale=None,
+                         stream=None) -> None:
+    """bgg_paged_attention of a batch whose groups share their first pages,
+    which are read once per group: sequences group_starts[g] ..
+    group_starts[g + 1] - 1 share those of the first shared_pages[
+    group_starts[g]] table entries.  group_starts int32 [G + 1], shared_pages
+    int32 [B]."""
+    _run_on("bgg_shared_attention", q, stream, _marshal.shared_attention, cache, k_cache, v_cache, page_table, lengths, q,
+            out, workspace, scale, window, lse, k_scale, v_scale, group_starts, shared_pages)
 
 
 # ---------------------------------------------------------------------------

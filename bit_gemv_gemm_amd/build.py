@@ -15,7 +15,7 @@ LIB = os.path.join(HERE, "libbgg.so")
 PROBE_LIB = os.path.join(HERE, "libbgg_probe.so")
 PROBE_SOURCES = ["probe_stream.hip"]
 SOURCES = ["bgg_host.cpp", "bgg_rotate.hip", "bgg_gemv.hip", "bgg_gemv_noalloc.hip", "bgg_mxv.hip", "bgg_unpack.hip", "bgg_gemm.hip",
-           "bgg_ternarize.hip", "bgg_cache.cpp", "bgg_assign.hip", "bgg_rotary.hip", "bgg_attention.hip",
+           "bgg_ternarize.hip", "bgg_cache.cpp", "bgg_assign.hip", "bgg_rotary.hip", "bgg_shared.hip", "bgg_attention.hip",
            "bgg_epilogue.cpp"]
 MARSHAL_LIB = os.path.join(HERE, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 CXX = os.environ.get("CXX", "g++")

@@ -16,82 +16,12 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <cfloat>
 
-#include "bgg_cache.h"
-#include "bgg_lowp.h"
+#include "bgg_shared.h"
 
 using namespace bgg;
 
 namespace {
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-constexpr int kWaves = 4;
-constexpr int kTokens = 32;  // tokens of a tile: one wave's step
-constexpr int kHeads = 16;   // query heads of a workgroup (columns of the products)
-
-struct AttnParams {
-  const uint16_t* q;
-  uint16_t* out;
-  int64_t q_stride, out_stride;
-  float* lse;
-  const uint8_t *k_cache, *v_cache;
-  const float *k_scale, *v_scale;
-  const int32_t* table;
-  int64_t table_stride;
-  const int32_t* lengths;
-  int64_t window;
-  uint32_t* counters;
-  float* parts;
-  float scale;
-  int max_tokens, pages, batch, q_heads, kv_heads, group, head_blocks, page_shift;
-  int target_items;
-};
-
-// ---------------------------------------------------------------------------
-// lane moves
-// ---------------------------------------------------------------------------
-// Sum over the lanes up to and including this one.
-__device__ __forceinline__ int scan_add(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1, 3
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2, 3
-  return v;
-}
-template <int MOVE, int ROWS>
-__device__ __forceinline__ float add_from(float v) {
-  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), MOVE, ROWS, 0xF, false));
-}
-// Sum over all lanes, in every lane.
-__device__ __forceinline__ float wave_add(float v) {
-  v = add_from<0x111, 0xF>(v);
-  v = add_from<0x112, 0xF>(v);
-  v = add_from<0x114, 0xF>(v);
-  v = add_from<0x118, 0xF>(v);
-  v = add_from<0x142, 0xA>(v);
-  v = add_from<0x143, 0xC>(v);
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
-}
-// Maximum and sum over the four lanes that hold one column (l, l ^ 16,
-// l ^ 32, l ^ 48).
-__device__ __forceinline__ float column_max(float v) {
-  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
-}
-__device__ __forceinline__ float column_sum(float v) {
-  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
 
 // ---------------------------------------------------------------------------
 // Which sequence, heads and tokens a workgroup takes.  The visible tokens of
@@ -108,44 +38,6 @@ __device__ __forceinline__ float column_sum(float v) {
 // ms, where their bytes take 8, 31 and 126 us; 500 tokens each: 104 us, 447
 // us and 3.0 ms against 86, 346 and 1383).
 // ---------------------------------------------------------------------------
-struct Item {
-  int b, head_block;  // head_block = key head * head_blocks + block of 16 of its query heads
-  int chunk, chunks;
-  int part;            // of a sequence with several chunks: this one among all such
-  int lo, n;           // visible tokens
-  int tile, tile_end;  // this chunk's tiles (token / 32)
-};
-
-__device__ __forceinline__ void visible(const AttnParams& p, int b, int& lo, int& n) {
-  const int len = p.lengths[b];
-  n = len < 0 ? 0 : len < p.max_tokens ? len : p.max_tokens;
-  lo = p.window > 0 && n > p.window ? n - (int)p.window : 0;
-}
-__device__ __forceinline__ int tiles_of(int lo, int n) {
-  return n > lo ? (n - 1) / kTokens - lo / kTokens + 1 : 0;
-}
-// A sequence of up to kOneChunk tiles stays whole: the join costs more than
-// the chunks gain (one sequence of 500 tokens, 8 x 128 f16: chunks of 4, 8,
-// 16 tiles 10.3, 11.2, 9.2 us).  A longer one is joined in any case; a wave's
-// tile costs about 1.2 us of latency and a part 0.15 us of the join, so up to
-// 128 tiles a chunk has at least about sqrt(tiles / 2) of them (chunks of 4,
-// 8, 16 tiles: 1024 tokens 10.0, 10.8, 12.9 us; 2048 11.7, 11.3, 13.3; 8192
-// 17.6, 17.4, 15.8).  The floor stays at 16 for longer sequences, whose even
-// share is more than that with eight head blocks; with one or two it is not,
-// and longer chunks are not measured there (1 x 65536 tokens: 16 heads on one
-// key head, 128 parts, 36 us; 8 on two 26; 1 x 262144: 68 and 54, their bytes
-// 22 and 44).
-constexpr int kOneChunk = 16;
-__device__ __forceinline__ int chunks_of(int tiles, int size) {
-  if (tiles <= kOneChunk) return 1;
-  size = max(size, tiles <= 32 ? 4 : tiles <= 128 ? 8 : 16);
-  return (tiles + size - 1) / size;
-}
-
-__device__ __forceinline__ int both_counts(int chunks) {
-  return chunks | (chunks > 1 ? chunks << 16 : 0);
-}
-
 __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item& it) {
   const int lane = threadIdx.x & 63;
   const int H = p.kv_heads * p.head_blocks;
@@ -227,273 +119,6 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item& 
   return true;
 }
 
-// ---------------------------------------------------------------------------
-// Element types of the products: q.k in the type of q, the probabilities and
-// values in the cache's 16-bit type (fp16 for E4M3, whose values fp16 holds).
-// ---------------------------------------------------------------------------
-template <class T>
-struct Mma;
-template <>
-struct Mma<F16> {
-  using op = f16x8;
-  // a probability is at most 2^(7 + kSlack) = 2^15, inside fp16, and fp16's
-  // subnormals begin at 2^-21 of the maximum
-  static constexpr float lift = 7.0f;
-  static __device__ __forceinline__ f32x4 mul(op a, op b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ op split(const float (&v)[8], float (&rest)[8]) {
-    op r;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      r[i] = (_Float16)v[i];
-      rest[i] = v[i] - (float)r[i];
-    }
-    return r;
-  }
-  // four e4m3 bytes -> four values
-  static __device__ __forceinline__ void widen(uint32_t w, uint32_t* out) {
-    out[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
-    out[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true));
-  }
-};
-template <>
-struct Mma<BF16> {
-  using op = bf16x8;
-  // a probability is at most 1, so that the largest bfloat16 values stay
-  // inside fp32
-  static constexpr float lift = -8.0f;
-  static __device__ __forceinline__ f32x4 mul(op a, op b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ op split(const float (&v)[8], float (&rest)[8]) {
-    op r;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      r[i] = (__bf16)v[i];
-      rest[i] = v[i] - (float)r[i];
-    }
-    return r;
-  }
-  static __device__ __forceinline__ void widen(uint32_t w, uint32_t* out) {
-    out[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
-    out[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
-  }
-};
-template <class T, class C>
-struct ValueType {
-  using type = C;
-};
-template <class T>
-struct ValueType<T, E4M3> {
-  using type = F16;
-};
-
-template <int BYTES>
-__device__ __forceinline__ void load_bytes(const uint8_t* p, uint32_t* out) {
-  if constexpr (BYTES == 16) {
-    const u32x4 v = *reinterpret_cast<const u32x4*>(p);
-    out[0] = v.x, out[1] = v.y, out[2] = v.z, out[3] = v.w;
-  } else if constexpr (BYTES == 8) {
-    const u32x2 v = *reinterpret_cast<const u32x2*>(p);
-    out[0] = v.x, out[1] = v.y;
-  } else if constexpr (BYTES == 4) {
-    out[0] = *reinterpret_cast<const uint32_t*>(p);
-  } else {
-    static_assert(BYTES == 2, "load_bytes: 2, 4, 8 or 16");
-    out[0] = *reinterpret_cast<const uint16_t*>(p);
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Registers of a tile.  Both products of a tile are 16x16x32 matrix
-// operations whose operands need no move between lanes:
-//   S^T = K Q^T: rows are 16 tokens, columns the query heads, K = 32 of the
-//     head's values.  Lane (r = lane % 16, g = lane / 16) gives K row r,
-//     values 32 step + 8 g .. + 7 (one 16-byte load; 8-bit caches: one
-//     16-byte load at 64 u + 16 g covers the steps 2 u and 2 u + 1), and Q
-//     the same values of head r.  It gets the scores of head r (= column)
-//     and tokens 4 g .. 4 g + 3 of the 16.
-//   O^T = V^T P^T: rows are head values, columns the query heads, K = the
-//     tile's 32 tokens.  The order of K is free, so the lane's eight are the
-//     tokens whose scores it has: 4 g + i and 16 + 4 g + i.  It loads those
-//     eight rows of V, values r * PL .. of each (16 lanes read a whole row),
-//     and pairs the halves of two tokens' words by byte permutes: operation
-//     c has the row values c of every lane's PL = D / 16.
-// So the softmax needs lane moves only to join maxima, and the accumulator
-// of head r sits with its maximum and sum in the same lanes.
-// ---------------------------------------------------------------------------
-template <class T, class C, int D>
-struct Tile {
-  using V = typename ValueType<T, C>::type;
-  static constexpr int ES = sizeof(typename C::bits_t);  // bytes of a cached value
-  static constexpr int Steps = D / 32;
-  static constexpr int PL = D / 16;  // row values of V per lane
-  // V's two loads per row: E0 values (the largest power of two that one
-  // load holds), then E1
-  static constexpr int E0 = ES == 1 ? (PL >= 16 ? 16 : PL >= 8 ? 8 : 4) : (PL >= 8 ? 8 : 4);
-  static constexpr int E1 = PL - E0;
-  static constexpr int W0 = E0 * ES / 4, W1 = (E1 * ES + 3) / 4;
-  static constexpr int KW = D * ES / 4 / 4;  // words of a K row per lane
-  static constexpr int Row = D * ES;         // bytes of a cached row
-
-  uint32_t k[2][KW];
-  uint32_t v[8][W0 + W1];
-
-  __device__ __forceinline__ void load_k(const uint8_t* const (&base)[2], int lane) {
-    const int r = lane & 15, g = lane >> 4;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint8_t* row = base[j];
-      const uint32_t at = r * Row + (ES == 2 ? 16 * g : 0);
-      if constexpr (ES == 2) {
-#pragma unroll
-        for (int s = 0; s < Steps; ++s) load_bytes<16>(row + at + 64 * s, &k[j][4 * s]);
-      } else {
-#pragma unroll
-        for (int u = 0; u < D / 64; ++u) load_bytes<16>(row + (at + 16 * g) + 64 * u, &k[j][4 * u]);
-        if constexpr (D % 64) load_bytes<8>(row + (at + 8 * g) + (D / 64) * 64, &k[j][4 * (D / 64)]);
-      }
-    }
-  }
-  __device__ __forceinline__ void load_v(const uint8_t* const (&base)[2], int lane) {
-    const int r = lane & 15, g = lane >> 4;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint8_t* row = base[e >> 2];
-      const uint32_t at = 4 * g * Row;
-      load_bytes<E0 * ES>(row + (at + r * (E0 * ES)) + (e & 3) * Row, &v[e][0]);
-      if constexpr (E1 > 0)
-        load_bytes<E1 * ES>(row + (at + r * (E1 * ES)) + ((e & 3) * Row + 16 * E0 * ES), &v[e][W0]);
-    }
-  }
-  // the head value of operation c in lane row r
-  static __device__ __forceinline__ int dim(int r, int c) {
-    return c < E0 ? r * E0 + c : 16 * E0 + r * E1 + (c - E0);
-  }
-
-  // operand of q.k step s: the values d(s, g, e) of Q or K (see load_k)
-  static __device__ __forceinline__ int q_dim(int s, int g) {
-    if (ES == 2 || 64 * (s / 2) + 64 > D) return 32 * s + 8 * g;
-    return 64 * (s / 2) + 16 * g + 8 * (s % 2);
-  }
-  __device__ __forceinline__ typename Mma<T>::op k_op(int j, int s) const {
-    uint32_t w[4];
-    if constexpr (ES == 2) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = k[j][4 * s + i];
-    } else {
-      Mma<T>::widen(k[j][2 * s], w);
-      Mma<T>::widen(k[j][2 * s + 1], w + 2);
-    }
-    typename Mma<T>::op r;
-    __builtin_memcpy(&r, w, 16);
-    return r;
-  }
-  // operand of operations c and c + 1 (c even): tokens e of their row values
-  __device__ __forceinline__ void v_ops(int c, typename Mma<V>::op& a, typename Mma<V>::op& b) const {
-    uint32_t lo[4], hi[4];
-    const int in = c < E0 ? c : c - E0, base = c < E0 ? 0 : W0;
-    if constexpr (ES == 2) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t x = v[2 * i][base + in / 2], y = v[2 * i + 1][base + in / 2];
-        lo[i] = __builtin_amdgcn_perm(y, x, 0x05040100u);
-        hi[i] = __builtin_amdgcn_perm(y, x, 0x07060302u);
-      }
-    } else {
-      // bytes (x.c, y.c, x.c+1, y.c+1), then each pair to fp16
-      const uint32_t sel = in % 4 == 0 ? 0x05010400u : 0x07030602u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t x = v[2 * i][base + in / 4], y = v[2 * i + 1][base + in / 4];
-        uint32_t w[2];
-        Mma<V>::widen(__builtin_amdgcn_perm(y, x, sel), w);
-        lo[i] = w[0], hi[i] = w[1];
-      }
-    }
-    __builtin_memcpy(&a, lo, 16);
-    __builtin_memcpy(&b, hi, 16);
-  }
-};
-
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// A maximum is raised only where a score passes it by more than kSlack (in
-// powers of two), so most tiles need no lane moves and no rescaling.
-// Probabilities are kept 2^lift times their value, at most 2^(lift + kSlack)
-// (Mma::lift).
-constexpr float kSlack = 8.0f;
-
-// Floats of a part: rows of D accumulators, then each row's maximum and sum.
-__host__ __device__ constexpr int64_t part_floats(int64_t rows, int64_t D) {
-  return (rows * (D + 2) + 3) / 4 * 4;
-}
-// Chunks of a sequence at most (the items of one sequence and head block,
-// about target_items of which there are kMaxItems at most).
-constexpr int kMaxItems = 256, kMaxChunks = kMaxItems + 1;
-
-// The parts pass from one workgroup to another, maybe on another die with
-// its own L2, by stores and loads that go through to the memory all dies
-// share (relaxed atomics of device scope).  Plain stores with a fence would
-// write back and drop a die's whole L2 for every workgroup: 2 us each, one
-// after the other (1 x 262144 tokens in 512 workgroups: 283 us).
-__device__ __forceinline__ void put2(float* p, float a, float b) {
-  const uint64_t v = (uint64_t)__float_as_uint(a) | ((uint64_t)__float_as_uint(b) << 32);
-  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ uint64_t get2(const float* p) {
-  return __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-
-// Infinite values.  A visible one makes its element infinite (NaN where both
-// signs or a NaN meet), but times a 16-bit term that is zero or negative, or
-// a weight that has become zero, it is NaN.  So an element that came out NaN
-// from scores that are numbers is decided again, from the infinite and NaN
-// values alone: their sum is what the element is.  (1 x 500 tokens: 9.10 us
-// without, 9.28 with the pass over the values inlined among the code that
-// every launch fetches, 9.13 with it called; 1 x 262144 tokens of infinite
-// values 1.4 ms instead of 0.19.)
-__device__ __forceinline__ bool any_nan(const f32x4& o) {
-  return __builtin_isunordered(o[0], o[1]) | __builtin_isunordered(o[2], o[3]);
-}
-__device__ __forceinline__ float not_finite(float v) { return fabsf(v) < INFINITY ? 0.0f : v; }
-__device__ __forceinline__ void take_infinite(f32x4& o, const f32x4& s) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (o[i] != o[i] && fabsf(s[i]) == INFINITY) o[i] = s[i];
-}
-// Values d .. d + 3 of the visible tokens first .. end - 1 (at least one;
-// 16-bit caches: E4M3 has no infinity), by one thread, eight tokens in flight
-// (past the end the last one again, which changes no such sum).
-template <class C, int D>
-__device__ __attribute__((noinline)) f32x4 infinite_values(const int32_t* table, const uint16_t* v_cache, int pages,
-                                                           int kv_heads, int kh, int page_shift, int first, int end,
-                                                           int d) {
-  constexpr int kFlight = 8;
-  f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-  for (int t0 = first; t0 < end; t0 += kFlight) {
-    u32x2 v[kFlight];
-    bool in[kFlight];
-#pragma unroll
-    for (int j = 0; j < kFlight; ++j) {
-      const int t = min(t0 + j, end - 1);
-      const int page = table[t >> page_shift];
-      in[j] = page >= 0 && page < pages;
-      const int64_t cell = (((int64_t)(in[j] ? page : 0) * kv_heads + kh) << page_shift) + (t & ((1 << page_shift) - 1));
-      v[j] = *reinterpret_cast<const u32x2*>(v_cache + cell * D + d);
-    }
-#pragma unroll
-    for (int j = 0; j < kFlight; ++j) {
-      if (!in[j]) continue;
-      s[0] += not_finite(C::value((uint16_t)v[j].x));
-      s[1] += not_finite(C::value((uint16_t)(v[j].x >> 16)));
-      s[2] += not_finite(C::value((uint16_t)v[j].y));
-      s[3] += not_finite(C::value((uint16_t)(v[j].y >> 16)));
-    }
-  }
-  return s;
-}
 // Four accumulators of every part of a sequence.
 __device__ __forceinline__ f32x4 infinite_parts(const float* at, int64_t step, int chunks) {
   f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -525,6 +150,55 @@ __device__ __forceinline__ void store_out(const AttnParams& p, int b, int h, int
     p.lse[(int64_t)b * p.q_heads + h] = none ? -INFINITY : (m + (__builtin_amdgcn_logf(l) - Mma<V>::lift)) * kLn2;
 }
 
+// The parts of the prefix that sequence b shares (bgg_shared.hip), with the
+// accumulator, maximum and sum of values d .. d + 3 of head i of key head kh.
+template <int D>
+__device__ __forceinline__ void add_prefix(const AttnParams& p, int b, int kh, int i, int d, f32x4& o, float& m,
+                                           float& l) {
+  constexpr int kFlight = 4, RowF = D + 4;
+  const SharedSeq q = p.seqs[b];
+  const float* at = p.prefix_parts + ((int64_t)q.row + (int64_t)kh * q.rows + i) * RowF;
+  const int64_t step = (int64_t)p.kv_heads * q.rows * RowF;
+  const f32x4 own = o;
+#pragma unroll 1
+  for (int c0 = 0; c0 < q.chunks; c0 += kFlight) {
+    f32x4 x[kFlight];
+    float2 ml[kFlight];
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j) {
+      const float* row = at + min(c0 + j, q.chunks - 1) * step;
+      x[j] = *reinterpret_cast<const f32x4*>(row + d);
+      ml[j] = *reinterpret_cast<const float2*>(row + D);
+    }
+    float mn = m;
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j) mn = fmaxf(mn, ml[j].x);
+    const float f = __builtin_amdgcn_exp2f(m - mn);
+    o *= f;
+    l *= f;
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j) {
+      // (a part past the last is left out by selects: its values may be infinite)
+      const bool in = c0 + j < q.chunks;
+      const float w = __builtin_amdgcn_exp2f(ml[j].x - mn);
+      l = in ? fmaf(ml[j].y, w, l) : l;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = in ? fmaf(x[j][k], w, o[k]) : o[k];
+    }
+    m = mn;
+  }
+  if (__builtin_expect(__any(any_nan(o)), false) && any_nan(o) && l == l) {
+    f32x4 s = {not_finite(own[0]), not_finite(own[1]), not_finite(own[2]), not_finite(own[3])};
+#pragma unroll 1
+    for (int c = 0; c < q.chunks; ++c) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(at + c * step + d);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] += not_finite(x[k]);
+    }
+    take_infinite(o, s);
+  }
+}
+
 // The parts of a sequence's chunks (at parts, parts + step, ...) into its
 // output: each chunk's weight 2^(m_c - m), then the weighted rows, four
 // values (a column) per thread and step; with fewer columns than threads the
@@ -534,7 +208,7 @@ __device__ __forceinline__ void store_out(const AttnParams& p, int b, int h, int
 // block, so its instructions come from memory too: it is kept short by loops
 // (unrolled to 16 parts in flight and three columns per thread it took 9 us
 // for 32 chunks of 6 x 128).  `lds` holds 32 kMaxChunks floats.
-template <class T, class V, int D>
+template <class T, class V, int D, bool SHARED>
 __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, const float* parts,
                                            int64_t step, int rows, int heads, int h0, float vs,
                                            float* lds, float* lds16) {
@@ -597,7 +271,12 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
     const int h = col / (D / 4);
     if (__builtin_expect(__any(any_nan(o)), false) && any_nan(o) && heads_l[h] == heads_l[h])
       take_infinite(o, infinite_parts(parts + 4 * col, step, it.chunks));
-    store_out<T, V>(p, it.b, h0 + h, D, 4 * (col % (D / 4)), o, heads_m[h], heads_l[h], vs);
+    float m = heads_m[h], l = heads_l[h];
+    if constexpr (SHARED) {
+      const int kh = it.head_block / p.head_blocks;
+      add_prefix<D>(p, it.b, kh, h0 + h - kh * p.group, 4 * (col % (D / 4)), o, m, l);
+    }
+    store_out<T, V>(p, it.b, h0 + h, D, 4 * (col % (D / 4)), o, m, l, vs);
   };
 
   f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -643,8 +322,10 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
 // One workgroup per item: its waves take the chunk's tiles in turn, each
 // with its own maximum, sum and accumulator; joined through LDS, then, where
 // a sequence has several chunks, through the workspace: the workgroup that
-// arrives last adds the parts in chunk order.
-template <class T, class C, int D>
+// arrives last adds the parts in chunk order.  SHARED: the items are
+// bgg_shared.hip's, of the sequences' own tokens, and the parts of the prefix
+// join at the end.
+template <class T, class C, int D, bool SHARED>
 __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 384 ? 1 : 2) k_paged_attention(AttnParams p) {
   using TL = Tile<T, C, D>;
   using V = typename TL::V;
@@ -659,7 +340,14 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
   __shared__ uint32_t arrived;
 
   Item it;
-  if (!find_item(p, blockIdx.x, it)) return;
+  if constexpr (SHARED) {
+    const int H = p.kv_heads * p.head_blocks, at = blockIdx.x / H;
+    if (at >= *p.own_count) return;
+    const OwnItem e = p.own_items[at];
+    it = Item{e.b, (int)blockIdx.x % H, e.chunk, e.chunks, e.part, e.lo, e.n, e.tile, e.tile_end};
+  } else {
+    if (!find_item(p, blockIdx.x, it)) return;
+  }
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kh = it.head_block / p.head_blocks, hb = it.head_block % p.head_blocks;
@@ -825,6 +513,7 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
                                                p.page_shift, max(it.lo, it.tile * kTokens), end, d));
       }
     if (it.chunks == 1) {
+      if constexpr (SHARED) add_prefix<D>(p, it.b, kh, hb * kHeads + h, d, o, mh, lh);
       store_out<T, V>(p, it.b, h0 + h, D, d, o, mh, lh, vs);
     } else {
       put2(part + h * D + d, o[0], o[1]);
@@ -845,7 +534,7 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
   __syncthreads();
   if (arrived != (uint32_t)it.chunks - 1) return;
   if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  join_parts<T, V, D>(p, it, part - (int64_t)it.chunk * H * slot, H * slot, rows, heads, h0, vs,
+  join_parts<T, V, D, SHARED>(p, it, part - (int64_t)it.chunk * H * slot, H * slot, rows, heads, h0, vs,
                    lds, red_j);
 }
 
@@ -879,37 +568,61 @@ AttnPlan plan_attention(const bgg_cache_desc* c, int64_t q_heads, int64_t batch)
   return p;
 }
 
-template <class T, class C>
+template <class T, class C, bool SHARED>
 void launch_dim(const AttnParams& p, int64_t items, int64_t head_dim, hipStream_t s) {
   const dim3 grid((unsigned)items), block(64 * kWaves);
   switch (head_dim) {
-    case 64: hipLaunchKernelGGL((k_paged_attention<T, C, 64>), grid, block, 0, s, p); break;
-    case 96: hipLaunchKernelGGL((k_paged_attention<T, C, 96>), grid, block, 0, s, p); break;
-    case 128: hipLaunchKernelGGL((k_paged_attention<T, C, 128>), grid, block, 0, s, p); break;
-    case 192: hipLaunchKernelGGL((k_paged_attention<T, C, 192>), grid, block, 0, s, p); break;
-    default: hipLaunchKernelGGL((k_paged_attention<T, C, 256>), grid, block, 0, s, p); break;
+    case 64: hipLaunchKernelGGL((k_paged_attention<T, C, 64, SHARED>), grid, block, 0, s, p); break;
+    case 96: hipLaunchKernelGGL((k_paged_attention<T, C, 96, SHARED>), grid, block, 0, s, p); break;
+    case 128: hipLaunchKernelGGL((k_paged_attention<T, C, 128, SHARED>), grid, block, 0, s, p); break;
+    case 192: hipLaunchKernelGGL((k_paged_attention<T, C, 192, SHARED>), grid, block, 0, s, p); break;
+    default: hipLaunchKernelGGL((k_paged_attention<T, C, 256, SHARED>), grid, block, 0, s, p); break;
   }
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t bgg_attention_workspace_size(const bgg_cache_desc* c, int64_t q_heads, int64_t batch) {
-  if (check_cache(c) != BGG_OK || q_heads < 1 || q_heads > kMaxQHeads || q_heads % c->kv_heads ||
-      batch < 1 || batch > kMaxBatch)
-    return 0;
-  return (size_t)plan_attention(c, q_heads, batch).total_bytes;
+template <bool SHARED>
+void launch_attention(const AttnParams& p, int64_t items, int32_t type, bool e4m3, int64_t head_dim, hipStream_t s) {
+  if (type == BGG_TYPE_F16) {
+    if (e4m3)
+      launch_dim<F16, E4M3, SHARED>(p, items, head_dim, s);
+    else
+      launch_dim<F16, F16, SHARED>(p, items, head_dim, s);
+  } else {
+    if (e4m3)
+      launch_dim<BF16, E4M3, SHARED>(p, items, head_dim, s);
+    else
+      launch_dim<BF16, BF16, SHARED>(p, items, head_dim, s);
+  }
 }
 
-bgg_status bgg_paged_attention(const bgg_cache_desc* c, const bgg_attention_args* a, void* stream) {
-  bgg_status st = check_attention(c, a);
-  if (st) return st;
+// What bgg_shared_attention's workspace holds behind bgg_paged_attention's.
+struct SharedPlan {
+  uint64_t items, seqs, parts, total_bytes;  // byte offsets
+};
+SharedPlan plan_shared(const bgg_cache_desc* c, int64_t q_heads, int64_t batch) {
+  SharedPlan p;
+  p.items = plan_attention(c, q_heads, batch).total_bytes + 256;  // (the count before it)
+  p.seqs = p.items + align256((kMaxItems + batch) * sizeof(OwnItem));
+  p.parts = p.seqs + align256(batch * sizeof(SharedSeq));
+  p.total_bytes = p.parts + align256(4 * (uint64_t)prefix_part_floats(c, q_heads, batch, kMaxItems));
+  return p;
+}
+
+bool sizes_ok(const bgg_cache_desc* c, int64_t q_heads, int64_t batch) {
+  return check_cache(c) == BGG_OK && q_heads >= 1 && q_heads <= kMaxQHeads && q_heads % c->kv_heads == 0 && batch >= 1 &&
+         batch <= kMaxBatch;
+}
+
+// The call, its arguments checked; shared: nullptr without groups.
+bgg_status attend(const char* who, const bgg_cache_desc* c, const bgg_attention_args* a, const bgg_shared_args* shared,
+                  void* stream) {
   if (a->batch == 0) return BGG_OK;
   const AttnPlan plan = plan_attention(c, a->q_heads, a->batch);
-  if (a->workspace_bytes < plan.total_bytes)
-    return fail(BGG_ERR_BUFFER, "bgg_paged_attention: workspace has %zu bytes, needs %llu",
-                a->workspace_bytes, (unsigned long long)plan.total_bytes);
+  const SharedPlan more = shared ? plan_shared(c, a->q_heads, a->batch) : SharedPlan{};
+  const uint64_t need = shared ? more.total_bytes : plan.total_bytes;
+  if (a->workspace_bytes < need)
+    return fail(BGG_ERR_BUFFER, "%s: workspace has %zu bytes, needs %llu", who, a->workspace_bytes,
+                (unsigned long long)need);
   AttnParams p{};
   p.q = (const uint16_t*)a->q_dev;
   p.out = (uint16_t*)a->out_dev;
@@ -936,20 +649,49 @@ bgg_status bgg_paged_attention(const bgg_cache_desc* c, const bgg_attention_args
   p.head_blocks = (int)ceil_div(p.group, kHeads);
   p.page_shift = __builtin_ctzll((unsigned long long)c->page_size);
   p.target_items = (int)plan.target;
-  hipStream_t s = (hipStream_t)stream;
   const bool e4m3 = c->type == BGG_TYPE_E4M3;
-  if (a->type == BGG_TYPE_F16) {
-    if (e4m3)
-      launch_dim<F16, E4M3>(p, plan.items, c->head_dim, s);
-    else
-      launch_dim<F16, F16>(p, plan.items, c->head_dim, s);
-  } else {
-    if (e4m3)
-      launch_dim<BF16, E4M3>(p, plan.items, c->head_dim, s);
-    else
-      launch_dim<BF16, BF16>(p, plan.items, c->head_dim, s);
+  hipStream_t s = (hipStream_t)stream;
+  if (!shared || shared->groups == 0) {
+    launch_attention<false>(p, plan.items, a->type, e4m3, c->head_dim, s);
+    return hip_check(who);
   }
-  return hip_check("bgg_paged_attention");
+  uint8_t* const w = (uint8_t*)a->workspace;
+  p.group_starts = shared->group_starts_dev;
+  p.shared_pages = shared->shared_pages_dev;
+  p.groups = (int)shared->groups;
+  p.prefix_target = (int)plan.target;
+  p.own_count = (int32_t*)(w + more.items - 256);
+  p.own_items = (OwnItem*)(w + more.items);
+  p.seqs = (SharedSeq*)(w + more.seqs);
+  p.prefix_parts = (float*)(w + more.parts);
+  launch_prefix(p, a->type, e4m3, c->head_dim, s);
+  const bgg_status st = hip_check(who);
+  if (st) return st;
+  launch_attention<true>(p, plan.items, a->type, e4m3, c->head_dim, s);
+  return hip_check(who);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t bgg_attention_workspace_size(const bgg_cache_desc* c, int64_t q_heads, int64_t batch) {
+  return sizes_ok(c, q_heads, batch) ? (size_t)plan_attention(c, q_heads, batch).total_bytes : 0;
+}
+
+bgg_status bgg_paged_attention(const bgg_cache_desc* c, const bgg_attention_args* a, void* stream) {
+  const bgg_status st = check_attention(c, a);
+  return st ? st : attend("bgg_paged_attention", c, a, nullptr, stream);
+}
+
+size_t bgg_shared_attention_workspace_size(const bgg_cache_desc* c, int64_t q_heads, int64_t batch) {
+  return sizes_ok(c, q_heads, batch) ? (size_t)plan_shared(c, q_heads, batch).total_bytes : 0;
+}
+
+bgg_status bgg_shared_attention(const bgg_cache_desc* c, const bgg_attention_args* a, const bgg_shared_args* shared,
+                                void* stream) {
+  const bgg_status st = check_shared(c, a, shared);
+  return st ? st : attend("bgg_shared_attention", c, a, shared, stream);
 }
 
 }  // extern "C"

@@ -153,8 +153,7 @@ static bool heads_ok(const bgg_cache_desc* c, int64_t q_heads) {
   return q_heads >= 1 && q_heads <= kMaxQHeads && q_heads % c->kv_heads == 0;
 }
 
-bgg_status check_attention(const bgg_cache_desc* c, const bgg_attention_args* a) {
-  const char* who = "bgg_paged_attention";
+static bgg_status check_attention(const char* who, const bgg_cache_desc* c, const bgg_attention_args* a) {
   bgg_status st = check_cache(c);
   if (st) return st;
   if (!a) return fail(BGG_ERR_NULL, "%s: NULL arguments", who);
@@ -183,6 +182,24 @@ bgg_status check_attention(const bgg_cache_desc* c, const bgg_attention_args* a)
   if ((st = check_rows(who, "out", a->out_dev, a->out_stride, a->q_heads * c->head_dim))) return st;
   if (a->out_dev == a->q_dev && a->out_stride != a->q_stride && a->batch > 1)
     return fail(BGG_ERR_SHAPE, "%s: out in the place of q with two strides", who);
+  return BGG_OK;
+}
+
+bgg_status check_attention(const bgg_cache_desc* c, const bgg_attention_args* a) {
+  return check_attention("bgg_paged_attention", c, a);
+}
+
+bgg_status check_shared(const bgg_cache_desc* c, const bgg_attention_args* a, const bgg_shared_args* s) {
+  const char* who = "bgg_shared_attention";
+  bgg_status st = check_attention(who, c, a);
+  if (st) return st;
+  if (!s) return fail(BGG_ERR_NULL, "%s: NULL groups", who);
+  if (s->groups < 0 || s->groups > a->batch)
+    return fail(BGG_ERR_SHAPE, "%s: %lld groups of %lld sequences", who, (long long)s->groups, (long long)a->batch);
+  if (s->groups == 0) return BGG_OK;
+  if (!s->group_starts_dev || !s->shared_pages_dev) return fail(BGG_ERR_NULL, "%s: NULL buffer", who);
+  if (!aligned(s->group_starts_dev, 4) || !aligned(s->shared_pages_dev, 4))
+    return fail(BGG_ERR_BUFFER, "%s: misaligned buffer", who);
   return BGG_OK;
 }
 

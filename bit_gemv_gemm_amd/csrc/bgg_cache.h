@@ -17,5 +17,6 @@ bgg_status check_rotary_axes(const bgg_cache_desc* c, const bgg_rotary_args* a,
                              const bgg_rotary_axes_args* x);
 bgg_status check_assign(const bgg_cache_desc* c, const bgg_assign_args* a);
 bgg_status check_attention(const bgg_cache_desc* c, const bgg_attention_args* a);
+bgg_status check_shared(const bgg_cache_desc* c, const bgg_attention_args* a, const bgg_shared_args* s);
 
 }  // namespace bgg

@@ -7,11 +7,13 @@ namespace bgg {
 // Tags of the element types; bits() stores one value, value() reads one.
 struct F16 {
   using bits_t = uint16_t;
+  static constexpr uint16_t exponent = 0x7C00;  // all ones: infinite or NaN
   static __device__ __forceinline__ float value(uint16_t b) { return h2f(b); }
   static __device__ __forceinline__ uint16_t bits(float v) { return f2h(v); }
 };
 struct BF16 {
   using bits_t = uint16_t;
+  static constexpr uint16_t exponent = 0x7F80;
   static __device__ __forceinline__ float value(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
   static __device__ __forceinline__ uint16_t bits(float v) {
     return __builtin_bit_cast(uint16_t, (__bf16)v);

@@ -25,6 +25,7 @@ decltype(&bgg_paged_attention) p_attention;
 decltype(&bgg_rotary_append) p_rotary;
 decltype(&bgg_rotary_append_axes) p_rotary_axes;
 decltype(&bgg_cache_assign) p_assign;
+decltype(&bgg_shared_attention) p_shared;
 decltype(&bgg_ternary_gemv_epilogue) p_gemv;
 decltype(&bgg_gemv_run_epilogue) p_run;
 decltype(&bgg_ternary_gemm_epilogue) p_gemm;
@@ -167,44 +168,57 @@ void cache_buffers(const Cache& c, PyObject* k, PyObject* v, int dev, void** kp,
   *vp = vector(v, n, t, dev, "v_cache");
 }
 
-// (cache, k_cache, v_cache, page_table, lengths, q, out, workspace, scale, window, lse, k_scale, v_scale, stream)
+// (cache, k_cache, v_cache, page_table, lengths, q, out, workspace, scale, window, lse, k_scale, v_scale, stream),
+// with shared prefixes (group_starts, shared_pages, stream) at the end
+PyObject* attention(PyObject* const* a, bool with_groups) {
+  Cache c(a[0], "cache");
+  const at::Tensor& q = tensor(a[5], "q");
+  const int dev = device_of(q, "q");
+  bgg_attention_args g{};
+  g.type = type_of(q, "q");
+  g.batch = q.dim() ? q.size(0) : 0;
+  const Rows rq = rows(a[5], g.batch, c->head_dim, q.scalar_type(), dev, "q");
+  const Rows ro = rows(a[6], g.batch, c->head_dim, q.scalar_type(), dev, "out");
+  if (ro.heads != rq.heads) refuse("out", "must have q's heads");
+  g.q_heads = rq.heads;
+  g.q_dev = rq.data, g.q_stride = rq.stride;
+  g.out_dev = ro.data, g.out_stride = ro.stride;
+  void *kc, *vc;
+  cache_buffers(c, a[1], a[2], dev, &kc, &vc);
+  g.k_cache_dev = kc, g.v_cache_dev = vc;
+  const at::Tensor& t = tensor(a[3], "page_table");
+  if (!t.is_cuda() || t.get_device() != dev || t.scalar_type() != at::kInt || t.dim() != 2 ||
+      t.size(0) != g.batch || (t.size(1) > 1 && t.stride(1) != 1))
+    refuse("page_table", "must be int32 [batch, pages] with contiguous rows on q's device");
+  g.page_table_dev = (const int32_t*)t.data_ptr();
+  g.table_width = t.size(1);
+  g.table_stride = g.batch > 1 ? t.stride(0) : t.size(1);
+  g.lengths_dev = (const int32_t*)vector(a[4], g.batch, at::kInt, dev, "lengths");
+  uint64_t size;
+  g.workspace = bytes(a[7], 0, dev, "workspace", &size);
+  g.workspace_bytes = size;
+  g.scale = (float)number(a[8]);
+  g.window = integer(a[9]);
+  g.lse_dev = (float*)vector(a[10], g.batch * g.q_heads, at::kFloat, dev, "lse");
+  g.k_scale_dev = (const float*)vector(a[11], c->kv_heads, at::kFloat, dev, "k_scale");
+  g.v_scale_dev = (const float*)vector(a[12], c->kv_heads, at::kFloat, dev, "v_scale");
+  bgg_shared_args sh{};
+  if (with_groups) {
+    sh.groups = tensor(a[13], "group_starts").numel() - 1;
+    sh.group_starts_dev = (const int32_t*)vector(a[13], 1, at::kInt, dev, "group_starts");
+    tensor(a[14], "shared_pages");  // (None is refused)
+    sh.shared_pages_dev = (const int32_t*)vector(a[14], g.batch, at::kInt, dev, "shared_pages");
+  }
+  if (g.batch == 0) return PyLong_FromLong(0);  // (empty tensors have no pointers)
+  void* stream = (void*)(uintptr_t)integer(a[with_groups ? 15 : 13]);
+  if (with_groups) return status_of([&] { return p_shared(c.get(), &g, &sh, stream); });
+  return status_of([&] { return p_attention(c.get(), &g, stream); });
+}
 PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded("paged_attention", n, 14, [&]() -> PyObject* {
-    Cache c(a[0], "cache");
-    const at::Tensor& q = tensor(a[5], "q");
-    const int dev = device_of(q, "q");
-    bgg_attention_args g{};
-    g.type = type_of(q, "q");
-    g.batch = q.dim() ? q.size(0) : 0;
-    const Rows rq = rows(a[5], g.batch, c->head_dim, q.scalar_type(), dev, "q");
-    const Rows ro = rows(a[6], g.batch, c->head_dim, q.scalar_type(), dev, "out");
-    if (ro.heads != rq.heads) refuse("out", "must have q's heads");
-    g.q_heads = rq.heads;
-    g.q_dev = rq.data, g.q_stride = rq.stride;
-    g.out_dev = ro.data, g.out_stride = ro.stride;
-    void *kc, *vc;
-    cache_buffers(c, a[1], a[2], dev, &kc, &vc);
-    g.k_cache_dev = kc, g.v_cache_dev = vc;
-    const at::Tensor& t = tensor(a[3], "page_table");
-    if (!t.is_cuda() || t.get_device() != dev || t.scalar_type() != at::kInt || t.dim() != 2 ||
-        t.size(0) != g.batch || (t.size(1) > 1 && t.stride(1) != 1))
-      refuse("page_table", "must be int32 [batch, pages] with contiguous rows on q's device");
-    g.page_table_dev = (const int32_t*)t.data_ptr();
-    g.table_width = t.size(1);
-    g.table_stride = g.batch > 1 ? t.stride(0) : t.size(1);
-    g.lengths_dev = (const int32_t*)vector(a[4], g.batch, at::kInt, dev, "lengths");
-    uint64_t size;
-    g.workspace = bytes(a[7], 0, dev, "workspace", &size);
-    g.workspace_bytes = size;
-    g.scale = (float)number(a[8]);
-    g.window = integer(a[9]);
-    g.lse_dev = (float*)vector(a[10], g.batch * g.q_heads, at::kFloat, dev, "lse");
-    g.k_scale_dev = (const float*)vector(a[11], c->kv_heads, at::kFloat, dev, "k_scale");
-    g.v_scale_dev = (const float*)vector(a[12], c->kv_heads, at::kFloat, dev, "v_scale");
-    if (g.batch == 0) return PyLong_FromLong(0);  // (empty tensors have no pointers)
-    void* stream = (void*)(uintptr_t)integer(a[13]);
-    return status_of([&] { return p_attention(c.get(), &g, stream); });
-  });
+  return guarded("paged_attention", n, 14, [&] { return attention(a, false); });
+}
+PyObject* shared_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("shared_attention", n, 16, [&] { return attention(a, true); });
 }
 
 // (cache, k_cache, v_cache, positions, slots, freqs, q, q_out, k, v, layout, magnitude, k_scale, v_scale, stream),
@@ -352,11 +366,12 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // The addresses of bgg_paged_attention, bgg_rotary_append, bgg_ternary_gemv_epilogue,
-// bgg_gemv_run_epilogue, bgg_ternary_gemm_epilogue, bgg_rotary_append_axes and bgg_cache_assign.
+// bgg_gemv_run_epilogue, bgg_ternary_gemm_epilogue, bgg_rotary_append_axes, bgg_cache_assign and
+// bgg_shared_attention.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded("bind", n, 7, [&]() -> PyObject* {
-    void* p[7];
-    for (int i = 0; i < 7; ++i) p[i] = (void*)(uintptr_t)integer(a[i]);
+  return guarded("bind", n, 8, [&]() -> PyObject* {
+    void* p[8];
+    for (int i = 0; i < 8; ++i) p[i] = (void*)(uintptr_t)integer(a[i]);
     p_attention = (decltype(p_attention))p[0];
     p_rotary = (decltype(p_rotary))p[1];
     p_gemv = (decltype(p_gemv))p[2];
@@ -364,6 +379,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p_gemm = (decltype(p_gemm))p[4];
     p_rotary_axes = (decltype(p_rotary_axes))p[5];
     p_assign = (decltype(p_assign))p[6];
+    p_shared = (decltype(p_shared))p[7];
     Py_RETURN_NONE;
   });
 }
@@ -376,6 +392,7 @@ PyMethodDef methods[] = {{"bind", entry<bind>(), METH_FASTCALL, nullptr},
                          {"paged_attention", entry<paged_attention>(), METH_FASTCALL, nullptr},
                          {"rotary_append", entry<rotary_append>(), METH_FASTCALL, nullptr},
                          {"rotary_append_axes", entry<rotary_append_axes>(), METH_FASTCALL, nullptr},
+                         {"shared_attention", entry<shared_attention>(), METH_FASTCALL, nullptr},
                          {"cache_assign", entry<cache_assign>(), METH_FASTCALL, nullptr},
                          {"product", entry<product>(), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

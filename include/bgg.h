@@ -695,6 +695,44 @@ size_t bgg_attention_workspace_size(const bgg_cache_desc* cache, int64_t q_heads
 bgg_status bgg_paged_attention(const bgg_cache_desc* cache, const bgg_attention_args* args,
                                void* stream);
 
+/* The groups of bgg_shared_attention: sequences group_starts[g] ..
+ * group_starts[g + 1] - 1 of the batch share the pages of their first
+ * shared_pages[group_starts[g]] table entries (cut to 0 .. table_width; the
+ * array is bgg_cache_assign's: a value per sequence, of which a group's first
+ * counts). */
+typedef struct bgg_shared_args {
+  int64_t groups;                  /* 0 <= G <= B */
+  const int32_t* group_starts_dev; /* [G + 1]: starts that rise within 0 .. B (cut to that, and
+                                      a start below an earlier one counts as that one) */
+  const int32_t* shared_pages_dev; /* [B] */
+} bgg_shared_args;
+
+/* Device workspace bytes of bgg_shared_attention for a batch of at most
+ * `batch` sequences (0 as bgg_attention_workspace_size; no page passage). */
+size_t bgg_shared_attention_workspace_size(const bgg_cache_desc* cache, int64_t q_heads,
+                                           int64_t batch);
+
+/*
+ * bgg_paged_attention of a batch whose groups of sequences begin with the
+ * same pages (a system prompt, a document, several samples of one prompt; no
+ * page passage): the same result, but the keys and values of a group's shared
+ * pages are read once for all its sequences.  They are found through the
+ * table of the group's first sequence; the others' entries there are not
+ * read.  Each sequence sees of them what lies below its length (and inside
+ * its window), and then its own tokens; sequences outside every group have
+ * no shared part.
+ * As there, but for the rounding of the shared part: its probabilities enter
+ * their product with the values as one 16-bit term (the type of the values;
+ * fp16 for E4M3), off by half a step of it at most, so an element of out is
+ * off by at most that times sum_t p_t |v_t| over the shared tokens, beside
+ * its own rounding.  Softmax statistics and all sums are fp32.
+ * Workspace as there, of bgg_shared_attention_workspace_size bytes; the two
+ * calls may share one.
+ * Errors: as bgg_paged_attention.
+ */
+bgg_status bgg_shared_attention(const bgg_cache_desc* cache, const bgg_attention_args* args,
+                                const bgg_shared_args* shared, void* stream);
+
 /* Static English name of a status (bookkeeping, no page passage). */
 const char* bgg_status_string(int32_t status);
 

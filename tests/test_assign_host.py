@@ -126,3 +126,37 @@ def test_assign_descriptor():
     assert LIB.bgg_cache_assign(ctypes.byref(d), None, None) == NULL
     d.total_bytes += 1
     assert assign(d) == DESC
+
+
+# --- attention of groups ---------------------------------------------------------
+ATTENTION = dict(type=1, scale=0.1, batch=2, q_heads=4, window=0, q=P, out=P, qs=256, os=256, lse=P, kc=P, vc=P, ksc=0,
+                 vsc=0, table=P, width=4, stride=4, lengths=P, ws=P, wsb=1 << 40)
+SHARED = dict(groups=1, starts=P, shared=P)
+
+
+def shared(desc, attention={}, **change):
+    return LIB.bgg_shared_attention(ctypes.byref(desc), bgg._ATTENTION_ARGS.pack(*dict(ATTENTION, **attention).values()),
+                                    bgg._SHARED_ARGS.pack(*dict(SHARED, **change).values()), None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(groups=-1), SHAPE), (dict(groups=3), SHAPE), (dict(groups=1 << 40), SHAPE), (dict(starts=0), NULL),
+    (dict(shared=0), NULL), (dict(starts=P + 2), BUFFER), (dict(shared=P + 1), BUFFER),
+    (dict(attention=dict(q_heads=3)), SHAPE), (dict(attention=dict(type=2)), FORMAT), (dict(attention=dict(q=0)), NULL),
+    (dict(attention=dict(wsb=1 << 16)), BUFFER), (dict(attention=dict(ws=P + 8)), BUFFER),
+    (dict(groups=0, starts=0, shared=0, attention=dict(wsb=1 << 16)), BUFFER)])
+def test_shared_refusals(change, status):
+    assert shared(describe(), **change) == status
+    assert "bgg_shared_attention" in bgg.bgg_last_error()
+
+
+def test_shared_null_empty_batch_and_workspace():
+    d = describe()
+    assert LIB.bgg_shared_attention(ctypes.byref(d), bgg._ATTENTION_ARGS.pack(*ATTENTION.values()), None, None) == NULL
+    assert LIB.bgg_shared_attention(ctypes.byref(d), None, bgg._SHARED_ARGS.pack(*SHARED.values()), None) == NULL
+    assert shared(d, attention=dict(batch=0), groups=0) == 0
+    assert shared(d, attention=dict(batch=0), groups=1) == SHAPE
+    size = bgg.bgg_shared_attention_workspace_size
+    assert size(d, 4, 1) > bgg.bgg_attention_workspace_size(d, 4, 1)
+    assert size(d, 4, 64) >= size(d, 4, 1)
+    assert size(d, 3, 1) == size(d, 0, 1) == size(d, 4, 0) == size(d, 4, 4097) == 0
