@@ -14,36 +14,85 @@ using namespace bgg;
 
 namespace {
 
-constexpr int kThreads = 64 * kWaves;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+
 constexpr int kGroupsMax = (int)kMaxBatch;
 
-// Sum over the lanes up to and including this one, of larger of the two.
+// The shape of the kernel's work.
+template <class T, class C, int D>
+struct PrefixShape {
+  using TL = Tile<T, C, D>;
+  static constexpr int Row = TL::Row;
+  // Eight waves, two on a SIMD, so that one's matrix operations run beside
+  // the other's exponentials; wide heads do not fit their registers.
+  static constexpr int Waves = D <= 128 ? 8 : 4;
+  static constexpr bool Ahead = Waves == 4;  // a tile's keys are read while the one before is worked on
+  static constexpr int Blocks = 2;  // blocks of 16 rows of a wave (queries, accumulators)
+  static constexpr int Rows = 16 * Blocks;
+  static constexpr int RowF = D + 4;  // floats of a row of the parts: values, maximum, sum
+  // tiles of a step: each wave fetches half a tile; the keys and values of
+  // two steps take up to 128 KB of LDS
+  static constexpr int Subs = Waves / 2;
+  static constexpr int Least = 2;  // row waves at least
+  static constexpr int TileBytes = kTokens * Row;
+  static constexpr int Pieces = Row / 16;                // 16-byte pieces of a row
+  static constexpr int Loads = (16 * Pieces + 63) / 64;  // of a wave: keys (and values) of a step
+  static constexpr int RedDims = D > 128 ? D / 2 : D;    // dimensions that the waves' parts join at a time
+  static constexpr int RedF = RedDims + 4;
+  // In LDS, piece q of row r lies at piece q ^ mix(r) of the row, so that the
+  // rows that are read together lie in different banks (256 bytes hold all
+  // banks once).  Keys: piece q of 16 rows, 8 of them at a time.  Values:
+  // 32 bytes of 16 rows (8-bit: 16 bytes of 32).
+  static __device__ __forceinline__ int mix_k(int r) {
+    return Pieces % 8 == 0 ? r & 7 : Pieces % 4 == 0 ? (r >> 1) & 3 : (r >> 2) & 1;
+  }
+  static __device__ __forceinline__ int mix_v(int r) {
+    if (TL::ES == 2) return Pieces % 16 == 0 ? 2 * (r & 7) : Pieces % 8 == 0 ? 2 * ((r >> 1) & 3) : 2 * ((r >> 2) & 1);
+    return Pieces % 16 == 0 ? r & 15 : Pieces % 8 == 0 ? (r >> 1) & 7 : Pieces % 4 == 0 ? (r >> 2) & 3 : (r >> 3) & 1;
+  }
+};
+
 template <int MOVE, int ROWS>
 __device__ __forceinline__ int max_from(int v) {
   return max(v, __builtin_amdgcn_update_dpp(0, v, MOVE, ROWS, 0xF, false));
 }
 
-// The groups, in LDS: group g has the sequences start[g] .. start[g + 1] - 1,
-// `tokens` tokens of prefix, of which its sequences see lo .. hi - 1.
-struct Groups {
-  int start[kGroupsMax + 1], tokens[kGroupsMax], lo[kGroupsMax], hi[kGroupsMax];
+// The batch, in LDS: sequence b has n[b] tokens and shares pages[b] pages
+// (of which a group's first counts); group g has the sequences start[g] ..
+// start[g + 1] - 1, which see tokens lo .. hi - 1 of its prefix.
+struct Batch {
+  int *n, *pages;  // [kGroupsMax]
+  int *lo, *hi;    // [kGroupsMax]
+  uint16_t* start;  // [kGroupsMax + 1]
+
+  __device__ __forceinline__ int prefix(const AttnParams& p, int g) const { return pages[start[g]] << p.page_shift; }
+  __device__ __forceinline__ int first_seen(const AttnParams& p, int b) const {
+    return p.window > 0 && n[b] > p.window ? n[b] - (int)p.window : 0;
+  }
+  // Largest g <= G - 1 with start[g] <= b (or 0).
+  __device__ __forceinline__ int group_of(int G, int b) const {
+    int g = 0, m = G;
+#pragma unroll 1
+    while (m > 1) {
+      const int half = m >> 1;
+      const bool right = start[g + half] <= b;
+      g = right ? g + half : g;
+      m = right ? m - half : half;
+    }
+    return g;
+  }
 };
 
-// Largest g <= G - 1 with start[g] <= b (start[0] <= b).
-__device__ __forceinline__ int group_of(const Groups& s, int G, int b) {
-  int lo = 0, n = G;
-#pragma unroll 1
-  while (n > 1) {
-    const int half = n >> 1;
-    const bool right = s.start[lo + half] <= b;
-    lo = right ? lo + half : lo;
-    n = right ? n - half : half;
-  }
-  return lo;
-}
-
-__device__ __forceinline__ void read_groups(const AttnParams& p, Groups& s) {
+template <int WAVES>
+__device__ __forceinline__ void read_batch(const AttnParams& p, const Batch& s) {
+  constexpr int kThreads = 64 * WAVES;
   const int tid = threadIdx.x, G = p.groups;
+  for (int b = tid; b < p.batch; b += kThreads) {
+    s.n[b] = min(max(p.lengths[b], 0), p.max_tokens);
+    s.pages[b] = min(max(p.shared_pages[b], 0), p.max_tokens >> p.page_shift);
+  }
+  for (int g = tid; g < G; g += kThreads) s.lo[g] = 0x7FFFFFFF, s.hi[g] = 0;
   // starts below an earlier one count as that one, so that no sequence is in
   // two groups whatever the caller's array holds
   if (tid < 64) {
@@ -58,24 +107,13 @@ __device__ __forceinline__ void read_groups(const AttnParams& p, Groups& s) {
       v = max_from<0x142, 0xA>(v);
       v = max_from<0x143, 0xC>(v);
       v = max(v, before);
-      if (g <= G) s.start[g] = v;
+      if (g <= G) s.start[g] = (uint16_t)v;
       before = __builtin_amdgcn_readlane(v, 63);
     }
   }
   __syncthreads();
-  for (int g = tid; g < G; g += kThreads) {
-    const int b = s.start[g];
-    const int pages = s.start[g + 1] > b ? p.shared_pages[b] : 0;
-    s.tokens[g] = min(max(pages, 0), p.max_tokens >> p.page_shift) << p.page_shift;
-    s.lo[g] = 0x7FFFFFFF;
-    s.hi[g] = 0;
-  }
-  __syncthreads();
   for (int b = s.start[0] + tid; b < s.start[G]; b += kThreads) {
-    int lo, n;
-    visible(p, b, lo, n);
-    const int g = group_of(s, G, b);
-    n = min(n, s.tokens[g]);
+    const int g = s.group_of(G, b), lo = s.first_seen(p, b), n = min(s.n[b], s.prefix(p, g));
     if (lo < n) {
       atomicMin(&s.lo[g], lo);
       atomicMax(&s.hi[g], n);
@@ -84,67 +122,85 @@ __device__ __forceinline__ void read_groups(const AttnParams& p, Groups& s) {
   __syncthreads();
 }
 
-// Chunks of a group's prefix, as even as the even size allows.
-constexpr int kMinTiles = kWaves;
-__device__ __forceinline__ int prefix_chunks(int tiles, int size) {
-  return (tiles + size - 1) / size;
+// Waves of a workgroup on different rows of a group (the others take other
+// tokens): as many as fit the group's blocks of ROWS rows without much of the
+// last workgroup's rows empty, since they share the tiles that one of them
+// loads.
+template <class S>
+__device__ __forceinline__ int row_waves(int rows) {
+  const int units = (rows + S::Rows - 1) / S::Rows;  // waves that work
+  int w = S::Waves;
+#pragma unroll
+  for (; w > S::Least; w >>= 1)
+    if ((units + w - 1) / w * w * 5 <= units * 6) break;
+  return w;
+}
+
+// How a group's prefix is cut: into blocks of rows and chunks of tokens.
+struct Cut {
+  int tiles, rows, waves, blocks, chunks;
+};
+// `size`: tiles times row waves of an item.
+template <class S>
+__device__ __forceinline__ Cut cut_of(const AttnParams& p, const Batch& s, int g, int size) {
+  Cut c;
+  c.tiles = tiles_of(s.lo[g], s.hi[g]);
+  c.rows = (s.start[g + 1] - s.start[g]) * p.group;
+  c.waves = row_waves<S>(c.rows);
+  const int block = S::Rows * c.waves;
+  c.blocks = (c.rows + block - 1) / block;
+  const int each = ((size + c.waves - 1) / c.waves + S::Subs - 1) / S::Subs * S::Subs;
+  c.chunks = (c.tiles + each - 1) / each;
+  return c;
 }
 
 struct PrefixItem {
-  int group, kh, block, chunk, chunks, row;  // row: the group's first row of the parts
+  int group, kh, block, chunk, row;  // row: the group's first row of the parts
+  int waves;
   int tile, tile_end;
 };
 
-// The item of this workgroup; in `base` and `count`, if given, the first row
-// and the chunks of every group.  Every wave works it out by itself.
-template <int RB>
-__device__ __forceinline__ bool find_prefix(const AttnParams& p, const Groups& s, int index, PrefixItem& it, int* base,
-                                            int* count) {
+// The item of workgroup `index`, and in `base`, if given, the first row of
+// every group's parts and the size of an item.  Every wave works it out by
+// itself.
+template <class S>
+__device__ __forceinline__ bool find_prefix(const AttnParams& p, const Batch& s, int index, PrefixItem& it, int* base,
+                                            int* size_out) {
   const int lane = threadIdx.x & 63, G = p.groups;
   const int per = (G + 63) / 64, g0 = min(G, lane * per), g1 = min(G, g0 + per);
-  auto shape = [&](int g, int& tiles, int& blocks, int& rows) {
-    tiles = tiles_of(s.lo[g], s.hi[g]);
-    rows = (s.start[g + 1] - s.start[g]) * p.group;
-    blocks = (rows + RB - 1) / RB;
-  };
   float work = 0.0f;
-  int tiles, blocks, rows;
 #pragma unroll 1
   for (int g = g0; g < g1; ++g) {
-    shape(g, tiles, blocks, rows);
-    work += (float)tiles * (float)blocks;
+    const Cut c = cut_of<S>(p, s, g, 1);
+    work += (float)c.tiles * (float)c.blocks * (float)c.waves;
   }
   const float even = fminf(ceilf(wave_add(work) * (float)p.kv_heads / (float)p.prefix_target * 1.0001f), 1e8f);
-  int size = 0, mine = 0, upto = 0;
+  int size = 0, mine = 0, upto = 0, rows = 0;
 #pragma unroll 1
   for (int k = 8; k <= 16; k += 2) {
-    size = max(kMinTiles, (int)(even * (float)k * 0.125f));
-    mine = 0;
+    size = max(1, (int)(even * (float)k * 0.125f));
+    mine = rows = 0;
 #pragma unroll 1
     for (int g = g0; g < g1; ++g) {
-      shape(g, tiles, blocks, rows);
-      mine += prefix_chunks(tiles, size) * blocks;
+      const Cut c = cut_of<S>(p, s, g, size);
+      mine += c.chunks * c.blocks;
+      rows += c.chunks * p.kv_heads * c.rows;
     }
     upto = scan_add(mine);
     if (__builtin_amdgcn_readlane(upto, 63) * p.kv_heads <= p.prefix_target) break;
   }
   size = __builtin_amdgcn_readfirstlane(size);
-  // rows of the parts before this lane's groups
-  int lane_rows = 0;
+  int row = scan_add(rows) - rows;  // rows of the parts before this lane's groups
+  if (base) {
+    *size_out = size;
+    if (threadIdx.x < 64) {
+      int r = row;
 #pragma unroll 1
-  for (int g = g0; g < g1; ++g) {
-    shape(g, tiles, blocks, rows);
-    lane_rows += prefix_chunks(tiles, size) * p.kv_heads * rows;
-  }
-  int row = scan_add(lane_rows) - lane_rows;
-  if (base && threadIdx.x < 64) {
-    int r = row;
-#pragma unroll 1
-    for (int g = g0; g < g1; ++g) {
-      shape(g, tiles, blocks, rows);
-      base[g] = r;
-      count[g] = prefix_chunks(tiles, size);
-      r += count[g] * p.kv_heads * rows;
+      for (int g = g0; g < g1; ++g) {
+        const Cut c = cut_of<S>(p, s, g, size);
+        base[g] = r;
+        r += c.chunks * p.kv_heads * c.rows;
+      }
     }
   }
   const int at = index / p.kv_heads;
@@ -155,61 +211,67 @@ __device__ __forceinline__ bool find_prefix(const AttnParams& p, const Groups& s
   int first = __builtin_amdgcn_readlane(upto - mine, owner);
   row = __builtin_amdgcn_readlane(row, owner);
   int g = owner * per;
+  Cut c;
 #pragma unroll 1
   for (;; ++g) {
-    shape(g, tiles, blocks, rows);
-    const int n = prefix_chunks(tiles, size) * blocks;
-    if (at < first + n) break;
-    first += n;
-    row += prefix_chunks(tiles, size) * p.kv_heads * rows;
+    c = cut_of<S>(p, s, g, size);
+    if (at < first + c.chunks * c.blocks) break;
+    first += c.chunks * c.blocks;
+    row += c.chunks * p.kv_heads * c.rows;
   }
   it.group = __builtin_amdgcn_readfirstlane(g);
   it.kh = index % p.kv_heads;
   it.row = __builtin_amdgcn_readfirstlane(row);
-  it.chunks = __builtin_amdgcn_readfirstlane(prefix_chunks(tiles, size));
+  it.waves = __builtin_amdgcn_readfirstlane(c.waves);
   const int local = at - first;
-  it.block = __builtin_amdgcn_readfirstlane(local % blocks);
-  it.chunk = __builtin_amdgcn_readfirstlane(local / blocks);
-  const int t0 = s.lo[g] / kTokens, each = (tiles + it.chunks - 1) / it.chunks;
-  it.tile = __builtin_amdgcn_readfirstlane(t0 + it.chunk * each);
-  it.tile_end = __builtin_amdgcn_readfirstlane(t0 + min(tiles, (it.chunk + 1) * each));
+  it.block = __builtin_amdgcn_readfirstlane(local % c.blocks);
+  it.chunk = __builtin_amdgcn_readfirstlane(local / c.blocks);
+  const int t0 = s.lo[g] / kTokens;
+  const int each = ((c.tiles + c.chunks - 1) / c.chunks + S::Subs - 1) / S::Subs * S::Subs;
+  it.tile = __builtin_amdgcn_readfirstlane(t0 + min(c.tiles, it.chunk * each));
+  it.tile_end = __builtin_amdgcn_readfirstlane(t0 + min(c.tiles, (it.chunk + 1) * each));
   return true;
 }
 
-// The schedule of the sequences' own tokens (one workgroup): bgg_attention's
-// chunks, an entry each.
-__device__ __forceinline__ void plan_own(const AttnParams& p, const Groups& s, const int* base, const int* count,
+// The schedule of the sequences' own tokens (one workgroup): chunks as
+// bgg_paged_attention cuts them, an entry each.
+template <class S>
+__device__ __forceinline__ void plan_own(const AttnParams& p, const Batch& s, const int* base, int size_of_prefix,
                                          int* scratch) {
+  constexpr int kThreads = 64 * S::Waves;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int H = p.kv_heads * p.head_blocks, G = p.groups;
   const int per = (p.batch + kThreads - 1) / kThreads, b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
   auto own = [&](int b, int& lo, int& n) {
-    visible(p, b, lo, n);
-    const int g = group_of(s, G, b);
-    SharedSeq q{0, 0, 0, 0};
-    if (s.start[g] <= b && b < s.start[g + 1]) {
-      q.tokens = s.tokens[g];
-      q.chunks = count[g];
-      q.rows = (s.start[g + 1] - s.start[g]) * p.group;
-      q.row = base[g] + (b - s.start[g]) * p.group;
-    }
-    lo = max(lo, q.tokens);
-    return q;
+    n = s.n[b];
+    lo = s.first_seen(p, b);
+    const int g = s.group_of(G, b);
+    if (s.start[g] <= b && b < s.start[g + 1]) lo = max(lo, s.prefix(p, g));
   };
   float* const sums = reinterpret_cast<float*>(scratch);
   float tiles = 0.0f;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     int lo, n;
-    p.seqs[b] = own(b, lo, n);
+    own(b, lo, n);
     tiles += (float)tiles_of(lo, n);
+    SharedSeq q{0, 0, 0, 0};
+    const int g = s.group_of(G, b);
+    if (s.start[g] <= b && b < s.start[g + 1]) {
+      const Cut c = cut_of<S>(p, s, g, size_of_prefix);
+      q.tokens = s.prefix(p, g);
+      q.chunks = c.chunks;
+      q.rows = c.rows;
+      q.row = base[g] + (b - s.start[g]) * p.group;
+    }
+    p.seqs[b] = q;
   }
   tiles = wave_add(tiles);
   if (lane == 0) sums[wave] = tiles;
   __syncthreads();
   float all = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) all += sums[w];
+  for (int w = 0; w < S::Waves; ++w) all += sums[w];
   __syncthreads();
   const float even = fminf(ceilf(all * (float)H / (float)p.target_items * 1.0001f), 1e8f);
   int size = 0, mine = 0, before = 0;
@@ -229,7 +291,7 @@ __device__ __forceinline__ void plan_own(const AttnParams& p, const Groups& s, c
     before = upto - mine;
     int total = 0;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < S::Waves; ++w) {
       if (w < wave) before += scratch[w];
       total += scratch[w];
     }
@@ -258,88 +320,104 @@ __device__ __forceinline__ void plan_own(const AttnParams& p, const Groups& s, c
 }
 
 // Halves of a word whose exponent is all ones to 0; `found` if there is one.
-template <class C>
-__device__ __forceinline__ uint32_t without_infinite(uint32_t w, bool& found) {
-  if constexpr (sizeof(typename C::bits_t) == 2) {
-    constexpr uint32_t e = (uint32_t)C::exponent;
-    const bool lo = (w & e) == e, hi = (w & (e << 16)) == (e << 16);
-    found |= lo | hi;
-    return (lo ? 0u : w & 0xFFFFu) | (hi ? 0u : w & 0xFFFF0000u);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool bad = ((w >> (8 * i)) & 0x7Fu) == 0x7Fu;
-      found |= bad;
-      w = bad ? w & ~(0xFFu << (8 * i)) : w;
-    }
-    return w;
-  }
+template <class V>
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w, bool& found) {
+  constexpr uint32_t e = (uint32_t)V::exponent;
+  const bool lo = (w & e) == e, hi = (w & (e << 16)) == (e << 16);
+  found |= lo | hi;
+  return (lo ? 0u : w & 0xFFFFu) | (hi ? 0u : w & 0xFFFF0000u);
 }
 
-template <class T, class C, int D>
-struct PrefixShape {
-  // blocks of 16 rows that a wave keeps in registers (queries, accumulators)
-  static constexpr int Blocks = D <= 128 ? 4 : 2;
-  static constexpr int Rows = 16 * Blocks;
-  static constexpr int RowF = D + 4;  // floats of a row of the parts: values, maximum, sum
-};
+// Halves of a word times 0: NaN where they are infinite or NaN.
+template <class T>
+__device__ __forceinline__ uint32_t not_finite_halves(uint32_t w) {
+  constexpr uint32_t e = (uint32_t)T::exponent;
+  return ((w & e) == e ? 0x7FFFu : 0u) | ((w & (e << 16)) == (e << 16) ? 0x7FFF0000u : 0u);
+}
 
+constexpr int at_least(int a, int b) { return a > b ? a : b; }
+
+// 16 bytes per lane from base + from to LDS, lane l's at `to` + 16 l, without
+// registers.  In assembly, so that the compiler, which does not see what is
+// read while they are in flight, does not wait for every load before it reads
+// LDS; landed_barrier is what waits.  (Nothing else in these kernels uses m0.)
+__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(from), "s"(base) : "memory");
+}
+// All but the youngest N of this wave's loads have landed (those to LDS
+// included) and its LDS reads are done, and so for the other waves.
+template <int N>
+__device__ __forceinline__ void landed_barrier() {
+  static_assert(N < 64, "the counter has six bits");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// The keys and values of a step's tiles go from the cache to LDS without
+// registers, two steps ahead, each wave a quarter; all the waves that work on
+// the same tokens read them from there.
 template <class T, class C, int D>
-__global__ void __launch_bounds__(kThreads, 1) k_shared_prefix(AttnParams p) {
+__global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_prefix(AttnParams p) {
   using TL = Tile<T, C, D>;
   using V = typename TL::V;
   using S = PrefixShape<T, C, D>;
-  constexpr int PL = TL::PL, NB = S::Blocks, RowF = S::RowF;
-  __shared__ union {
-    struct {
-      Groups groups;
-      int base[kGroupsMax], count[kGroupsMax], scratch[kWaves];
-    } plan;
-    __attribute__((aligned(16))) float red[kWaves][kHeads][RowF];
-  } lds;
-  __shared__ float red_m[kWaves][kHeads], red_l[kWaves][kHeads];
+  constexpr int PL = TL::PL, NB = S::Blocks, RowF = S::RowF, Row = S::Row, Subs = S::Subs, Waves = S::Waves;
+  constexpr int kThreads = 64 * Waves;
+  constexpr int kKeys = Subs * S::TileBytes, kBuf = 2 * kKeys;  // a step's keys, then its values
+  // two buffers; before and after the loop other uses
+  constexpr int kPlan = 24 * kGroupsMax + 16, kRed = 4 * Waves * kHeads * S::RedF;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[at_least(2 * kBuf, at_least(kPlan, kRed))];
+  __shared__ float red_m[Waves][kHeads], red_l[Waves][kHeads];
+  __shared__ int scratch[Waves];
+  __shared__ __attribute__((aligned(8))) uint8_t has_page[2][Waves];  // of a step's buffer: half a tile each
 
-  read_groups(p, lds.plan.groups);
+  int* const plan = (int*)lds;
+  const Batch batch{plan, plan + kGroupsMax, plan + 2 * kGroupsMax, plan + 3 * kGroupsMax, (uint16_t*)(plan + 4 * kGroupsMax)};
+  int* const base = plan + 5 * kGroupsMax;  // (the starts take half of the words before, and one value more)
+  read_batch<Waves>(p, batch);
   PrefixItem it;
   if (blockIdx.x == 0) {
-    find_prefix<S::Rows>(p, lds.plan.groups, 0, it, lds.plan.base, lds.plan.count);
+    int size;
+    find_prefix<S>(p, batch, 0, it, base, &size);
     __syncthreads();
-    plan_own(p, lds.plan.groups, lds.plan.base, lds.plan.count, lds.plan.scratch);
+    plan_own<S>(p, batch, base, size, scratch);
     return;
   }
-  if (!find_prefix<S::Rows>(p, lds.plan.groups, blockIdx.x - 1, it, nullptr, nullptr)) return;
+  if (!find_prefix<S>(p, batch, blockIdx.x - 1, it, nullptr, nullptr)) return;
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kh = it.kh;
-  const int s0 = lds.plan.groups.start[it.group], rows = (lds.plan.groups.start[it.group + 1] - s0) * p.group;
-  const int prefix = lds.plan.groups.tokens[it.group];
-  const int lo_all = lds.plan.groups.lo[it.group], hi_all = lds.plan.groups.hi[it.group];
+  const int s0 = batch.start[it.group], rows = (batch.start[it.group + 1] - s0) * p.group;
+  const int prefix = batch.prefix(p, it.group);
+  const int lo_all = batch.lo[it.group], hi_all = batch.hi[it.group];
+  // rows: those of wave % it.waves; tokens: those of wave / it.waves
+  const int streams = Waves / it.waves, stream = wave / it.waves;
+  const int row0 = (it.block * it.waves + wave % it.waves) * S::Rows;
 
   // the lane's row of each block: queries and the tokens it sees
+  // (the factor is kept positive, for the maxima: a negative one turns the
+  // queries' signs, and with 0 the queries are multiplied by it instead)
   float factor = p.scale * (p.k_scale ? p.k_scale[kh] : 1.0f) * kLog2e;
+  const bool turn = factor < 0.0f, zero = factor == 0.0f;
+  factor = zero ? 1.0f : fabsf(factor);
   typename Mma<T>::op q[NB][TL::Steps];
   int lo[NB], hi[NB];
   int lo_max = 0, hi_min = 0x7FFFFFFF;
+  const int members = rows / p.group;
 #pragma unroll
-  for (int c = 0; c < NB; ++c) {
-    const int row = it.block * S::Rows + 16 * c + r;
-    const int member = row / p.group, b = s0 + min(member, rows / p.group - 1);
-    lo[c] = 0, hi[c] = 0x7FFFFFFF;
-    if (row < rows) {
-      visible(p, b, lo[c], hi[c]);
-      hi[c] = min(hi[c], prefix);
-      lo_max = max(lo_max, lo[c]);
-      hi_min = min(hi_min, hi[c]);
-    }
+  for (int c = 0; c < NB; ++c) {  // (rows past the last read its queries)
+    const int row = row0 + 16 * c + r, member = min(row / p.group, members - 1), b = s0 + member;
+    const int head = row < rows ? row - member * p.group : 0;
+    const uint8_t* from = reinterpret_cast<const uint8_t*>(p.q + b * p.q_stride + (int64_t)(kh * p.group + head) * D);
 #pragma unroll
     for (int s = 0; s < TL::Steps; ++s) {
-      uint32_t w[4] = {0, 0, 0, 0};
-      if (row < rows)
-        load_bytes<16>(reinterpret_cast<const uint8_t*>(p.q + b * p.q_stride +
-                                                        (int64_t)(kh * p.group + row - member * p.group) * D + TL::q_dim(s, g)),
-                       w);
+      uint32_t w[4];
+      load_bytes<16>(from + 2 * TL::q_dim(s, g), w);
       __builtin_memcpy(&q[c][s], w, 16);
     }
+    lo[c] = row < rows ? batch.first_seen(p, b) : 0;
+    hi[c] = row < rows ? min(batch.n[b], prefix) : 0x7FFFFFFF;
+    lo_max = max(lo_max, lo[c]);
+    hi_min = min(hi_min, hi[c]);
   }
   // over the rows (the same in each of the four lanes of a row)
 #pragma unroll
@@ -349,206 +427,325 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_prefix(AttnParams p) {
   }
   lo_max = __builtin_amdgcn_readfirstlane(lo_max);
   hi_min = __builtin_amdgcn_readfirstlane(hi_min);
-  __syncthreads();  // (the plan is read: its place takes the sums)
+  __syncthreads();  // (the batch is read: its place takes the tiles)
 
+  if (turn || zero) {
+#pragma unroll
+    for (int c = 0; c < NB; ++c)
+#pragma unroll
+      for (int s = 0; s < TL::Steps; ++s) {
+        uint32_t w[4];
+        __builtin_memcpy(w, &q[c][s], 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = zero ? not_finite_halves<T>(w[i]) : w[i] ^ 0x80008000u;
+        __builtin_memcpy(&q[c][s], w, 16);
+      }
+  }
   f32x4 acc[NB][PL];
-  float m[NB], l[NB];
+  // maximum and sum of a row; over: what the exponent of a score gets added
+  float m[NB], l[NB], over[NB];
 #pragma unroll
   for (int c = 0; c < NB; ++c) {
-    m[c] = -FLT_MAX, l[c] = 0.0f;
+    m[c] = -FLT_MAX, l[c] = 0.0f, over[c] = FLT_MAX;
 #pragma unroll
     for (int i = 0; i < PL; ++i) acc[c][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
   bool infinite = false;  // a value that is not finite was taken out
 
-  // the page numbers of this wave's tiles, a tile per lane (64 at a time)
+  // --- from the cache to LDS: this wave's half of a tile of a step (half
+  // `wave` of the step's tokens); the pages of 64 steps at a time, one per lane
   const int32_t* table = p.table + s0 * p.table_stride;
-  int page_of[2] = {-1, -1};
-  auto load_pages = [&](int tile) {
+  const int steps = (it.tile_end - it.tile + Subs - 1) / Subs;
+  int page_of = -1;
+  auto load_pages = [&](int step) __attribute__((always_inline)) {
+    const int tile = it.tile + (step + lane) * Subs + wave / 2, t = tile * kTokens + 16 * (wave & 1);
+    page_of = tile < it.tile_end && t < hi_all ? table[t >> p.page_shift] : -1;
+    if (page_of >= p.pages) page_of = -1;
+  };
+  int from_k[S::Loads], from_v[S::Loads];  // where in the half's tokens a lane's piece of each load is
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int t = (tile + kWaves * lane) * kTokens + 16 * j;
-      page_of[j] = tile + kWaves * lane < it.tile_end && t < hi_all ? table[t >> p.page_shift] : -1;
-      if (page_of[j] >= p.pages) page_of[j] = -1;
-    }
-  };
-  struct Place {
-    const uint8_t *k[2], *v[2];
-    bool ok[2];
-  };
-  auto place = [&](int step, int tile) {
-    Place a;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int page = __builtin_amdgcn_readlane(page_of[j], step & 63);
-      a.ok[j] = page >= 0;
-      const int t = (tile * kTokens + 16 * j) & ((1 << p.page_shift) - 1);
-      const int64_t at = ((((int64_t)(page < 0 ? 0 : page) * p.kv_heads + kh) << p.page_shift) + t) * TL::Row;
-      a.k[j] = p.k_cache + at;
-      a.v[j] = p.v_cache + at;
-    }
-    return a;
-  };
-
-  TL tl;
-  const int first = it.tile + wave;
-  Place now;
-  if (first < it.tile_end) {
-    load_pages(first);
-    now = place(0, first);
-    tl.load_k(now.k, lane);
-    __builtin_amdgcn_sched_barrier(0);
-    tl.load_v(now.v, lane);
-    __builtin_amdgcn_sched_barrier(0);
+  for (int i = 0; i < S::Loads; ++i) {
+    const int piece = 64 * i + lane, row = piece / S::Pieces, at = piece % S::Pieces;
+    from_k[i] = row * Row + 16 * (at ^ S::mix_k(row));
+    from_v[i] = row * Row + 16 * (at ^ S::mix_v(16 * (wave & 1) + row));
   }
-  for (int tile = first, step = 0; tile < it.tile_end; tile += kWaves, ++step) {
-    const bool more = tile + kWaves < it.tile_end;
-    f32x4 s[NB][2];
+  const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds + wave * (16 * Row);
+  // keys and values of a step into buffer step % 2
+  auto fetch = [&](int step) __attribute__((always_inline)) {
+    const int page = __builtin_amdgcn_readlane(page_of, step & 63);
+    const int t = ((it.tile + step * Subs + wave / 2) * kTokens + 16 * (wave & 1)) & ((1 << p.page_shift) - 1);
+    const int64_t at = ((((int64_t)(page < 0 ? 0 : page) * p.kv_heads + kh) << p.page_shift) + t) * Row;
+    const uint32_t to = lds_at + (step & 1) * kBuf;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int i = 0; i < S::Loads; ++i)
+      if (16 * S::Pieces % 64 == 0 || 64 * i + lane < 16 * S::Pieces) load_to_lds(p.k_cache + at, from_k[i], to + 1024 * i);
 #pragma unroll
-      for (int c = 0; c < NB; ++c) s[c][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int st = 0; st < TL::Steps; ++st) {
-        const typename Mma<T>::op k = tl.k_op(j, st);
-#pragma unroll
-        for (int c = 0; c < NB; ++c) s[c][j] = Mma<T>::mul(k, q[c][st], s[c][j]);
-      }
-    }
-    if (more && ((step + 1) & 63) == 0) load_pages(tile + kWaves);
-    const Place next = place(step + more, tile + (more ? kWaves : 0));
-    __builtin_amdgcn_sched_barrier(0);
-    tl.load_k(next.k, lane);
-    __builtin_amdgcn_sched_barrier(0);
-    const int t0 = tile * kTokens;
+    for (int i = 0; i < S::Loads; ++i)
+      if (16 * S::Pieces % 64 == 0 || 64 * i + lane < 16 * S::Pieces) load_to_lds(p.v_cache + at, from_v[i], to + kKeys + 1024 * i);
+    if (lane == 0) has_page[step & 1][wave] = page >= 0;
+  };
+  // (the accumulators stay where the matrix operations have them: without
+  // this the rare branch that rescales them makes the compiler move them all
+  // to other registers and back for every tile)
+  auto in_place = [&]() __attribute__((always_inline)) {
+    if (!S::Ahead) return;
 #pragma unroll
     for (int c = 0; c < NB; ++c)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[c][e >> 2][e & 3] *= factor;
-    if (!(t0 >= lo_max && t0 + kTokens <= hi_min && now.ok[0] && now.ok[1])) {
-      // some row does not see some token: no score there.  Nobody sees a
-      // token outside lo_all .. hi_all - 1 or without a page; the values of
-      // the others stay, but for those that would be NaN times a probability
-      // of 0 (the rows that see them get them at the end)
+      for (int i = 0; i < PL; ++i) asm("" : "+a"(acc[c][i]));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int t = t0 + 16 * (e >> 2) + 4 * g + (e & 3);
-        const bool is = now.ok[e >> 2] && t >= lo_all && t < hi_all;
+    for (int c = 0; c < NB; ++c)
 #pragma unroll
-        for (int w = 0; w < TL::W0 + TL::W1; ++w) {
-          tl.v[e][w] = is ? tl.v[e][w] : 0u;
-          tl.v[e][w] = without_infinite<C>(tl.v[e][w], infinite);
+      for (int i = 0; i < TL::Steps; ++i) asm("" : "+a"(q[c][i]));
+  };
+  // --- a tile's operands, from LDS
+  TL x;  // (its keys)
+  typename Mma<V>::op v[PL];
+  uint32_t bytes[TL::ES == 1 ? PL : 1][2];  // 8-bit values as they are read
+  auto load_keys = [&](int step, int sub) __attribute__((always_inline)) {
+    const uint8_t* keys = lds + (step & 1) * kBuf + sub * S::TileBytes;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint8_t* row = keys + (16 * j + r) * Row;
+      if constexpr (TL::ES == 2) {
+#pragma unroll
+        for (int st = 0; st < TL::Steps; ++st) load_bytes<16>(row + 16 * ((4 * st + g) ^ S::mix_k(r)), &x.k[j][4 * st]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) load_bytes<16>(row + 16 * ((4 * u + g) ^ S::mix_k(r)), &x.k[j][4 * u]);
+        if constexpr (D % 64)
+          load_bytes<8>(row + 16 * ((4 * (D / 64) + (g >> 1)) ^ S::mix_k(r)) + 8 * (g & 1), &x.k[j][4 * (D / 64)]);
+      }
+    }
+  };
+  // operand i of the values is 16 dimensions of the tile's tokens: a read that
+  // transposes gives lane (r, g) dimension 16 i + r of the four tokens (8-bit:
+  // eight) whose rows its 16 lanes name
+  auto load_values = [&](int step, int sub) __attribute__((always_inline)) {
+    const uint8_t* values = lds + (step & 1) * kBuf + kKeys + sub * S::TileBytes;
+    if constexpr (TL::ES == 2) {
+      const int t = 4 * g + (r >> 2);
+      const uint8_t* row = values + t * Row + 8 * (r & 1);
+#pragma unroll
+      for (int i = 0; i < PL; ++i) {
+        const int at = 16 * ((2 * i + (r >> 1 & 1)) ^ S::mix_v(t));
+        static_assert(TL::ES == 1 || S::Pieces % 4 == 0, "tokens t and t + 16 are mixed alike");
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(row + at));
+        const s16x4 hi =
+            __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(row + at + 16 * Row));
+        __builtin_memcpy(&v[i], &lo, 8);
+        __builtin_memcpy((uint8_t*)&v[i] + 8, &hi, 8);
+      }
+    } else {
+      const int t = 16 * (r >> 3) + 4 * g + (r >> 1 & 3);
+      const uint8_t* row = values + t * Row + 8 * (r & 1);
+#pragma unroll
+      for (int i = 0; i < PL; ++i) {
+        const i32x2 b = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)(row + 16 * (i ^ S::mix_v(t))));
+        bytes[i][0] = b.x, bytes[i][1] = b.y;
+      }
+    }
+  };
+  auto widen_values = [&]() __attribute__((always_inline)) {
+    if constexpr (TL::ES == 1) {
+#pragma unroll
+      for (int i = 0; i < PL; ++i) {
+        uint32_t w[4];
+        Mma<V>::widen(bytes[i][0], w);
+        Mma<V>::widen(bytes[i][1], w + 2);
+        __builtin_memcpy(&v[i], w, 16);
+      }
+    }
+  };
+
+  // Step i of the workgroup: the tiles that buffer i % 2 holds, each wave its
+  // stream's.  A wave reads a tile's operands while it works on the one
+  // before, so when all have come to their last tile of a step its buffer is
+  // free for the step after the next, and that step's loads have a step's
+  // time to land.
+  if (steps > 0) {
+    load_pages(0);
+    fetch(0);
+    if (steps > 1) {
+      fetch(1);
+      landed_barrier<2 * S::Loads>();
+    } else {
+      landed_barrier<0>();
+    }
+  }
+  auto pages_of = [&](int step) __attribute__((always_inline)) {
+    uint64_t v = 0;
+    __builtin_memcpy(&v, has_page[step & 1], Waves);
+    return (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)v) |
+           (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32;
+  };
+  if (it.tile + stream < it.tile_end) {
+    uint64_t pages = pages_of(0);
+    int step = 0, sub = stream;
+    if (S::Ahead) load_keys(0, sub);
+#pragma unroll 1
+    for (;;) {
+      const int tile = it.tile + step * Subs + sub, t0 = tile * kTokens;
+      if (!S::Ahead) load_keys(step, sub);
+      load_values(step, sub);
+      in_place();
+      f32x4 s[NB][2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int c = 0; c < NB; ++c) s[c][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int st = 0; st < TL::Steps; ++st) {
+          const typename Mma<T>::op k = x.k_op(j, st);
+#pragma unroll
+          for (int c = 0; c < NB; ++c) s[c][j] = Mma<T>::mul(k, q[c][st], s[c][j]);
+        }
+      }
+      widen_values();
+      const uint32_t have = (uint32_t)(pages >> (16 * sub) & 1) | (uint32_t)(pages >> (16 * sub + 7) & 2);
+      if (!(t0 >= lo_max && t0 + kTokens <= hi_min && have == 3)) {
+        // some row does not see some token: no score there.  Nobody sees a
+        // token outside lo_all .. hi_all - 1 or without a page; the values
+        // of the others stay, but for those that would be NaN times a
+        // probability of 0 (the rows that see them get them at the end)
+        uint32_t is = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int t = t0 + 16 * (e >> 2) + 4 * g + (e & 3);
+          if ((have >> (e >> 2) & 1) && t >= lo_all && t < hi_all) is |= 1u << e;
+#pragma unroll
+          for (int c = 0; c < NB; ++c)
+            s[c][e >> 2][e & 3] = (is >> e & 1) && t >= lo[c] && t < hi[c] ? s[c][e >> 2][e & 3] : -INFINITY;
         }
 #pragma unroll
-        for (int c = 0; c < NB; ++c)
-          s[c][e >> 2][e & 3] = is && t >= lo[c] && t < hi[c] ? s[c][e >> 2][e & 3] : -INFINITY;
-      }
-    }
-    float top[NB];
-    bool raise = false;
+        for (int i = 0; i < PL; ++i) {
+          uint32_t w[4];
+          __builtin_memcpy(w, &v[i], 16);
 #pragma unroll
-    for (int c = 0; c < NB; ++c) {
-      top[c] = fmaxf(fmaxf(fmaxf(s[c][0][0], s[c][0][1]), fmaxf(s[c][0][2], s[c][0][3])),
-                     fmaxf(fmaxf(s[c][1][0], s[c][1][1]), fmaxf(s[c][1][2], s[c][1][3])));
-      raise |= top[c] > m[c] + kSlack;
-    }
-    if (__any(raise)) {
+          for (int k = 0; k < 4; ++k)  // (tokens 2 k and 2 k + 1)
+            w[k] = finite_halves<V>(w[k] & ((is >> (2 * k) & 1 ? 0xFFFFu : 0u) | (is >> (2 * k + 1) & 1 ? 0xFFFF0000u : 0u)), infinite);
+          __builtin_memcpy(&v[i], w, 16);
+        }
+      }
+      float top[NB];
+      bool raise = false;
 #pragma unroll
       for (int c = 0; c < NB; ++c) {
-        const float mn = fmaxf(m[c], column_max(top[c]));
-        const float f = __builtin_amdgcn_exp2f(m[c] - mn);
-        l[c] *= f;
-#pragma unroll
-        for (int i = 0; i < PL; ++i) acc[c][i] *= f;
-        m[c] = mn;
+        top[c] = fmaxf(fmaxf(fmaxf(s[c][0][0], s[c][0][1]), fmaxf(s[c][0][2], s[c][0][3])),
+                       fmaxf(fmaxf(s[c][1][0], s[c][1][1]), fmaxf(s[c][1][2], s[c][1][3])));
+        raise |= fmaf(top[c], factor, over[c]) > kSlack + Mma<V>::lift;
       }
-    }
-    typename Mma<V>::op pr[NB];
+      if (__any(raise)) {
 #pragma unroll
-    for (int c = 0; c < NB; ++c) {
-      float e[8];
+        for (int c = 0; c < NB; ++c) {
+          const float mn = fmaxf(m[c], column_max(top[c]) * factor);
+          const float f = __builtin_amdgcn_exp2f(m[c] - mn);
+          l[c] *= f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        e[i] = __builtin_amdgcn_exp2f(s[c][i >> 2][i & 3] - m[c] + Mma<V>::lift);
-        l[c] += e[i];
+          for (int i = 0; i < PL; ++i) acc[c][i] *= f;
+          m[c] = mn;
+          over[c] = Mma<V>::lift - mn;
+        }
       }
-      pr[c] = Mma<V>::round(e);
-    }
-#pragma unroll
-    for (int i = 0; i < PL; i += 2) {
-      typename Mma<V>::op a, b;
-      tl.v_ops(i, a, b);
+      // the next tile (after the last one, this one again)
+      int next_step = step, next_sub = sub + streams;
+      if (next_sub >= Subs) {
+        next_step = step + 1, next_sub = stream;
+        if (next_step < steps) {
+          landed_barrier<0>();
+          if (step + 2 < steps) {
+            if (((step + 2) & 63) == 0) load_pages(step + 2);
+            fetch(step + 2);
+          }
+          pages = pages_of(next_step);
+        }
+      }
+      const bool done = next_step == steps || it.tile + next_step * Subs + next_sub >= it.tile_end;
+      if (done) next_step = step, next_sub = sub;
+      in_place();
+      if (S::Ahead) load_keys(next_step, next_sub);
 #pragma unroll
       for (int c = 0; c < NB; ++c) {
-        acc[c][i] = Mma<V>::mul(a, pr[c], acc[c][i]);
-        acc[c][i + 1] = Mma<V>::mul(b, pr[c], acc[c][i + 1]);
+        float e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          e[i] = __builtin_amdgcn_exp2f(fmaf(s[c][i >> 2][i & 3], factor, over[c]));
+          l[c] += e[i];
+        }
+        const typename Mma<V>::op pr = Mma<V>::round(e);
+#pragma unroll
+        for (int i = 0; i < PL; ++i) acc[c][i] = Mma<V>::mul(v[i], pr, acc[c][i]);
       }
+      if (done) break;
+      step = next_step, sub = next_sub;
     }
-    __builtin_amdgcn_sched_barrier(0);
-    tl.load_v(next.v, lane);
-    __builtin_amdgcn_sched_barrier(0);
-    now = next;
   }
 
-  // the waves' parts, a block after the other, into the chunk's
+  // the parts of the waves with the same rows, a block after the other, into
+  // the chunk's
+  float(*const red)[kHeads][S::RedF] = reinterpret_cast<float(*)[kHeads][S::RedF]>(lds);
   infinite = __syncthreads_or(infinite);
 #pragma unroll
   for (int c = 0; c < NB; ++c) {
     const float sum = column_sum(l[c]);
-    if (c) __syncthreads();  // (the block before is read)
     if (g == 0) red_m[wave][r] = m[c], red_l[wave][r] = sum;
     __syncthreads();
-    float mw = red_m[0][r];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) mw = fmaxf(mw, red_m[w][r]);
+    float mw = m[c];
+    for (int w = wave % it.waves; w < Waves; w += it.waves) mw = fmaxf(mw, red_m[w][r]);
     const float f = __builtin_amdgcn_exp2f(m[c] - mw);
 #pragma unroll
-    for (int i = 0; i < PL; ++i)
+    for (int d0 = 0; d0 < D; d0 += S::RedDims) {
+      if (d0) __syncthreads();  // (the dimensions before are read)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) lds.red[wave][r][TL::dim(4 * g + k, i)] = acc[c][i][k] * f;
-    __syncthreads();
-    for (int i = threadIdx.x; i < kHeads * (D / 4); i += kThreads) {
-      const int h = i / (D / 4), d = 4 * (i % (D / 4)), row = it.block * S::Rows + 16 * c + h;
-      if (row >= rows) break;
-      float mh = red_m[0][h], lh = 0.0f;
-      f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) mh = fmaxf(mh, red_m[w][h]);
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        lh += red_l[w][h] * __builtin_amdgcn_exp2f(red_m[w][h] - mh);
-        o += *reinterpret_cast<const f32x4*>(&lds.red[w][h][d]);
-      }
-      if (__builtin_expect(infinite || any_nan(o), false) && lh == lh) {
-        int seen_lo, seen_hi;
-        visible(p, s0 + row / p.group, seen_lo, seen_hi);
-        seen_lo = max(seen_lo, it.tile * kTokens);
-        seen_hi = min(min(seen_hi, prefix), it.tile_end * kTokens);
-        if (seen_lo < seen_hi) {
-          const f32x4 x = infinite_values<C, D>(table, reinterpret_cast<const typename C::bits_t*>(p.v_cache), p.pages,
-                                                p.kv_heads, kh, p.page_shift, seen_lo, seen_hi, d);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[k] = x[k] != 0.0f ? x[k] : o[k];
+      for (int i = d0 / 16; i < (d0 + S::RedDims) / 16; ++i)
+        *reinterpret_cast<f32x4*>(&red[wave][r][16 * i - d0 + 4 * g]) = acc[c][i] * f;
+      __syncthreads();
+      for (int i = threadIdx.x; i < it.waves * kHeads * (S::RedDims / 4); i += kThreads) {
+        const int which = i / (kHeads * (S::RedDims / 4)), h = i / (S::RedDims / 4) % kHeads;
+        const int d = 4 * (i % (S::RedDims / 4)), row = (it.block * it.waves + which) * S::Rows + 16 * c + h;
+        if (row >= rows) continue;
+        float mh = red_m[which][h], lh = 0.0f;
+        f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int w = which + it.waves; w < Waves; w += it.waves) mh = fmaxf(mh, red_m[w][h]);
+        for (int w = which; w < Waves; w += it.waves) {
+          lh += red_l[w][h] * __builtin_amdgcn_exp2f(red_m[w][h] - mh);
+          o += *reinterpret_cast<const f32x4*>(&red[w][h][d]);
         }
+        if (__builtin_expect(infinite || any_nan(o), false) && lh == lh) {
+          int seen_lo, seen_hi;
+          visible(p, s0 + row / p.group, seen_lo, seen_hi);
+          seen_lo = max(seen_lo, it.tile * kTokens);
+          seen_hi = min(min(seen_hi, prefix), it.tile_end * kTokens);
+          if (seen_lo < seen_hi) {
+            const f32x4 x = infinite_values<C, D>(table, reinterpret_cast<const typename C::bits_t*>(p.v_cache), p.pages,
+                                                  p.kv_heads, kh, p.page_shift, seen_lo, seen_hi, d0 + d);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = x[k] != 0.0f ? x[k] : o[k];
+          }
+        }
+        float* out = p.prefix_parts + ((int64_t)it.row + ((int64_t)it.chunk * p.kv_heads + kh) * rows + row) * RowF;
+        *reinterpret_cast<f32x4*>(out + d0 + d) = o;
+        if (d0 + d == 0) *reinterpret_cast<float2*>(out + D) = make_float2(mh, lh);
       }
-      float* out = p.prefix_parts + ((int64_t)it.row + ((int64_t)it.chunk * p.kv_heads + kh) * rows + row) * RowF;
-      *reinterpret_cast<f32x4*>(out + d) = o;
-      if (d == 0) *reinterpret_cast<float2*>(out + D) = make_float2(mh, lh);
     }
+    if (c + 1 < NB) __syncthreads();  // (the block is read)
   }
 }
 
 template <class T, class C>
 void launch_dim(const AttnParams& p, int64_t head_dim, hipStream_t s) {
-  const dim3 block(kThreads);
-  auto grid = [&](int64_t rows_of_block) {
+  auto grid = [&](int64_t least_rows) {
     // the plan, about prefix_target workgroups, and one more per key head and
     // row block
-    return dim3((unsigned)(1 + p.prefix_target + p.kv_heads * ((int64_t)p.batch * p.group / rows_of_block + p.groups)));
+    return dim3((unsigned)(1 + p.prefix_target + p.kv_heads * ((int64_t)p.batch * p.group / least_rows + p.groups)));
   };
   switch (head_dim) {
-#define BGG_PREFIX(D) \
-  case D: hipLaunchKernelGGL((k_shared_prefix<T, C, D>), grid(PrefixShape<T, C, D>::Rows), block, 0, s, p); break
+#define BGG_PREFIX(D)                                                                                          \
+  case D:                                                                                                      \
+    hipLaunchKernelGGL((k_shared_prefix<T, C, D>),                                                             \
+                       grid(PrefixShape<T, C, D>::Rows * PrefixShape<T, C, D>::Least),                  \
+                       dim3(64 * PrefixShape<T, C, D>::Waves), 0, s, p);                                       \
+    break
     BGG_PREFIX(64);
     BGG_PREFIX(96);
     BGG_PREFIX(128);
@@ -563,8 +760,10 @@ void launch_dim(const AttnParams& p, int64_t head_dim, hipStream_t s) {
 namespace bgg {
 
 int64_t prefix_part_floats(const bgg_cache_desc* c, int64_t q_heads, int64_t batch, int64_t target) {
+  // an item has at most 256 rows (128 of wide heads) and there are target of
+  // them, and each row one part more
   const int64_t D = c->head_dim;
-  return (target * (D <= 128 ? 64 : 32) + batch * q_heads) * (D + 4);
+  return (target * (D <= 128 ? 256 : 128) + batch * q_heads) * (D + 4);
 }
 
 void launch_prefix(const AttnParams& p, int32_t type, bool e4m3, int64_t head_dim, hipStream_t s) {
