@@ -27,17 +27,19 @@ struct PrefixShape {
   // Eight waves, two on a SIMD, so that one's matrix operations run beside
   // the other's exponentials; wide heads do not fit their registers.
   static constexpr int Waves = D <= 128 ? 8 : 4;
-  static constexpr bool Ahead = Waves == 4;  // a tile's keys are read while the one before is worked on
   static constexpr int Blocks = 2;  // blocks of 16 rows of a wave (queries, accumulators)
   static constexpr int Rows = 16 * Blocks;
   static constexpr int RowF = D + 4;  // floats of a row of the parts: values, maximum, sum
-  // tiles of a step: each wave fetches half a tile; the keys and values of
-  // two steps take up to 128 KB of LDS
+  // tiles of a step; the keys and values of two steps take up to 128 KB of LDS
   static constexpr int Subs = Waves / 2;
+  // Four waves fetch them, a tile each (two a step: half a tile).  Of eight
+  // they are the ones whose instructions the SIMDs prefer: the others work
+  // while these stand in the queue of the loads.
+  static constexpr int Halves = Subs / 2;  // half tiles of a fetching wave
   static constexpr int Least = 2;  // row waves at least
   static constexpr int TileBytes = kTokens * Row;
   static constexpr int Pieces = Row / 16;                // 16-byte pieces of a row
-  static constexpr int Loads = (16 * Pieces + 63) / 64;  // of a wave: keys (and values) of a step
+  static constexpr int Loads = (16 * Pieces + 63) / 64;  // of the keys (and the values) of half a tile
   static constexpr int RedDims = D > 128 ? D / 2 : D;    // dimensions that the waves' parts join at a time
   static constexpr int RedF = RedDims + 4;
   // In LDS, piece q of row r lies at piece q ^ mix(r) of the row, so that the
@@ -177,17 +179,20 @@ __device__ __forceinline__ bool find_prefix(const AttnParams& p, const Batch& s,
   const float even = fminf(ceilf(wave_add(work) * (float)p.kv_heads / (float)p.prefix_target * 1.0001f), 1e8f);
   int size = 0, mine = 0, upto = 0, rows = 0;
 #pragma unroll 1
-  for (int k = 8; k <= 16; k += 2) {
-    size = max(1, (int)(even * (float)k * 0.125f));
+  for (int k = 32; k <= 64; ++k) {
+    size = max(1, (int)(even * (float)k * 0.03125f));
     mine = rows = 0;
+    int least = 0;
 #pragma unroll 1
     for (int g = g0; g < g1; ++g) {
       const Cut c = cut_of<S>(p, s, g, size);
       mine += c.chunks * c.blocks;
+      least += c.chunks ? c.blocks : 0;
       rows += c.chunks * p.kv_heads * c.rows;
     }
     upto = scan_add(mine);
     if (__builtin_amdgcn_readlane(upto, 63) * p.kv_heads <= p.prefix_target) break;
+    if (wave_add((float)least) * (float)p.kv_heads > (float)p.prefix_target) break;  // (no size is large enough)
   }
   size = __builtin_amdgcn_readfirstlane(size);
   int row = scan_add(rows) - rows;  // rows of the parts before this lane's groups
@@ -368,7 +373,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   __shared__ __attribute__((aligned(16))) uint8_t lds[at_least(2 * kBuf, at_least(kPlan, kRed))];
   __shared__ float red_m[Waves][kHeads], red_l[Waves][kHeads];
   __shared__ int scratch[Waves];
-  __shared__ __attribute__((aligned(8))) uint8_t has_page[2][Waves];  // of a step's buffer: half a tile each
+  __shared__ __attribute__((aligned(8))) uint8_t has_page[2][2 * S::Subs];  // of a step's buffer: half a tile each
 
   int* const plan = (int*)lds;
   const Batch batch{plan, plan + kGroupsMax, plan + 2 * kGroupsMax, plan + 3 * kGroupsMax, (uint16_t*)(plan + 4 * kGroupsMax)};
@@ -401,6 +406,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   factor = zero ? 1.0f : fabsf(factor);
   typename Mma<T>::op q[NB][TL::Steps];
   int lo[NB], hi[NB];
+  bool none[NB];
   int lo_max = 0, hi_min = 0x7FFFFFFF;
   const int members = rows / p.group;
 #pragma unroll
@@ -414,10 +420,14 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
       load_bytes<16>(from + 2 * TL::q_dim(s, g), w);
       __builtin_memcpy(&q[c][s], w, 16);
     }
-    lo[c] = row < rows ? batch.first_seen(p, b) : 0;
-    hi[c] = row < rows ? min(batch.n[b], prefix) : 0x7FFFFFFF;
-    lo_max = max(lo_max, lo[c]);
-    hi_min = min(hi_min, hi[c]);
+    lo[c] = batch.first_seen(p, b);
+    hi[c] = min(batch.n[b], prefix);
+    // a row that sees nothing of the item's tokens (an unused sequence, a
+    // window) does not keep the others from the fast path: it is emptied at
+    // the end instead
+    none[c] = row >= rows || max(lo[c], it.tile * kTokens) >= min(hi[c], it.tile_end * kTokens);
+    lo_max = max(lo_max, none[c] ? 0 : lo[c]);
+    hi_min = min(hi_min, none[c] ? 0x7FFFFFFF : hi[c]);
   }
   // over the rows (the same in each of the four lanes of a row)
 #pragma unroll
@@ -452,43 +462,53 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   }
   bool infinite = false;  // a value that is not finite was taken out
 
-  // --- from the cache to LDS: this wave's half of a tile of a step (half
-  // `wave` of the step's tokens); the pages of 64 steps at a time, one per lane
+  // --- from the cache to LDS: the wave's half tiles of a step; the pages of
+  // 64 steps at a time, one per lane
   const int32_t* table = p.table + s0 * p.table_stride;
   const int steps = (it.tile_end - it.tile + Subs - 1) / Subs;
-  int page_of = -1;
+  int page_of[S::Halves];
   auto load_pages = [&](int step) __attribute__((always_inline)) {
-    const int tile = it.tile + (step + lane) * Subs + wave / 2, t = tile * kTokens + 16 * (wave & 1);
-    page_of = tile < it.tile_end && t < hi_all ? table[t >> p.page_shift] : -1;
-    if (page_of >= p.pages) page_of = -1;
+#pragma unroll
+    for (int j = 0; j < S::Halves; ++j) {
+      const int half = wave * S::Halves + j, tile = it.tile + (step + lane) * Subs + half / 2;
+      const int t = tile * kTokens + 16 * (half & 1);
+      page_of[j] = tile < it.tile_end && t < hi_all ? table[t >> p.page_shift] : -1;
+      if (page_of[j] >= p.pages) page_of[j] = -1;
+    }
   };
-  int from_k[S::Loads], from_v[S::Loads];  // where in the half's tokens a lane's piece of each load is
+  int from_k[S::Loads], from_v[S::Halves][S::Loads];  // where in a half's tokens a lane's piece of each load is
 #pragma unroll
   for (int i = 0; i < S::Loads; ++i) {
     const int piece = 64 * i + lane, row = piece / S::Pieces, at = piece % S::Pieces;
     from_k[i] = row * Row + 16 * (at ^ S::mix_k(row));
-    from_v[i] = row * Row + 16 * (at ^ S::mix_v(16 * (wave & 1) + row));
+#pragma unroll
+    for (int j = 0; j < S::Halves; ++j)
+      from_v[j][i] = row * Row + 16 * (at ^ S::mix_v(16 * ((wave * S::Halves + j) & 1) + row));
   }
-  const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds + wave * (16 * Row);
+  const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds + wave * (S::Halves * 16 * Row);
   // keys and values of a step into buffer step % 2
   auto fetch = [&](int step) __attribute__((always_inline)) {
-    const int page = __builtin_amdgcn_readlane(page_of, step & 63);
-    const int t = ((it.tile + step * Subs + wave / 2) * kTokens + 16 * (wave & 1)) & ((1 << p.page_shift) - 1);
-    const int64_t at = ((((int64_t)(page < 0 ? 0 : page) * p.kv_heads + kh) << p.page_shift) + t) * Row;
-    const uint32_t to = lds_at + (step & 1) * kBuf;
 #pragma unroll
-    for (int i = 0; i < S::Loads; ++i)
-      if (16 * S::Pieces % 64 == 0 || 64 * i + lane < 16 * S::Pieces) load_to_lds(p.k_cache + at, from_k[i], to + 1024 * i);
+    for (int j = 0; j < S::Halves; ++j) {
+      const int half = wave * S::Halves + j, page = __builtin_amdgcn_readlane(page_of[j], step & 63);
+      const int t = ((it.tile + step * Subs + half / 2) * kTokens + 16 * (half & 1)) & ((1 << p.page_shift) - 1);
+      const int64_t at = ((((int64_t)(page < 0 ? 0 : page) * p.kv_heads + kh) << p.page_shift) + t) * Row;
+      const uint32_t to = lds_at + (step & 1) * kBuf + j * (16 * Row);
 #pragma unroll
-    for (int i = 0; i < S::Loads; ++i)
-      if (16 * S::Pieces % 64 == 0 || 64 * i + lane < 16 * S::Pieces) load_to_lds(p.v_cache + at, from_v[i], to + kKeys + 1024 * i);
-    if (lane == 0) has_page[step & 1][wave] = page >= 0;
+      for (int i = 0; i < S::Loads; ++i)
+        if (16 * S::Pieces % 64 == 0 || 64 * i + lane < 16 * S::Pieces) load_to_lds(p.k_cache + at, from_k[i], to + 1024 * i);
+#pragma unroll
+      for (int i = 0; i < S::Loads; ++i)
+        if (16 * S::Pieces % 64 == 0 || 64 * i + lane < 16 * S::Pieces)
+          load_to_lds(p.v_cache + at, from_v[j][i], to + kKeys + 1024 * i);
+      if (lane == 0) has_page[step & 1][half] = page >= 0;
+    }
   };
   // (the accumulators stay where the matrix operations have them: without
   // this the rare branch that rescales them makes the compiler move them all
   // to other registers and back for every tile)
   auto in_place = [&]() __attribute__((always_inline)) {
-    if (!S::Ahead) return;
+    if (S::Waves > 4) return;
 #pragma unroll
     for (int c = 0; c < NB; ++c)
 #pragma unroll
@@ -563,30 +583,32 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   // before, so when all have come to their last tile of a step its buffer is
   // free for the step after the next, and that step's loads have a step's
   // time to land.
+  const bool fetches = wave < 4;
   if (steps > 0) {
-    load_pages(0);
-    fetch(0);
+    if (fetches) {
+      load_pages(0);
+      fetch(0);
+      if (steps > 1) fetch(1);
+    }
     if (steps > 1) {
-      fetch(1);
-      landed_barrier<2 * S::Loads>();
+      landed_barrier<2 * S::Halves * S::Loads>();
     } else {
       landed_barrier<0>();
     }
   }
   auto pages_of = [&](int step) __attribute__((always_inline)) {
     uint64_t v = 0;
-    __builtin_memcpy(&v, has_page[step & 1], Waves);
+    __builtin_memcpy(&v, has_page[step & 1], 2 * Subs);
     return (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)v) |
            (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32;
   };
   if (it.tile + stream < it.tile_end) {
     uint64_t pages = pages_of(0);
     int step = 0, sub = stream;
-    if (S::Ahead) load_keys(0, sub);
+    load_keys(0, sub);
 #pragma unroll 1
     for (;;) {
       const int tile = it.tile + step * Subs + sub, t0 = tile * kTokens;
-      if (!S::Ahead) load_keys(step, sub);
       load_values(step, sub);
       in_place();
       f32x4 s[NB][2];
@@ -653,7 +675,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
         next_step = step + 1, next_sub = stream;
         if (next_step < steps) {
           landed_barrier<0>();
-          if (step + 2 < steps) {
+          if (step + 2 < steps && fetches) {
             if (((step + 2) & 63) == 0) load_pages(step + 2);
             fetch(step + 2);
           }
@@ -663,7 +685,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
       const bool done = next_step == steps || it.tile + next_step * Subs + next_sub >= it.tile_end;
       if (done) next_step = step, next_sub = sub;
       in_place();
-      if (S::Ahead) load_keys(next_step, next_sub);
+      load_keys(next_step, next_sub);
 #pragma unroll
       for (int c = 0; c < NB; ++c) {
         float e[8];
@@ -687,7 +709,12 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   infinite = __syncthreads_or(infinite);
 #pragma unroll
   for (int c = 0; c < NB; ++c) {
-    const float sum = column_sum(l[c]);
+    const float sum = none[c] ? 0.0f : column_sum(l[c]);
+    if (none[c]) {
+      m[c] = -FLT_MAX;
+#pragma unroll
+      for (int i = 0; i < PL; ++i) acc[c][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
     if (g == 0) red_m[wave][r] = m[c], red_l[wave][r] = sum;
     __syncthreads();
     float mw = m[c];
