@@ -26,7 +26,7 @@ struct PrefixShape {
   static constexpr int Row = TL::Row;
   // Eight waves, two on a SIMD, so that one's matrix operations run beside
   // the other's exponentials; wide heads do not fit their registers.
-  static constexpr int Waves = D <= 128 ? 8 : 4;
+  static constexpr int Waves = D <= 128 ? 8 : 4, WaveBits = D <= 128 ? 3 : 2;
   static constexpr int Blocks = 2;  // blocks of 16 rows of a wave (queries, accumulators)
   static constexpr int Rows = 16 * Blocks;
   static constexpr int RowF = D + 4;  // floats of a row of the parts: values, maximum, sum
@@ -40,8 +40,6 @@ struct PrefixShape {
   static constexpr int TileBytes = kTokens * Row;
   static constexpr int Pieces = Row / 16;                // 16-byte pieces of a row
   static constexpr int Loads = (16 * Pieces + 63) / 64;  // of the keys (and the values) of half a tile
-  static constexpr int RedDims = D > 128 ? D / 2 : D;    // dimensions that the waves' parts join at a time
-  static constexpr int RedF = RedDims + 4;
   // In LDS, piece q of row r lies at piece q ^ mix(r) of the row, so that the
   // rows that are read together lie in different banks (256 bytes hold all
   // banks once).  Keys: piece q of 16 rows, 8 of them at a time.  Values:
@@ -124,41 +122,36 @@ __device__ __forceinline__ void read_batch(const AttnParams& p, const Batch& s) 
   __syncthreads();
 }
 
-// Waves of a workgroup on different rows of a group (the others take other
-// tokens): as many as fit the group's blocks of ROWS rows without much of the
-// last workgroup's rows empty, since they share the tiles that one of them
-// loads.
-template <class S>
-__device__ __forceinline__ int row_waves(int rows) {
-  const int units = (rows + S::Rows - 1) / S::Rows;  // waves that work
-  int w = S::Waves;
-#pragma unroll
-  for (; w > S::Least; w >>= 1)
-    if ((units + w - 1) / w * w * 5 <= units * 6) break;
-  return w;
-}
-
 // How a group's prefix is cut: into blocks of rows and chunks of tokens.
 struct Cut {
-  int tiles, rows, waves, blocks, chunks;
+  int tiles, rows;
+  int wave_bits;  // 2^wave_bits waves of a workgroup on different rows, the others on other tokens
+  int blocks, chunks, each;  // each: tiles of a chunk
 };
-// `size`: tiles times row waves of an item.
+// Row waves share the tiles that LDS holds, so there are as many as fit the
+// rows without much of the last workgroup's empty.  `size`: tiles times row
+// waves of an item.
 template <class S>
 __device__ __forceinline__ Cut cut_of(const AttnParams& p, const Batch& s, int g, int size) {
   Cut c;
   c.tiles = tiles_of(s.lo[g], s.hi[g]);
   c.rows = (s.start[g + 1] - s.start[g]) * p.group;
-  c.waves = row_waves<S>(c.rows);
-  const int block = S::Rows * c.waves;
-  c.blocks = (c.rows + block - 1) / block;
-  const int each = ((size + c.waves - 1) / c.waves + S::Subs - 1) / S::Subs * S::Subs;
-  c.chunks = (c.tiles + each - 1) / each;
+  const int units = (c.rows + S::Rows - 1) / S::Rows;  // waves that work
+  c.wave_bits = S::WaveBits;
+#pragma unroll
+  for (int i = 0; i < S::WaveBits; ++i) {
+    const int w = 1 << c.wave_bits, padded = (units + w - 1) >> c.wave_bits << c.wave_bits;
+    if (c.wave_bits > 1 && padded * 5 > units * 6) --c.wave_bits;
+  }
+  c.blocks = (units + (1 << c.wave_bits) - 1) >> c.wave_bits;
+  c.each = (((size + (1 << c.wave_bits) - 1) >> c.wave_bits) + S::Subs - 1) / S::Subs * S::Subs;
+  c.chunks = (c.tiles + c.each - 1) / c.each;
   return c;
 }
 
 struct PrefixItem {
   int group, kh, block, chunk, row;  // row: the group's first row of the parts
-  int waves;
+  int wave_bits;
   int tile, tile_end;
 };
 
@@ -174,7 +167,7 @@ __device__ __forceinline__ bool find_prefix(const AttnParams& p, const Batch& s,
 #pragma unroll 1
   for (int g = g0; g < g1; ++g) {
     const Cut c = cut_of<S>(p, s, g, 1);
-    work += (float)c.tiles * (float)c.blocks * (float)c.waves;
+    work += (float)c.tiles * (float)(c.blocks << c.wave_bits);
   }
   const float even = fminf(ceilf(wave_add(work) * (float)p.kv_heads / (float)p.prefix_target * 1.0001f), 1e8f);
   int size = 0, mine = 0, upto = 0, rows = 0;
@@ -227,7 +220,7 @@ __device__ __forceinline__ bool find_prefix(const AttnParams& p, const Batch& s,
   it.group = __builtin_amdgcn_readfirstlane(g);
   it.kh = index % p.kv_heads;
   it.row = __builtin_amdgcn_readfirstlane(row);
-  it.waves = __builtin_amdgcn_readfirstlane(c.waves);
+  it.wave_bits = __builtin_amdgcn_readfirstlane(c.wave_bits);
   const int local = at - first;
   it.block = __builtin_amdgcn_readfirstlane(local % c.blocks);
   it.chunk = __builtin_amdgcn_readfirstlane(local / c.blocks);
@@ -369,9 +362,9 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   constexpr int kThreads = 64 * Waves;
   constexpr int kKeys = Subs * S::TileBytes, kBuf = 2 * kKeys;  // a step's keys, then its values
   // two buffers; before and after the loop other uses
-  constexpr int kPlan = 24 * kGroupsMax + 16, kRed = 4 * Waves * kHeads * S::RedF;
+  constexpr int kPlan = 24 * kGroupsMax + 16, kRed = 4 * Waves * S::Rows * RowF;
   __shared__ __attribute__((aligned(16))) uint8_t lds[at_least(2 * kBuf, at_least(kPlan, kRed))];
-  __shared__ float red_m[Waves][kHeads], red_l[Waves][kHeads];
+  __shared__ float red_m[Waves * S::Rows];
   __shared__ int scratch[Waves];
   __shared__ __attribute__((aligned(8))) uint8_t has_page[2][2 * S::Subs];  // of a step's buffer: half a tile each
 
@@ -391,37 +384,41 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kh = it.kh;
-  const int s0 = batch.start[it.group], rows = (batch.start[it.group + 1] - s0) * p.group;
+  const int s0 = batch.start[it.group], members = batch.start[it.group + 1] - s0, rows = members * p.group;
   const int prefix = batch.prefix(p, it.group);
   const int lo_all = batch.lo[it.group], hi_all = batch.hi[it.group];
-  // rows: those of wave % it.waves; tokens: those of wave / it.waves
-  const int streams = Waves / it.waves, stream = wave / it.waves;
-  const int row0 = (it.block * it.waves + wave % it.waves) * S::Rows;
+  // rows: those of wave % row_waves; tokens: those of wave / row_waves
+  const int row_waves = 1 << it.wave_bits, streams = Waves >> it.wave_bits, stream = wave >> it.wave_bits;
+  const int row0 = ((it.block << it.wave_bits) + (wave & (row_waves - 1))) * S::Rows;
 
-  // the lane's row of each block: queries and the tokens it sees
-  // (the factor is kept positive, for the maxima: a negative one turns the
-  // queries' signs, and with 0 the queries are multiplied by it instead)
-  float factor = p.scale * (p.k_scale ? p.k_scale[kh] : 1.0f) * kLog2e;
-  const bool turn = factor < 0.0f, zero = factor == 0.0f;
-  factor = zero ? 1.0f : fabsf(factor);
-  typename Mma<T>::op q[NB][TL::Steps];
-  int lo[NB], hi[NB];
+  // --- from the cache to LDS: the wave's half tiles of a step; the pages of
+  // 64 steps at a time, one per lane
+  const int32_t* table = p.table + s0 * p.table_stride;
+  const int steps = (it.tile_end - it.tile + Subs - 1) / Subs;
+  int page_of[S::Halves];
+  const bool fetches = wave < 4;
+  auto load_pages = [&](int step) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < S::Halves; ++j) {
+      const int half = wave * S::Halves + j, tile = it.tile + (step + lane) * Subs + half / 2;
+      const int t = tile * kTokens + 16 * (half & 1);
+      page_of[j] = tile < it.tile_end && t < hi_all ? table[t >> p.page_shift] : -1;
+      if (page_of[j] >= p.pages) page_of[j] = -1;
+    }
+  };
+  if (fetches) load_pages(0);
+
+  // the lane's row of each block: the tokens it sees
+  int lo[NB], hi[NB], member[NB], head[NB];
   bool none[NB];
   int lo_max = 0, hi_min = 0x7FFFFFFF;
-  const int members = rows / p.group;
 #pragma unroll
   for (int c = 0; c < NB; ++c) {  // (rows past the last read its queries)
-    const int row = row0 + 16 * c + r, member = min(row / p.group, members - 1), b = s0 + member;
-    const int head = row < rows ? row - member * p.group : 0;
-    const uint8_t* from = reinterpret_cast<const uint8_t*>(p.q + b * p.q_stride + (int64_t)(kh * p.group + head) * D);
-#pragma unroll
-    for (int s = 0; s < TL::Steps; ++s) {
-      uint32_t w[4];
-      load_bytes<16>(from + 2 * TL::q_dim(s, g), w);
-      __builtin_memcpy(&q[c][s], w, 16);
-    }
-    lo[c] = batch.first_seen(p, b);
-    hi[c] = min(batch.n[b], prefix);
+    const int row = row0 + 16 * c + r;
+    member[c] = min(row / p.group, members - 1);
+    head[c] = row < rows ? row - member[c] * p.group : 0;
+    lo[c] = batch.first_seen(p, s0 + member[c]);
+    hi[c] = min(batch.n[s0 + member[c]], prefix);
     // a row that sees nothing of the item's tokens (an unused sequence, a
     // window) does not keep the others from the fast path: it is emptied at
     // the end instead
@@ -439,43 +436,6 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   hi_min = __builtin_amdgcn_readfirstlane(hi_min);
   __syncthreads();  // (the batch is read: its place takes the tiles)
 
-  if (turn || zero) {
-#pragma unroll
-    for (int c = 0; c < NB; ++c)
-#pragma unroll
-      for (int s = 0; s < TL::Steps; ++s) {
-        uint32_t w[4];
-        __builtin_memcpy(w, &q[c][s], 16);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = zero ? not_finite_halves<T>(w[i]) : w[i] ^ 0x80008000u;
-        __builtin_memcpy(&q[c][s], w, 16);
-      }
-  }
-  f32x4 acc[NB][PL];
-  // maximum and sum of a row; over: what the exponent of a score gets added
-  float m[NB], l[NB], over[NB];
-#pragma unroll
-  for (int c = 0; c < NB; ++c) {
-    m[c] = -FLT_MAX, l[c] = 0.0f, over[c] = FLT_MAX;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) acc[c][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-  bool infinite = false;  // a value that is not finite was taken out
-
-  // --- from the cache to LDS: the wave's half tiles of a step; the pages of
-  // 64 steps at a time, one per lane
-  const int32_t* table = p.table + s0 * p.table_stride;
-  const int steps = (it.tile_end - it.tile + Subs - 1) / Subs;
-  int page_of[S::Halves];
-  auto load_pages = [&](int step) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < S::Halves; ++j) {
-      const int half = wave * S::Halves + j, tile = it.tile + (step + lane) * Subs + half / 2;
-      const int t = tile * kTokens + 16 * (half & 1);
-      page_of[j] = tile < it.tile_end && t < hi_all ? table[t >> p.page_shift] : -1;
-      if (page_of[j] >= p.pages) page_of[j] = -1;
-    }
-  };
   int from_k[S::Loads], from_v[S::Halves][S::Loads];  // where in a half's tokens a lane's piece of each load is
 #pragma unroll
   for (int i = 0; i < S::Loads; ++i) {
@@ -504,6 +464,53 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
       if (lane == 0) has_page[step & 1][half] = page >= 0;
     }
   };
+  if (fetches) {
+    if (steps > 0) fetch(0);
+    if (steps > 1) fetch(1);
+  }
+
+  // the queries, while those are on their way
+  // (the factor is kept positive, for the maxima: a negative one turns the
+  // queries' signs, and with 0 the queries are multiplied by it instead)
+  float factor = p.scale * (p.k_scale ? p.k_scale[kh] : 1.0f) * kLog2e;
+  const bool turn = factor < 0.0f, zero = factor == 0.0f;
+  factor = zero ? 1.0f : fabsf(factor);
+  typename Mma<T>::op q[NB][TL::Steps];
+#pragma unroll
+  for (int c = 0; c < NB; ++c) {
+    const uint8_t* from = reinterpret_cast<const uint8_t*>(p.q + (s0 + member[c]) * p.q_stride +
+                                                           (int64_t)(kh * p.group + head[c]) * D);
+#pragma unroll
+    for (int s = 0; s < TL::Steps; ++s) {
+      uint32_t w[4];
+      load_bytes<16>(from + 2 * TL::q_dim(s, g), w);
+      __builtin_memcpy(&q[c][s], w, 16);
+    }
+  }
+
+  if (turn || zero) {
+#pragma unroll
+    for (int c = 0; c < NB; ++c)
+#pragma unroll
+      for (int s = 0; s < TL::Steps; ++s) {
+        uint32_t w[4];
+        __builtin_memcpy(w, &q[c][s], 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = zero ? not_finite_halves<T>(w[i]) : w[i] ^ 0x80008000u;
+        __builtin_memcpy(&q[c][s], w, 16);
+      }
+  }
+  f32x4 acc[NB][PL];
+  // maximum and sum of a row; over: what the exponent of a score gets added
+  float m[NB], l[NB], over[NB];
+#pragma unroll
+  for (int c = 0; c < NB; ++c) {
+    m[c] = -FLT_MAX, l[c] = 0.0f, over[c] = FLT_MAX;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) acc[c][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  bool infinite = false;  // a value that is not finite was taken out
+
   // (the accumulators stay where the matrix operations have them: without
   // this the rare branch that rescales them makes the compiler move them all
   // to other registers and back for every tile)
@@ -583,19 +590,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   // before, so when all have come to their last tile of a step its buffer is
   // free for the step after the next, and that step's loads have a step's
   // time to land.
-  const bool fetches = wave < 4;
-  if (steps > 0) {
-    if (fetches) {
-      load_pages(0);
-      fetch(0);
-      if (steps > 1) fetch(1);
-    }
-    if (steps > 1) {
-      landed_barrier<2 * S::Halves * S::Loads>();
-    } else {
-      landed_barrier<0>();
-    }
-  }
+  if (steps > 0) landed_barrier<0>();
   auto pages_of = [&](int step) __attribute__((always_inline)) {
     uint64_t v = 0;
     __builtin_memcpy(&v, has_page[step & 1], 2 * Subs);
@@ -703,59 +698,57 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
     }
   }
 
-  // the parts of the waves with the same rows, a block after the other, into
-  // the chunk's
-  float(*const red)[kHeads][S::RedF] = reinterpret_cast<float(*)[kHeads][S::RedF]>(lds);
-  infinite = __syncthreads_or(infinite);
+  // the parts of the waves with the same rows into the chunk's: each brings
+  // its sums to the largest maximum, then they are added up
+  float(*const red)[RowF] = reinterpret_cast<float(*)[RowF]>(lds);  // [Waves * Rows]
+  infinite = __syncthreads_or(infinite);  // (also: the tiles are read)
 #pragma unroll
   for (int c = 0; c < NB; ++c) {
-    const float sum = none[c] ? 0.0f : column_sum(l[c]);
-    if (none[c]) {
-      m[c] = -FLT_MAX;
+    l[c] = none[c] ? 0.0f : column_sum(l[c]);
+    m[c] = none[c] ? -FLT_MAX : m[c];
+    if (g == 0) red_m[wave * S::Rows + 16 * c + r] = m[c];
+  }
+  __syncthreads();
 #pragma unroll
-      for (int i = 0; i < PL; ++i) acc[c][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-    if (g == 0) red_m[wave][r] = m[c], red_l[wave][r] = sum;
-    __syncthreads();
+  for (int c = 0; c < NB; ++c) {
     float mw = m[c];
-    for (int w = wave % it.waves; w < Waves; w += it.waves) mw = fmaxf(mw, red_m[w][r]);
-    const float f = __builtin_amdgcn_exp2f(m[c] - mw);
+    for (int w = wave & (row_waves - 1); w < Waves; w += row_waves) mw = fmaxf(mw, red_m[w * S::Rows + 16 * c + r]);
+    const float f = none[c] ? 0.0f : __builtin_amdgcn_exp2f(m[c] - mw);
+    float* const row = red[wave * S::Rows + 16 * c + r];
 #pragma unroll
-    for (int d0 = 0; d0 < D; d0 += S::RedDims) {
-      if (d0) __syncthreads();  // (the dimensions before are read)
+    for (int i = 0; i < PL; ++i) {
+      const f32x4 o = acc[c][i] * f;
+      *reinterpret_cast<f32x4*>(row + 16 * i + 4 * g) = none[c] ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : o;
+    }
+    if (g == 0) row[D] = mw, row[D + 1] = none[c] ? 0.0f : l[c] * f;
+  }
+  __syncthreads();
+  const int first_row = it.block * row_waves * S::Rows;
+  float* const parts = p.prefix_parts + ((int64_t)it.row + ((int64_t)it.chunk * p.kv_heads + kh) * rows + first_row) * RowF;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < row_waves * S::Rows * (D / 4); i += kThreads) {
+    const int k = i / (D / 4), d = 4 * (i % (D / 4));
+    if (first_row + k >= rows) break;
+    f32x4 o = *reinterpret_cast<const f32x4*>(&red[k][d]);
+    float sum = red[k][D + 1];
+    for (int w = row_waves; w < Waves; w += row_waves) {
+      o += *reinterpret_cast<const f32x4*>(&red[w * S::Rows + k][d]);
+      sum += red[w * S::Rows + k][D + 1];
+    }
+    if (__builtin_expect(infinite || any_nan(o), false) && sum == sum) {
+      int seen_lo, seen_hi;
+      visible(p, s0 + (first_row + k) / p.group, seen_lo, seen_hi);
+      seen_lo = max(seen_lo, it.tile * kTokens);
+      seen_hi = min(min(seen_hi, prefix), it.tile_end * kTokens);
+      if (seen_lo < seen_hi) {
+        const f32x4 y = infinite_values<C, D>(table, reinterpret_cast<const typename C::bits_t*>(p.v_cache), p.pages,
+                                              p.kv_heads, kh, p.page_shift, seen_lo, seen_hi, d);
 #pragma unroll
-      for (int i = d0 / 16; i < (d0 + S::RedDims) / 16; ++i)
-        *reinterpret_cast<f32x4*>(&red[wave][r][16 * i - d0 + 4 * g]) = acc[c][i] * f;
-      __syncthreads();
-      for (int i = threadIdx.x; i < it.waves * kHeads * (S::RedDims / 4); i += kThreads) {
-        const int which = i / (kHeads * (S::RedDims / 4)), h = i / (S::RedDims / 4) % kHeads;
-        const int d = 4 * (i % (S::RedDims / 4)), row = (it.block * it.waves + which) * S::Rows + 16 * c + h;
-        if (row >= rows) continue;
-        float mh = red_m[which][h], lh = 0.0f;
-        f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int w = which + it.waves; w < Waves; w += it.waves) mh = fmaxf(mh, red_m[w][h]);
-        for (int w = which; w < Waves; w += it.waves) {
-          lh += red_l[w][h] * __builtin_amdgcn_exp2f(red_m[w][h] - mh);
-          o += *reinterpret_cast<const f32x4*>(&red[w][h][d]);
-        }
-        if (__builtin_expect(infinite || any_nan(o), false) && lh == lh) {
-          int seen_lo, seen_hi;
-          visible(p, s0 + row / p.group, seen_lo, seen_hi);
-          seen_lo = max(seen_lo, it.tile * kTokens);
-          seen_hi = min(min(seen_hi, prefix), it.tile_end * kTokens);
-          if (seen_lo < seen_hi) {
-            const f32x4 x = infinite_values<C, D>(table, reinterpret_cast<const typename C::bits_t*>(p.v_cache), p.pages,
-                                                  p.kv_heads, kh, p.page_shift, seen_lo, seen_hi, d0 + d);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[k] = x[k] != 0.0f ? x[k] : o[k];
-          }
-        }
-        float* out = p.prefix_parts + ((int64_t)it.row + ((int64_t)it.chunk * p.kv_heads + kh) * rows + row) * RowF;
-        *reinterpret_cast<f32x4*>(out + d0 + d) = o;
-        if (d0 + d == 0) *reinterpret_cast<float2*>(out + D) = make_float2(mh, lh);
+        for (int j = 0; j < 4; ++j) o[j] = y[j] != 0.0f ? y[j] : o[j];
       }
     }
-    if (c + 1 < NB) __syncthreads();  // (the block is read)
+    *reinterpret_cast<f32x4*>(parts + (int64_t)k * RowF + d) = o;
+    if (d == 0) *reinterpret_cast<float2*>(parts + (int64_t)k * RowF + D) = make_float2(red[k][D], sum);
   }
 }
 
