@@ -526,7 +526,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
       for (int i = 0; i < TL::Steps; ++i) asm("" : "+a"(q[c][i]));
   };
   // --- a tile's operands, from LDS
-  TL x;  // (its keys)
+  TL tl;  // (its keys)
   typename Mma<V>::op v[PL];
   uint32_t bytes[TL::ES == 1 ? PL : 1][2];  // 8-bit values as they are read
   auto load_keys = [&](int step, int sub) __attribute__((always_inline)) {
@@ -536,12 +536,12 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
       const uint8_t* row = keys + (16 * j + r) * Row;
       if constexpr (TL::ES == 2) {
 #pragma unroll
-        for (int st = 0; st < TL::Steps; ++st) load_bytes<16>(row + 16 * ((4 * st + g) ^ S::mix_k(r)), &x.k[j][4 * st]);
+        for (int st = 0; st < TL::Steps; ++st) load_bytes<16>(row + 16 * ((4 * st + g) ^ S::mix_k(r)), &tl.k[j][4 * st]);
       } else {
 #pragma unroll
-        for (int u = 0; u < D / 64; ++u) load_bytes<16>(row + 16 * ((4 * u + g) ^ S::mix_k(r)), &x.k[j][4 * u]);
+        for (int u = 0; u < D / 64; ++u) load_bytes<16>(row + 16 * ((4 * u + g) ^ S::mix_k(r)), &tl.k[j][4 * u]);
         if constexpr (D % 64)
-          load_bytes<8>(row + 16 * ((4 * (D / 64) + (g >> 1)) ^ S::mix_k(r)) + 8 * (g & 1), &x.k[j][4 * (D / 64)]);
+          load_bytes<8>(row + 16 * ((4 * (D / 64) + (g >> 1)) ^ S::mix_k(r)) + 8 * (g & 1), &tl.k[j][4 * (D / 64)]);
       }
     }
   };
@@ -613,7 +613,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
         for (int c = 0; c < NB; ++c) s[c][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int st = 0; st < TL::Steps; ++st) {
-          const typename Mma<T>::op k = x.k_op(j, st);
+          const typename Mma<T>::op k = tl.k_op(j, st);
 #pragma unroll
           for (int c = 0; c < NB; ++c) s[c][j] = Mma<T>::mul(k, q[c][st], s[c][j]);
         }
@@ -644,18 +644,28 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
           __builtin_memcpy(&v[i], w, 16);
         }
       }
-      float top[NB];
-      bool raise = false;
+      // exponents of the probabilities (2^lift times them).  The maxima are
+      // taken of these, whose products the compiler need not quieten first.
+      float x[NB][8];
+      auto exponents = [&]() __attribute__((always_inline)) {
 #pragma unroll
-      for (int c = 0; c < NB; ++c) {
-        top[c] = fmaxf(fmaxf(fmaxf(s[c][0][0], s[c][0][1]), fmaxf(s[c][0][2], s[c][0][3])),
-                       fmaxf(fmaxf(s[c][1][0], s[c][1][1]), fmaxf(s[c][1][2], s[c][1][3])));
-        raise |= fmaf(top[c], factor, over[c]) > kSlack + Mma<V>::lift;
-      }
-      if (__any(raise)) {
+        for (int c = 0; c < NB; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[c][i] = fmaf(s[c][i >> 2][i & 3], factor, over[c]);
+      };
+      exponents();
+      float top = x[0][0];
+#pragma unroll
+      for (int c = 0; c < NB; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, x[c][i]);
+      if (__any(top > kSlack + Mma<V>::lift)) {
 #pragma unroll
         for (int c = 0; c < NB; ++c) {
-          const float mn = fmaxf(m[c], column_max(top[c]) * factor);
+          float most = s[c][0][0];
+#pragma unroll
+          for (int i = 1; i < 8; ++i) most = fmaxf(most, s[c][i >> 2][i & 3]);
+          const float mn = fmaxf(m[c], column_max(most) * factor);
           const float f = __builtin_amdgcn_exp2f(m[c] - mn);
           l[c] *= f;
 #pragma unroll
@@ -663,6 +673,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
           m[c] = mn;
           over[c] = Mma<V>::lift - mn;
         }
+        exponents();
       }
       // the next tile (after the last one, this one again)
       int next_step = step, next_sub = sub + streams;
@@ -686,7 +697,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
         float e[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          e[i] = __builtin_amdgcn_exp2f(fmaf(s[c][i >> 2][i & 3], factor, over[c]));
+          e[i] = __builtin_amdgcn_exp2f(x[c][i]);
           l[c] += e[i];
         }
         const typename Mma<V>::op pr = Mma<V>::round(e);
