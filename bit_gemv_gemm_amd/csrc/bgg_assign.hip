@@ -33,6 +33,7 @@ struct AssignParams {
 };
 
 constexpr uint32_t kNotServed = 0xFFFFFFFFu;
+constexpr int kBack = 4;  // pages given back at a time by a thread
 
 // What fill() needs of the sequences, in LDS.
 template <int N>
@@ -90,32 +91,56 @@ __device__ __forceinline__ int first_above(const uint32_t* v, int n, uint32_t x)
   return lo;
 }
 
-// Rows first .. end - 1.  `top` is the height of the stack before pages were
-// taken.
-template <int THREADS, int N>
+// Rows first .. end - 1, EACH neighbours per thread: one looks its sequence
+// up, the others look on from there, and their page numbers are loaded
+// together.  `top` is the height of the stack before pages were taken.
+template <int THREADS, int EACH, int N>
 __device__ __forceinline__ void fill(const AssignParams& p, const Sums<N>& s, int first, int end, uint32_t top) {
+  typedef int32_t positions_t __attribute__((ext_vector_type(EACH), aligned(4)));
+  typedef int64_t slots_t __attribute__((ext_vector_type(EACH), aligned(8)));
   const int cells = (1 << p.page_shift) - 1;
-#pragma unroll 2
-  for (int t = first + (int)threadIdx.x; t < end; t += THREADS) {
-    int32_t position = 0;
-    int64_t slot = -1;
-    const int b = first_above(s.end, p.batch, (uint32_t)t);
-    if (b < p.batch && s.taken[b] != kNotServed) {
-      const uint32_t past = s.past[b];
-      position = (int32_t)(past + (uint32_t)t - (b ? s.end[b - 1] : 0u));
-      const int entry = position >> p.page_shift, held = (int)((past + cells) >> p.page_shift);
-      int32_t* const cell = p.table + b * p.table_stride + entry;
-      int32_t page;
-      if (entry >= held) {
-        page = p.free_pages[top - 1 - (s.taken[b] + (uint32_t)(entry - held))];
-        if ((position & cells) == 0) *cell = page;  // (a new page's first token is always new)
-      } else {
-        page = *cell;
+#pragma unroll 1
+  for (int t = first + EACH * (int)threadIdx.x; t < end; t += EACH * THREADS) {
+    int32_t position[EACH], page[EACH];
+    int32_t* cell[EACH];
+    bool fresh[EACH];
+    int b = -1;
+    uint32_t before = 0, upto = 0, taken = kNotServed, past = 0;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      if (i == 0 || (b < p.batch && upto <= (uint32_t)(t + i))) {
+        b += 1 + first_above(s.end + (b + 1), p.batch - (b + 1), (uint32_t)(t + i));
+        if (b < p.batch) before = b ? s.end[b - 1] : 0u, upto = s.end[b], taken = s.taken[b], past = s.past[b];
       }
-      if (page >= 0 && page < p.pages) slot = ((int64_t)page << p.page_shift) + (position & cells);
+      position[i] = 0, page[i] = -1, fresh[i] = false;
+      cell[i] = nullptr;
+      if (b < p.batch && taken != kNotServed && t + i < end) {
+        position[i] = (int32_t)(past + (uint32_t)(t + i) - before);
+        const int entry = position[i] >> p.page_shift, held = (int)((past + cells) >> p.page_shift);
+        cell[i] = p.table + b * p.table_stride + entry;
+        fresh[i] = entry >= held;
+        page[i] = *(fresh[i] ? p.free_pages + (top - 1 - (taken + (uint32_t)(entry - held))) : cell[i]);
+      }
     }
-    p.positions[t] = position;
-    p.slots[t] = slot;
+    int64_t slot[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      // (a new page's first token is always new)
+      if (fresh[i] && (position[i] & cells) == 0) *cell[i] = page[i];
+      slot[i] = page[i] >= 0 && page[i] < p.pages ? ((int64_t)page[i] << p.page_shift) + (position[i] & cells) : -1;
+    }
+    if (t + EACH <= end) {
+      positions_t x;
+      slots_t y;
+#pragma unroll
+      for (int i = 0; i < EACH; ++i) x[i] = position[i], y[i] = slot[i];
+      *reinterpret_cast<positions_t*>(p.positions + t) = x;
+      *reinterpret_cast<slots_t*>(p.slots + t) = y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < EACH; ++i)
+        if (t + i < end) p.positions[t + i] = position[i], p.slots[t + i] = slot[i];
+    }
   }
 }
 
@@ -166,25 +191,42 @@ __global__ void __launch_bounds__(THREADS) k_cache_plan(AssignParams p) {
     }
     __syncthreads();
 #pragma unroll 1
-    for (uint32_t done = 0; done < entries; done += THREADS) {
-      int page = -1;
-      if (done + tid < entries) {
-        const uint32_t e = entries - 1 - (done + tid);
-        const int b = first_above(s.end, p.batch, e);
-        page = p.table[b * p.table_stride + s.past[b] + (e - (b ? s.end[b - 1] : 0u))];
+    for (uint32_t done = 0; done < entries; done += kBack * THREADS) {
+      // (kBack neighbours per thread, loaded together)
+      int32_t page[kBack];
+      int b = p.batch;
+      uint32_t low = 0;
+#pragma unroll
+      for (int i = 0; i < kBack; ++i) {
+        const uint32_t k = done + kBack * tid + i, e = entries - 1 - k;
+        page[i] = -1;
+        if (k >= entries) continue;
+        if (i == 0 || e < low) {
+          b = first_above(s.end, b, e);
+          low = b ? s.end[b - 1] : 0u;
+        }
+        page[i] = p.table[b * p.table_stride + s.past[b] + (e - low)];
       }
-      const bool is = page >= 0 && page < p.pages;
-      const uint64_t those = __ballot(is);
-      if (lane == 0) waves[0][wave] = (uint32_t)__popcll(those);
+      uint32_t at = top, all_of_wave = 0, pushed = 0;
+#pragma unroll
+      for (int i = 0; i < kBack; ++i) {
+        const uint64_t those = __ballot(page[i] >= 0 && page[i] < p.pages);
+        at += (uint32_t)__popcll(those & ((1ull << lane) - 1));
+        all_of_wave += (uint32_t)__popcll(those);
+      }
+      if (lane == 0) waves[0][wave] = all_of_wave;
       __syncthreads();
-      uint32_t at = top + (uint32_t)__popcll(those & ((1ull << lane) - 1));
-      uint32_t pushed = 0;
 #pragma unroll
       for (int w = 0; w < THREADS / 64; ++w) {
         if (w < wave) at += waves[0][w];
         pushed += waves[0][w];
       }
-      if (is && at < (uint32_t)p.capacity) p.free_pages[at] = page;
+#pragma unroll
+      for (int i = 0; i < kBack; ++i) {
+        if (page[i] < 0 || page[i] >= p.pages) continue;
+        if (at < (uint32_t)p.capacity) p.free_pages[at] = page[i];
+        ++at;
+      }
       top = min(top + pushed, (uint32_t)p.capacity);
       __syncthreads();  // (also the stores: rows read them below)
     }
@@ -203,13 +245,14 @@ __global__ void __launch_bounds__(THREADS) k_cache_plan(AssignParams p) {
   }
   uint32_t none = 0, upto = needs, all_needs;
   sums_before<THREADS>(none, upto, all_needs, most, waves);
+  uint32_t last = 0;  // pages taken up to this thread's last sequence that takes some
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int b = tid * PER + i;
     const uint32_t first = upto;
     upto += need[i];
     const bool served = fits[i] && (need[i] == 0 || upto <= top);
-    if (served && need[i]) atomicMax(&last_taken, upto);
+    if (served && need[i]) last = upto;
     if (b < p.batch) {
       p.lengths_out[b] = (int32_t)(past[i] + (served ? count[i] : 0u));
       p.past[b] = (int32_t)past[i];
@@ -217,12 +260,16 @@ __global__ void __launch_bounds__(THREADS) k_cache_plan(AssignParams p) {
       if (FILL) s.end[b] = row_end[i], s.taken[b] = served ? first : kNotServed, s.past[b] = past[i];
     }
   }
+  // (one atomic per wave: of 64 lanes each it took SPLIT)
+#pragma unroll
+  for (int i = 32; i > 0; i >>= 1) last = max(last, (uint32_t)__shfl_xor((int)last, i));
+  if (lane == 0 && last) atomicMax(&last_taken, last);
   __syncthreads();
   if (tid == 0) {
     p.starts[0] = 0;
     p.free_count_out[0] = (int32_t)(top - last_taken);
   }
-  if (FILL) fill<THREADS>(p, s, 0, p.rows, top);
+  if (FILL) fill<THREADS, 1>(p, s, 0, p.rows, top);
 }
 
 // The rows, after k_cache_plan: each workgroup forms the sums again from what
@@ -260,7 +307,7 @@ __global__ void __launch_bounds__(THREADS) k_cache_fill(AssignParams p) {
   }
   __syncthreads();
   const int t0 = blockIdx.x * p.rows_per_group;
-  fill<THREADS>(p, s, t0, min(p.rows, t0 + p.rows_per_group), (uint32_t)p.free_count_out[0] + all_needs);
+  fill<THREADS, 4>(p, s, t0, min(p.rows, t0 + p.rows_per_group), (uint32_t)p.free_count_out[0] + all_needs);
 }
 
 // Rows that the planning workgroup writes itself; more are a launch of their

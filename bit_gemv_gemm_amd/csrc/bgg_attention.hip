@@ -155,7 +155,7 @@ __device__ __forceinline__ void store_out(const AttnParams& p, int b, int h, int
 template <int D>
 __device__ __forceinline__ void add_prefix(const AttnParams& p, int b, int kh, int i, int d, f32x4& o, float& m,
                                            float& l) {
-  constexpr int kFlight = 4, RowF = D + 4;
+  constexpr int kFlight = 8, RowF = D + 4;  // (parts in flight: of 4, 8 and 16, 8 measured best)
   const SharedSeq q = p.seqs[b];
   const float* at = p.prefix_parts + ((int64_t)q.row + (int64_t)kh * q.rows + i) * RowF;
   const int64_t step = (int64_t)p.kv_heads * q.rows * RowF;
@@ -207,20 +207,20 @@ __device__ __forceinline__ void add_prefix(const AttnParams& p, int b, int kh, i
 // to memory.  This code runs once, by one workgroup per sequence and head
 // block, so its instructions come from memory too: it is kept short by loops
 // (unrolled to 16 parts in flight and three columns per thread it took 9 us
-// for 32 chunks of 6 x 128).  `lds` holds 32 kMaxChunks floats.
-template <class T, class V, int D, bool SHARED>
+// for 32 chunks of 6 x 128).  `lds` holds 32 most_chunks floats.
+template <class T, class V, int D, bool SHARED, int WAVES>
 __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, const float* parts,
                                            int64_t step, int rows, int heads, int h0, float vs,
                                            float* lds, float* lds16) {
-  constexpr int kThreads = 64 * kWaves, kRows = kThreads / 16;  // threads of a head
+  constexpr int kThreads = 64 * WAVES, kRows = kThreads / 16;  // threads of a head
   constexpr int kFlight = 8;                                    // a thread's parts in flight
   const int tid = threadIdx.x, hr = tid & 15, cr = tid >> 4;
   const int columns = heads * (D / 4);
   const int share = columns >= kThreads ? 1 : kThreads / columns;  // threads per column
   const int part_of = share > 1 ? tid / columns : 0;
   int col = share > 1 ? tid % columns : tid;
-  float* weight = lds;                     // [chunks][16]
-  float* sum = lds + 16 * kMaxChunks;      // [chunks][16]
+  float* weight = lds;                            // [chunks][16]
+  float* sum = lds + 16 * most_chunks(WAVES);     // [chunks][16]
 
   uint64_t a[kFlight][2];
   auto load_flight = [&](int c0, int cb) {
@@ -325,17 +325,17 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
 // arrives last adds the parts in chunk order.  SHARED: the items are
 // bgg_shared.hip's, of the sequences' own tokens, and the parts of the prefix
 // join at the end.
-template <class T, class C, int D, bool SHARED>
-__global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 384 ? 1 : 2) k_paged_attention(AttnParams p) {
+template <class T, class C, int D, bool SHARED, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, sizeof(typename C::bits_t) * D > 384 ? 1 : 2) k_paged_attention(AttnParams p) {
   using TL = Tile<T, C, D>;
   using V = typename TL::V;
   constexpr int PL = TL::PL;
   constexpr int RowF = D + 4;  // floats between heads in LDS
   // the waves' accumulators, then join_parts' weights and sums
-  constexpr int kRed = kWaves * kHeads * RowF, kJoin = 32 * kMaxChunks;
+  constexpr int kRed = WAVES * kHeads * RowF, kJoin = 32 * most_chunks(WAVES);
   __shared__ __attribute__((aligned(16))) float lds[kRed > kJoin ? kRed : kJoin];
-  __shared__ float red_m[kWaves][kHeads], red_l[kWaves][kHeads], red_j[64 * kWaves + 32];
-  static_assert(4 * 64 * kWaves <= 16 * kMaxChunks, "the shares of the columns fit");
+  __shared__ float red_m[WAVES][kHeads], red_l[WAVES][kHeads], red_j[64 * WAVES + 32];
+  static_assert(4 * 64 * WAVES <= 16 * most_chunks(WAVES), "the shares of the columns fit");
   float(*red)[kHeads][RowF] = reinterpret_cast<float(*)[kHeads][RowF]>(lds);
   __shared__ uint32_t arrived;
 
@@ -375,8 +375,8 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
   auto load_pages = [&](int tile) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int t = (tile + kWaves * lane) * kTokens + 16 * j;
-      page_of[j] = tile + kWaves * lane < it.tile_end && t < it.n ? table[t >> p.page_shift] : -1;
+      const int t = (tile + WAVES * lane) * kTokens + 16 * j;
+      page_of[j] = tile + WAVES * lane < it.tile_end && t < it.n ? table[t >> p.page_shift] : -1;
       if (page_of[j] >= p.pages) page_of[j] = -1;
     }
   };
@@ -409,10 +409,10 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
     tl.load_v(now.v, lane);
     __builtin_amdgcn_sched_barrier(0);
   }
-  for (int tile = first, step = 0; tile < it.tile_end; tile += kWaves, ++step) {
+  for (int tile = first, step = 0; tile < it.tile_end; tile += WAVES, ++step) {
     // the tile after this one, or this one again (loads without a branch
     // keep the waits for the loads before them exact)
-    const bool more = tile + kWaves < it.tile_end;
+    const bool more = tile + WAVES < it.tile_end;
     // scores of head r: tokens 16 j + 4 g + i
     f32x4 s[2];
 #pragma unroll
@@ -421,8 +421,8 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
 #pragma unroll
       for (int st = 0; st < TL::Steps; ++st) s[j] = Mma<T>::mul(tl.k_op(j, st), q[st], s[j]);
     }
-    if (more && ((step + 1) & 63) == 0) load_pages(tile + kWaves);
-    const Place next = place(step + more, tile + (more ? kWaves : 0));
+    if (more && ((step + 1) & 63) == 0) load_pages(tile + WAVES);
+    const Place next = place(step + more, tile + (more ? WAVES : 0));
     __builtin_amdgcn_sched_barrier(0);
     tl.load_k(next.k, lane);
     __builtin_amdgcn_sched_barrier(0);
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
   __syncthreads();
   float mw = red_m[0][r];
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) mw = fmaxf(mw, red_m[w][r]);
+  for (int w = 1; w < WAVES; ++w) mw = fmaxf(mw, red_m[w][r]);
   if (r < heads) {
     const float f = __builtin_amdgcn_exp2f(m - mw);
 #pragma unroll
@@ -495,14 +495,14 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
   const int64_t slot = part_floats(rows, D);
   float* part = p.parts + ((int64_t)it.part * H + it.head_block) * slot;
   const int columns = heads * (D / 4);
-  for (int i = threadIdx.x; i < columns; i += 64 * kWaves) {
+  for (int i = threadIdx.x; i < columns; i += 64 * WAVES) {
     const int h = i / (D / 4), d = 4 * (i % (D / 4));
     float mh = red_m[0][h], lh = 0.0f;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) mh = fmaxf(mh, red_m[w][h]);
+    for (int w = 1; w < WAVES; ++w) mh = fmaxf(mh, red_m[w][h]);
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
       lh += red_l[w][h] * __builtin_amdgcn_exp2f(red_m[w][h] - mh);
       o += *reinterpret_cast<const f32x4*>(&red[w][h][d]);
     }
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(64 * kWaves, sizeof(typename C::bits_t) * D > 
   __syncthreads();
   if (arrived != (uint32_t)it.chunks - 1) return;
   if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  join_parts<T, V, D, SHARED>(p, it, part - (int64_t)it.chunk * H * slot, H * slot, rows, heads, h0, vs,
+  join_parts<T, V, D, SHARED, WAVES>(p, it, part - (int64_t)it.chunk * H * slot, H * slot, rows, heads, h0, vs,
                    lds, red_j);
 }
 
@@ -568,30 +568,30 @@ AttnPlan plan_attention(const bgg_cache_desc* c, int64_t q_heads, int64_t batch)
   return p;
 }
 
-template <class T, class C, bool SHARED>
+template <class T, class C, bool SHARED, int WAVES>
 void launch_dim(const AttnParams& p, int64_t items, int64_t head_dim, hipStream_t s) {
-  const dim3 grid((unsigned)items), block(64 * kWaves);
+  const dim3 grid((unsigned)items), block(64 * WAVES);
   switch (head_dim) {
-    case 64: hipLaunchKernelGGL((k_paged_attention<T, C, 64, SHARED>), grid, block, 0, s, p); break;
-    case 96: hipLaunchKernelGGL((k_paged_attention<T, C, 96, SHARED>), grid, block, 0, s, p); break;
-    case 128: hipLaunchKernelGGL((k_paged_attention<T, C, 128, SHARED>), grid, block, 0, s, p); break;
-    case 192: hipLaunchKernelGGL((k_paged_attention<T, C, 192, SHARED>), grid, block, 0, s, p); break;
-    default: hipLaunchKernelGGL((k_paged_attention<T, C, 256, SHARED>), grid, block, 0, s, p); break;
+    case 64: hipLaunchKernelGGL((k_paged_attention<T, C, 64, SHARED, WAVES>), grid, block, 0, s, p); break;
+    case 96: hipLaunchKernelGGL((k_paged_attention<T, C, 96, SHARED, WAVES>), grid, block, 0, s, p); break;
+    case 128: hipLaunchKernelGGL((k_paged_attention<T, C, 128, SHARED, WAVES>), grid, block, 0, s, p); break;
+    case 192: hipLaunchKernelGGL((k_paged_attention<T, C, 192, SHARED, WAVES>), grid, block, 0, s, p); break;
+    default: hipLaunchKernelGGL((k_paged_attention<T, C, 256, SHARED, WAVES>), grid, block, 0, s, p); break;
   }
 }
 
-template <bool SHARED>
+template <bool SHARED, int WAVES>
 void launch_attention(const AttnParams& p, int64_t items, int32_t type, bool e4m3, int64_t head_dim, hipStream_t s) {
   if (type == BGG_TYPE_F16) {
     if (e4m3)
-      launch_dim<F16, E4M3, SHARED>(p, items, head_dim, s);
+      launch_dim<F16, E4M3, SHARED, WAVES>(p, items, head_dim, s);
     else
-      launch_dim<F16, F16, SHARED>(p, items, head_dim, s);
+      launch_dim<F16, F16, SHARED, WAVES>(p, items, head_dim, s);
   } else {
     if (e4m3)
-      launch_dim<BF16, E4M3, SHARED>(p, items, head_dim, s);
+      launch_dim<BF16, E4M3, SHARED, WAVES>(p, items, head_dim, s);
     else
-      launch_dim<BF16, BF16, SHARED>(p, items, head_dim, s);
+      launch_dim<BF16, BF16, SHARED, WAVES>(p, items, head_dim, s);
   }
 }
 
@@ -652,7 +652,7 @@ bgg_status attend(const char* who, const bgg_cache_desc* c, const bgg_attention_
   const bool e4m3 = c->type == BGG_TYPE_E4M3;
   hipStream_t s = (hipStream_t)stream;
   if (!shared || shared->groups == 0) {
-    launch_attention<false>(p, plan.items, a->type, e4m3, c->head_dim, s);
+    launch_attention<false, kWaves>(p, plan.items, a->type, e4m3, c->head_dim, s);
     return hip_check(who);
   }
   uint8_t* const w = (uint8_t*)a->workspace;
@@ -660,6 +660,13 @@ bgg_status attend(const char* who, const bgg_cache_desc* c, const bgg_attention_
   p.shared_pages = shared->shared_pages_dev;
   p.groups = (int)shared->groups;
   p.prefix_target = (int)plan.target;
+  // A batch of so many sequences and head blocks fills the GPU with one wave
+  // for each, and the starts and ends of workgroups of four cost more than
+  // four waves to a sequence save (256 sequences of up to 200 own tokens, 8 key
+  // heads of 128: one wave 19.1 us, four 25.8; where fewer workgroups are there
+  // four are faster: 64 sequences of up to 300, 15.6 against 12.4 us).
+  const bool single = a->batch * plan.heads >= 4 * plan.target;
+  p.own_chunks = most_chunks(single ? 1 : kWaves);
   p.own_count = (int32_t*)(w + more.items - 256);
   p.own_items = (OwnItem*)(w + more.items);
   p.seqs = (SharedSeq*)(w + more.seqs);
@@ -667,7 +674,10 @@ bgg_status attend(const char* who, const bgg_cache_desc* c, const bgg_attention_
   launch_prefix(p, a->type, e4m3, c->head_dim, s);
   const bgg_status st = hip_check(who);
   if (st) return st;
-  launch_attention<true>(p, plan.items, a->type, e4m3, c->head_dim, s);
+  if (p.own_chunks == kMaxChunks)
+    launch_attention<true, kWaves>(p, plan.items, a->type, e4m3, c->head_dim, s);
+  else
+    launch_attention<true, 1>(p, plan.items, a->type, e4m3, c->head_dim, s);
   return hip_check(who);
 }
 

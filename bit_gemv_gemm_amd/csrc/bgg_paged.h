@@ -49,6 +49,7 @@ struct AttnParams {
   // sequences that share a prefix (bgg_shared_attention)
   const int32_t *group_starts, *shared_pages;
   int groups, prefix_target;
+  int own_chunks;  // chunks of a sequence at most
   int32_t* own_count;  // [1]: entries of own_items
   OwnItem* own_items;
   SharedSeq* seqs;     // [batch]
@@ -97,6 +98,8 @@ __host__ __device__ constexpr int64_t part_floats(int64_t rows, int64_t D) {
 // Chunks of a sequence at most (the items of one sequence and head block,
 // about target_items of which there are kMaxItems at most).
 constexpr int kMaxItems = 256, kMaxChunks = kMaxItems + 1;
+// (a workgroup of one wave holds the weights of fewer parts)
+__host__ __device__ constexpr int most_chunks(int waves) { return waves == 1 ? 64 : kMaxChunks; }
 
 // ---------------------------------------------------------------------------
 // lane moves

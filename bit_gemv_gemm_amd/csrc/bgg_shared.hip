@@ -246,6 +246,7 @@ __device__ __forceinline__ void plan_own(const AttnParams& p, const Batch& s, co
     const int g = s.group_of(G, b);
     if (s.start[g] <= b && b < s.start[g + 1]) lo = max(lo, s.prefix(p, g));
   };
+  auto own_chunks = [&](int tiles, int size) { return chunks_of(tiles, max(size, (tiles + p.own_chunks - 1) / p.own_chunks)); };
   float* const sums = reinterpret_cast<float*>(scratch);
   float tiles = 0.0f;
 #pragma unroll 1
@@ -281,7 +282,7 @@ __device__ __forceinline__ void plan_own(const AttnParams& p, const Batch& s, co
     for (int b = b0; b < b1; ++b) {
       int lo, n;
       own(b, lo, n);
-      mine += both_counts(chunks_of(tiles_of(lo, n), size));
+      mine += both_counts(own_chunks(tiles_of(lo, n), size));
     }
     const int upto = scan_add(mine);
     if (lane == 63) scratch[wave] = upto;
@@ -301,7 +302,7 @@ __device__ __forceinline__ void plan_own(const AttnParams& p, const Batch& s, co
   for (int b = b0; b < b1; ++b) {
     OwnItem it;
     own(b, it.lo, it.n);
-    const int t = tiles_of(it.lo, it.n), first = it.lo / kTokens, chunks = chunks_of(t, size);
+    const int t = tiles_of(it.lo, it.n), first = it.lo / kTokens, chunks = own_chunks(t, size);
     const int each = (t + chunks - 1) / chunks;
     it.b = b;
     it.chunks = chunks;
