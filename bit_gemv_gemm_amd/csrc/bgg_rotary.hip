@@ -48,9 +48,16 @@ __device__ __forceinline__ void angle_of(int32_t position, float freq, float* c,
 __device__ __forceinline__ void angles_to_lds(const RotaryParams& p, int64_t t, float* cs, float* sn) {
   if ((int)threadIdx.x < p.pairs) {
     float c, s;
-    const int32_t* positions = p.positions;
-    if (p.axis_of_pair) positions += min((int)p.axis_of_pair[threadIdx.x], p.last_axis) * p.axis_stride;
-    angle_of(positions[t], p.freqs[threadIdx.x], &c, &s);
+    int32_t position = p.positions[t];
+    if (p.axis_of_pair) {  // (all axes' positions are loaded along with the pair's axis)
+      const int axis = p.axis_of_pair[threadIdx.x];
+#pragma unroll
+      for (int i = 1; i < BGG_MAX_AXES; ++i) {
+        const int32_t other = p.positions[min(i, p.last_axis) * p.axis_stride + t];
+        position = axis >= i ? other : position;
+      }
+    }
+    angle_of(position, p.freqs[threadIdx.x], &c, &s);
     cs[threadIdx.x] = c * p.magnitude;
     sn[threadIdx.x] = s * p.magnitude;
   }
