@@ -126,13 +126,15 @@ __device__ __forceinline__ void read_batch(const AttnParams& p, const Batch& s) 
 struct Cut {
   int tiles, rows;
   int wave_bits;  // 2^wave_bits waves of a workgroup on different rows, the others on other tokens
-  int blocks, chunks, each;  // each: tiles of a chunk
+  int blocks, chunks;
 };
 // Row waves share the tiles that LDS holds, so there are as many as fit the
-// rows without much of the last workgroup's empty.  `size`: tiles times row
-// waves of an item.
+// rows with at most a fifth of them empty (396 rows, bf16 heads of 128: eight
+// waves in two workgroups, 19 % empty, against two in seven: 256 sequences
+// 45.9 and 50.8 us; 384 rows: four in three against eight in two, a quarter
+// empty: 79.6 and 90 us).
 template <class S>
-__device__ __forceinline__ Cut cut_of(const AttnParams& p, const Batch& s, int g, int size) {
+__device__ __forceinline__ Cut cut_of(const AttnParams& p, const Batch& s, int g) {
   Cut c;
   c.tiles = tiles_of(s.lo[g], s.hi[g]);
   c.rows = (s.start[g + 1] - s.start[g]) * p.group;
@@ -141,12 +143,18 @@ __device__ __forceinline__ Cut cut_of(const AttnParams& p, const Batch& s, int g
 #pragma unroll
   for (int i = 0; i < S::WaveBits; ++i) {
     const int w = 1 << c.wave_bits, padded = (units + w - 1) >> c.wave_bits << c.wave_bits;
-    if (c.wave_bits > 1 && padded * 5 > units * 6) --c.wave_bits;
+    if (c.wave_bits > 1 && padded * 4 > units * 5) --c.wave_bits;
   }
   c.blocks = (units + (1 << c.wave_bits) - 1) >> c.wave_bits;
-  c.each = (((size + (1 << c.wave_bits) - 1) >> c.wave_bits) + S::Subs - 1) / S::Subs * S::Subs;
-  c.chunks = (c.tiles + c.each - 1) / c.each;
   return c;
+}
+// Chunks, and the tiles of each, at a size of items in tiles times row waves:
+// a tile or more for every stream of tokens.
+template <class S>
+__device__ __forceinline__ void cut_tiles(Cut& c, int size) {
+  const int streams = S::WaveBits - c.wave_bits;
+  const int each = (((size - 1) >> S::WaveBits) + 1) << streams;
+  c.chunks = (int)((uint32_t)(c.tiles + each - 1) / (uint32_t)each);
 }
 
 struct PrefixItem {
@@ -164,9 +172,10 @@ __device__ __forceinline__ bool find_prefix(const AttnParams& p, const Batch& s,
   const int lane = threadIdx.x & 63, G = p.groups;
   const int per = (G + 63) / 64, g0 = min(G, lane * per), g1 = min(G, g0 + per);
   float work = 0.0f;
+  Cut one{0, 0, 0, 0, 0};  // the lane's only group's, if there are not more
 #pragma unroll 1
   for (int g = g0; g < g1; ++g) {
-    const Cut c = cut_of<S>(p, s, g, 1);
+    const Cut c = one = cut_of<S>(p, s, g);
     work += (float)c.tiles * (float)(c.blocks << c.wave_bits);
   }
   const float even = fminf(ceilf(wave_add(work) * (float)p.kv_heads / (float)p.prefix_target * 1.0001f), 1e8f);
@@ -178,7 +187,9 @@ __device__ __forceinline__ bool find_prefix(const AttnParams& p, const Batch& s,
     int least = 0;
 #pragma unroll 1
     for (int g = g0; g < g1; ++g) {
-      const Cut c = cut_of<S>(p, s, g, size);
+      Cut c = one;
+      if (per > 1) c = cut_of<S>(p, s, g);
+      cut_tiles<S>(c, size);
       mine += c.chunks * c.blocks;
       least += c.chunks ? c.blocks : 0;
       rows += c.chunks * p.kv_heads * c.rows;
@@ -195,7 +206,8 @@ __device__ __forceinline__ bool find_prefix(const AttnParams& p, const Batch& s,
       int r = row;
 #pragma unroll 1
       for (int g = g0; g < g1; ++g) {
-        const Cut c = cut_of<S>(p, s, g, size);
+        Cut c = cut_of<S>(p, s, g);
+        cut_tiles<S>(c, size);
         base[g] = r;
         r += c.chunks * p.kv_heads * c.rows;
       }
@@ -212,7 +224,8 @@ __device__ __forceinline__ bool find_prefix(const AttnParams& p, const Batch& s,
   Cut c;
 #pragma unroll 1
   for (;; ++g) {
-    c = cut_of<S>(p, s, g, size);
+    c = cut_of<S>(p, s, g);
+    cut_tiles<S>(c, size);
     if (at < first + c.chunks * c.blocks) break;
     first += c.chunks * c.blocks;
     row += c.chunks * p.kv_heads * c.rows;
@@ -225,7 +238,8 @@ __device__ __forceinline__ bool find_prefix(const AttnParams& p, const Batch& s,
   it.block = __builtin_amdgcn_readfirstlane(local % c.blocks);
   it.chunk = __builtin_amdgcn_readfirstlane(local / c.blocks);
   const int t0 = s.lo[g] / kTokens;
-  const int each = ((c.tiles + c.chunks - 1) / c.chunks + S::Subs - 1) / S::Subs * S::Subs;
+  const int streams = S::WaveBits - c.wave_bits;
+  const int each = ((int)((uint32_t)(c.tiles + c.chunks - 1) / (uint32_t)c.chunks) + (1 << streams) - 1) >> streams << streams;
   it.tile = __builtin_amdgcn_readfirstlane(t0 + min(c.tiles, it.chunk * each));
   it.tile_end = __builtin_amdgcn_readfirstlane(t0 + min(c.tiles, (it.chunk + 1) * each));
   return true;
@@ -257,7 +271,8 @@ __device__ __forceinline__ void plan_own(const AttnParams& p, const Batch& s, co
     SharedSeq q{0, 0, 0, 0};
     const int g = s.group_of(G, b);
     if (s.start[g] <= b && b < s.start[g + 1]) {
-      const Cut c = cut_of<S>(p, s, g, size_of_prefix);
+      Cut c = cut_of<S>(p, s, g);
+      cut_tiles<S>(c, size_of_prefix);
       q.tokens = s.prefix(p, g);
       q.chunks = c.chunks;
       q.rows = c.rows;
@@ -465,10 +480,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
       if (lane == 0) has_page[step & 1][half] = page >= 0;
     }
   };
-  if (fetches) {
-    if (steps > 0) fetch(0);
-    if (steps > 1) fetch(1);
-  }
+  if (fetches && steps > 0) fetch(0);
 
   // the queries, while those are on their way
   // (the factor is kept positive, for the maxima: a negative one turns the
@@ -592,6 +604,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   // free for the step after the next, and that step's loads have a step's
   // time to land.
   if (steps > 0) landed_barrier<0>();
+  if (fetches && steps > 1) fetch(1);
   auto pages_of = [&](int step) __attribute__((always_inline)) {
     uint64_t v = 0;
     __builtin_memcpy(&v, has_page[step & 1], 2 * Subs);
