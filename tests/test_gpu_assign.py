@@ -150,6 +150,36 @@ def test_rows_around_the_own_launch(ps, W, T):
     run_case(T + ps, 37, ps, W, T, "mixed")
 
 
+@pytest.mark.parametrize("B", [37, 256])
+@pytest.mark.parametrize("T", [1023, 1024, 1025, 2047, 2049])
+def test_rows_around_the_own_launch_of_small_batches(B, T):
+    run_case(T + B, B, 16, 60, T, "mixed")
+
+
+@pytest.mark.parametrize("B", [257, 1023, 1024, 1025, 4096])
+@pytest.mark.parametrize("T", [4096, 4097, 9001])
+def test_rows_of_large_batches(B, T):
+    run_case(T + B, B, 16, 8, T, "mixed", extra_stride=1)
+
+
+@pytest.mark.parametrize("B", [5, 600, 3000])
+def test_one_long_sequence_among_unused_ones(B):
+    """Its rows are those of many workgroups, none of which hold its first."""
+    ps, W, T, at, n, c = 32, 700, 20000, B // 2, 45, 19990
+    counts = [c if b == at else 0 for b in range(B)]
+    lengths = [n if b == at else 0 for b in range(B)]
+    pages = W + 3
+    table, stack = [[-1] * W for _ in range(B)], list(range(pages - 2))
+    table[at][:2] = [pages - 1, pages - 2]
+    dt, dstack, buf = i32(table), i32(stack), Buffers(B, T)
+    cache = bgg.bgg_cache_describe("f16", pages, ps, 1, 64)
+    bgg.bgg_cache_assign(cache, i32(lengths), i32(counts), dt, dstack, i32([len(stack)]), buf.lengths_out, buf.free_count_out,
+                         buf.past, buf.starts, buf.positions, buf.slots)
+    torch.cuda.synchronize()
+    buf.check(step(ps, W, T, pages, len(stack), lengths, counts, table, stack, len(stack)))
+    assert dt.tolist() == table and dstack.tolist() == stack
+
+
 @pytest.mark.parametrize("T", [600, 20000])
 @pytest.mark.parametrize("B", [9, 300])
 @pytest.mark.parametrize("short", [1, 2, 5, 100])
@@ -180,9 +210,10 @@ def test_no_sequences_and_no_rows(T):
     run_case(2, 6, 16, 4, 0, "mixed")
 
 
-def test_largest_counts():
+@pytest.mark.parametrize("T", [10, 6000])
+def test_largest_counts(T):
     # counts whose sum passes 32 bits are not served; the sequences among them that fit the rows are
-    ps, W, T = 16, 1 << 20, 10
+    ps, W = 16, 1 << 20
     counts = [2, 2**31 - 1, 2**31 - 1, 3, 2**31 - 1, 0, MIN]
     lengths = [0, 5, W * ps, 0, 2**31 - 1, 17, 2**31 - 1]
     table = torch.full((7, W), -1, dtype=torch.int32, device=DEV)
@@ -193,7 +224,7 @@ def test_largest_counts():
                          buf.past, buf.starts, buf.positions, buf.slots)
     torch.cuda.synchronize()
     buf.check(dict(lengths_out=[2, 5, W * ps, 0, W * ps, 17, 0], free_count_out=[3], past=[0, 5, W * ps, 0, W * ps, 17, 0],
-                   starts=[0, 2, T, T, T, T, T, T], positions=[0, 1] + [0] * 8, slots=[0, 1] + [-1] * 8))
+                   starts=[0, 2, T, T, T, T, T, T], positions=[0, 1] + [0] * (T - 2), slots=[0, 1] + [-1] * (T - 2)))
 
 
 def test_a_step_given_back_leaves_the_stack_as_it_was():

@@ -418,6 +418,39 @@ def test_one_workspace_for_both_attentions_and_two_streams():
         d.check()
 
 
+def test_two_captured_calls_of_one_workspace():
+    """Replayed in turn, of different shapes, with eager calls in between."""
+    cs = [case([(40, [1, 900, 30]), (3, [700])], hq=12, hk=2, page=64, seed=1), case([(2, [5, 6])], hq=4, hk=2, D=64, seed=2)]
+    ws = bgg.workspace(max(Device(c).ws.numel() for c in cs))
+    ds, graphs, side = [Device(c, ws) for c in cs], [], torch.cuda.Stream()
+    for d in ds:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            d.step()
+        graphs.append(graph)
+    for i in (0, 1, 1, 0, 0, 1):
+        for d in ds:
+            d.out.fill_(NAN)
+        ds[1 - i].step()
+        graphs[i].replay()
+        for d in ds:
+            d.check()
+    assert not ws[:16384].any()
+
+
+@pytest.mark.parametrize("dtype,kv,D,hq,hk", [("f16", "f16", 128, 8, 2), ("bf16", "bf16", 256, 4, 4), ("f16", "e4m3", 64, 32, 1),
+                                              ("bf16", "e4m3", 96, 20, 2)])
+def test_large_batches_with_own_tokens_of_every_length(dtype, kv, D, hq, hk):
+    """So many sequences and head blocks that one wave takes an item, among
+    them sequences long enough to be cut."""
+    B = -(-1024 // (hk * -(-hq // hk // 16))) + 1
+    own = [(7 * b) % 45 for b in range(B)]
+    own[3], own[B // 2], own[B - 1] = 2900, 9000, None
+    c = case([(4, own[:B // 3]), (9, own[B // 3:])], hq=hq, hk=hk, D=D, dtype=dtype, kv=kv, page=32, seed=D)
+    run_check(c, [(b, h) for b in (0, 3, 4, B // 3 - 1, B // 3, B // 2, B - 2, B - 1) for h in range(hq)])
+
+
 def test_same_call_same_bits():
     c = case([(130, [1, 70, 40, 900]), (3, [4])], hq=12, hk=2, page=64, dtype="bf16", kv="bf16")
     d = Device(c)
