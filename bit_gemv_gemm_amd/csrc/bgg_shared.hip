@@ -30,6 +30,32 @@ namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// 32x32x16 matrix operations: the same values a cycle as 16x16x32 in half the
+// instructions (products and exponentials of a tile alone, two waves on a
+// SIMD: 1447 cycles against 1551).
+__device__ __forceinline__ f32x16 mul32(f16x8 a, f16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mul32(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 zeros() {
+  f32x16 v;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+  return v;
+}
+// Over the two lanes of a row.
+__device__ __forceinline__ float row_max(float v) {
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
 
 constexpr int kGroupsMax = (int)kMaxBatch;
 
@@ -41,8 +67,19 @@ struct PrefixShape {
   // Eight waves, two on a SIMD, so that one's matrix operations run beside
   // the other's exponentials; wide heads do not fit their registers.
   static constexpr int Waves = D <= 128 ? 8 : 4, WaveBits = D <= 128 ? 3 : 2;
-  static constexpr int Blocks = 2;  // blocks of 16 rows of a wave (queries, accumulators)
-  static constexpr int Rows = 16 * Blocks;
+  static constexpr int Rows = 32;  // of a wave (queries, accumulators)
+  static constexpr int Steps = D / 16, PL = D / 32;  // matrix operations of the scores, of 16 tokens' values
+  // The operands of a tile (in lane l: r = l % 32, h = l / 32):
+  //   S^T = K Q^T: rows are the tile's 32 tokens, columns 32 query rows, and
+  //     lane (r, h) gives values q_dim .. + 7 of token r and of row r.  It
+  //     gets the scores of row r at tokens 8 (i / 4) + 4 h + i % 4, i < 16.
+  //   O^T = V^T P^T: rows are 32 of the head's values, columns the rows; the
+  //     order of the tokens is free, so operation j of the two takes those of
+  //     the scores 8 j .. 8 j + 7, and lane (r, h) gets values 8 (i / 4) +
+  //     4 h + i % 4 of row r.
+  static __device__ __forceinline__ int q_dim(int s, int h) {
+    return TL::ES == 2 ? 16 * s + 8 * h : 32 * (s / 2) + 16 * h + 8 * (s % 2);
+  }
   static constexpr int RowF = D + 4;  // floats of a row of the parts: values, maximum, sum
   // tiles of a step; the keys and values of two steps take up to 128 KB of LDS
   static constexpr int Subs = Waves / 2;
@@ -54,16 +91,16 @@ struct PrefixShape {
   static constexpr int TileBytes = kTokens * Row;
   static constexpr int Pieces = Row / 16;                // 16-byte pieces of a row
   static constexpr int Loads = (16 * Pieces + 63) / 64;  // of the keys (and the values) of half a tile
-  // In LDS, piece q of row r lies at piece q ^ mix(r) of the row, so that the
-  // rows that are read together lie in different banks (256 bytes hold all
-  // banks once).  Keys: piece q of 16 rows, 8 of them at a time.  Values:
-  // 32 bytes of 16 rows (8-bit: 16 bytes of 32).
+  // In LDS, piece q of row r lies at piece q ^ mix(r) of the row, so that what
+  // is read together lies in different banks (256 bytes hold all banks once):
+  // of the keys, piece q of 16 rows; of the values, 64 bytes of rows 4 n .. 4 n
+  // + 3, or 32 bytes (8-bit) of those and of the rows 8 behind them.
   static __device__ __forceinline__ int mix_k(int r) {
-    return Pieces % 8 == 0 ? r & 7 : Pieces % 4 == 0 ? (r >> 1) & 3 : (r >> 2) & 1;
+    return Pieces % 16 == 0 ? r & 15 : Pieces % 8 == 0 ? (r >> 1) & 7 : Pieces % 4 == 0 ? (r >> 2) & 3 : (r >> 3) & 1;
   }
   static __device__ __forceinline__ int mix_v(int r) {
-    if (TL::ES == 2) return Pieces % 16 == 0 ? 2 * (r & 7) : Pieces % 8 == 0 ? 2 * ((r >> 1) & 3) : 2 * ((r >> 2) & 1);
-    return Pieces % 16 == 0 ? r & 15 : Pieces % 8 == 0 ? (r >> 1) & 7 : Pieces % 4 == 0 ? (r >> 2) & 3 : (r >> 3) & 1;
+    if (TL::ES == 2) return Pieces % 16 == 0 ? 4 * (r & 3) : Pieces % 8 == 0 ? 4 * ((r >> 1) & 1) : 0;
+    return 2 * (Pieces % 16 == 0 ? (r & 3) | ((r >> 1) & 4) : Pieces % 8 == 0 ? ((r >> 1) & 1) | ((r >> 2) & 2) : Pieces % 4 == 0 ? (r >> 3) & 1 : 0);
   }
 };
 
@@ -391,7 +428,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   using TL = Tile<T, C, D>;
   using V = typename TL::V;
   using S = PrefixShape<T, C, D>;
-  constexpr int PL = TL::PL, NB = S::Blocks, RowF = S::RowF, Row = S::Row, Subs = S::Subs, Waves = S::Waves;
+  constexpr int PL = S::PL, Steps = S::Steps, RowF = S::RowF, Row = S::Row, Subs = S::Subs, Waves = S::Waves;
   constexpr int kThreads = 64 * Waves;
   constexpr int kKeys = Subs * S::TileBytes, kBuf = 2 * kKeys;  // a step's keys, then its values
   // two buffers; before and after the loop other uses
@@ -414,7 +451,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
     return;
   }
   if (!find_prefix<S>(p, batch, blockIdx.x - 1, it, nullptr, nullptr)) return;
-  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, r = lane & 31, half_of = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kh = it.kh;
   const int s0 = batch.start[it.group], members = batch.start[it.group + 1] - s0, rows = members * p.group;
@@ -441,27 +478,17 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   };
   if (fetches) load_pages(0);
 
-  // the lane's row of each block: the tokens it sees
-  int lo[NB], hi[NB], member[NB], head[NB];
-  bool none[NB];
-  int lo_max = 0, hi_min = 0x7FFFFFFF;
+  // the lane's row: the tokens it sees (a row past the last reads its queries)
+  const int member = min((row0 + r) / p.group, members - 1), head = row0 + r < rows ? row0 + r - member * p.group : 0;
+  const int lo = batch.first_seen(p, s0 + member), hi = min(batch.n[s0 + member], prefix);
+  // a row that sees nothing of the item's tokens (an unused sequence, a
+  // window) does not keep the others from the fast path: it is emptied at the
+  // end instead
+  const bool none = row0 + r >= rows || max(lo, it.tile * kTokens) >= min(hi, it.tile_end * kTokens);
+  int lo_max = none ? 0 : lo, hi_min = none ? 0x7FFFFFFF : hi;
+  // over the rows (the same in both lanes of a row)
 #pragma unroll
-  for (int c = 0; c < NB; ++c) {  // (rows past the last read its queries)
-    const int row = row0 + 16 * c + r;
-    member[c] = min(row / p.group, members - 1);
-    head[c] = row < rows ? row - member[c] * p.group : 0;
-    lo[c] = batch.first_seen(p, s0 + member[c]);
-    hi[c] = min(batch.n[s0 + member[c]], prefix);
-    // a row that sees nothing of the item's tokens (an unused sequence, a
-    // window) does not keep the others from the fast path: it is emptied at
-    // the end instead
-    none[c] = row >= rows || max(lo[c], it.tile * kTokens) >= min(hi[c], it.tile_end * kTokens);
-    lo_max = max(lo_max, none[c] ? 0 : lo[c]);
-    hi_min = min(hi_min, none[c] ? 0x7FFFFFFF : hi[c]);
-  }
-  // over the rows (the same in each of the four lanes of a row)
-#pragma unroll
-  for (int s = 1; s < 16; s <<= 1) {
+  for (int s = 1; s < 32; s <<= 1) {
     lo_max = max(lo_max, __shfl_xor(lo_max, s));
     hi_min = min(hi_min, __shfl_xor(hi_min, s));
   }
@@ -505,40 +532,32 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   float factor = p.scale * (p.k_scale ? p.k_scale[kh] : 1.0f) * kLog2e;
   const bool turn = factor < 0.0f, zero = factor == 0.0f;
   factor = zero ? 1.0f : fabsf(factor);
-  typename Mma<T>::op q[NB][TL::Steps];
+  typename Mma<T>::op q[Steps];
+  {
+    const uint8_t* from = reinterpret_cast<const uint8_t*>(p.q + (s0 + member) * p.q_stride + (int64_t)(kh * p.group + head) * D);
 #pragma unroll
-  for (int c = 0; c < NB; ++c) {
-    const uint8_t* from = reinterpret_cast<const uint8_t*>(p.q + (s0 + member[c]) * p.q_stride +
-                                                           (int64_t)(kh * p.group + head[c]) * D);
-#pragma unroll
-    for (int s = 0; s < TL::Steps; ++s) {
+    for (int s = 0; s < Steps; ++s) {
       uint32_t w[4];
-      load_bytes<16>(from + 2 * TL::q_dim(s, g), w);
-      __builtin_memcpy(&q[c][s], w, 16);
+      load_bytes<16>(from + 2 * S::q_dim(s, half_of), w);
+      __builtin_memcpy(&q[s], w, 16);
     }
   }
 
   if (turn || zero) {
 #pragma unroll
-    for (int c = 0; c < NB; ++c)
+    for (int s = 0; s < Steps; ++s) {
+      uint32_t w[4];
+      __builtin_memcpy(w, &q[s], 16);
 #pragma unroll
-      for (int s = 0; s < TL::Steps; ++s) {
-        uint32_t w[4];
-        __builtin_memcpy(w, &q[c][s], 16);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = zero ? not_finite_halves<T>(w[i]) : w[i] ^ 0x80008000u;
-        __builtin_memcpy(&q[c][s], w, 16);
-      }
+      for (int i = 0; i < 4; ++i) w[i] = zero ? not_finite_halves<T>(w[i]) : w[i] ^ 0x80008000u;
+      __builtin_memcpy(&q[s], w, 16);
+    }
   }
-  f32x4 acc[NB][PL];
-  // maximum and sum of a row; over: what the exponent of a score gets added
-  float m[NB], l[NB], over[NB];
+  f32x16 acc[PL];
 #pragma unroll
-  for (int c = 0; c < NB; ++c) {
-    m[c] = -FLT_MAX, l[c] = 0.0f, over[c] = FLT_MAX;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) acc[c][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
+  for (int i = 0; i < PL; ++i) acc[i] = zeros();
+  // maximum and sum of the row; over: what the exponent of a score gets added
+  float m = -FLT_MAX, l = 0.0f, over = FLT_MAX;
   bool infinite = false;  // a value that is not finite was taken out
 
   // (the accumulators stay where the matrix operations have them: without
@@ -547,71 +566,78 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   auto in_place = [&]() __attribute__((always_inline)) {
     if (S::Waves > 4) return;
 #pragma unroll
-    for (int c = 0; c < NB; ++c)
+    for (int i = 0; i < PL; ++i) asm("" : "+a"(acc[i]));
 #pragma unroll
-      for (int i = 0; i < PL; ++i) asm("" : "+a"(acc[c][i]));
-#pragma unroll
-    for (int c = 0; c < NB; ++c)
-#pragma unroll
-      for (int i = 0; i < TL::Steps; ++i) asm("" : "+a"(q[c][i]));
+    for (int i = 0; i < Steps; ++i) asm("" : "+a"(q[i]));
   };
   // --- a tile's operands, from LDS
-  TL tl;  // (its keys)
-  typename Mma<V>::op v[PL];
-  uint32_t bytes[TL::ES == 1 ? PL : 1][2];  // 8-bit values as they are read
+  uint32_t k[D * TL::ES / 8];  // its keys
+  typename Mma<V>::op v[2][PL];
+  uint32_t bytes[TL::ES == 1 ? 2 : 1][TL::ES == 1 ? PL : 1][2];  // 8-bit values as they are read
   auto load_keys = [&](int step, int sub) __attribute__((always_inline)) {
-    const uint8_t* keys = lds + (step & 1) * kBuf + sub * S::TileBytes;
+    const uint8_t* row = lds + (step & 1) * kBuf + sub * S::TileBytes + r * Row;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint8_t* row = keys + (16 * j + r) * Row;
-      if constexpr (TL::ES == 2) {
-#pragma unroll
-        for (int st = 0; st < TL::Steps; ++st) load_bytes<16>(row + 16 * ((4 * st + g) ^ S::mix_k(r)), &tl.k[j][4 * st]);
-      } else {
-#pragma unroll
-        for (int u = 0; u < D / 64; ++u) load_bytes<16>(row + 16 * ((4 * u + g) ^ S::mix_k(r)), &tl.k[j][4 * u]);
-        if constexpr (D % 64)
-          load_bytes<8>(row + 16 * ((4 * (D / 64) + (g >> 1)) ^ S::mix_k(r)) + 8 * (g & 1), &tl.k[j][4 * (D / 64)]);
-      }
-    }
+    for (int i = 0; i < S::Pieces / 2; ++i) load_bytes<16>(row + 16 * ((2 * i + half_of) ^ S::mix_k(r)), &k[4 * i]);
   };
-  // operand i of the values is 16 dimensions of the tile's tokens: a read that
-  // transposes gives lane (r, g) dimension 16 i + r of the four tokens (8-bit:
-  // eight) whose rows its 16 lanes name
+  auto key_op = [&](int s) __attribute__((always_inline)) {
+    uint32_t w[4];
+    if constexpr (TL::ES == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = k[4 * s + i];
+    } else {
+      Mma<T>::widen(k[2 * s], w);
+      Mma<T>::widen(k[2 * s + 1], w + 2);
+    }
+    typename Mma<T>::op x;
+    __builtin_memcpy(&x, w, 16);
+    return x;
+  };
+  // operand (j, i) of the values is 32 dimensions of 16 of the tile's tokens:
+  // a read that transposes gives lane l of 16 dimension l of the four tokens
+  // (8-bit: eight) whose rows the 16 lanes name.  (Tokens 8 and 16 apart are
+  // mixed alike.)
+  const int side = lane >> 4 & 1, l16 = lane & 15;  // which 16 of the dimensions
   auto load_values = [&](int step, int sub) __attribute__((always_inline)) {
     const uint8_t* values = lds + (step & 1) * kBuf + kKeys + sub * S::TileBytes;
     if constexpr (TL::ES == 2) {
-      const int t = 4 * g + (r >> 2);
-      const uint8_t* row = values + t * Row + 8 * (r & 1);
+      const int t = 4 * half_of + (l16 >> 2);
+      const uint8_t* row = values + t * Row + 8 * (l16 & 1);
 #pragma unroll
       for (int i = 0; i < PL; ++i) {
-        const int at = 16 * ((2 * i + (r >> 1 & 1)) ^ S::mix_v(t));
-        static_assert(TL::ES == 1 || S::Pieces % 4 == 0, "tokens t and t + 16 are mixed alike");
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(row + at));
-        const s16x4 hi =
-            __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(row + at + 16 * Row));
-        __builtin_memcpy(&v[i], &lo, 8);
-        __builtin_memcpy((uint8_t*)&v[i] + 8, &hi, 8);
+        const int at = 16 * ((4 * i + 2 * side + (l16 >> 1 & 1)) ^ S::mix_v(t));
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const s16x4 four =
+                __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(row + at + (16 * j + 8 * x) * Row));
+            __builtin_memcpy((uint8_t*)&v[j][i] + 8 * x, &four, 8);
+          }
       }
     } else {
-      const int t = 16 * (r >> 3) + 4 * g + (r >> 1 & 3);
-      const uint8_t* row = values + t * Row + 8 * (r & 1);
+      const int t = 8 * (l16 >> 3) + 4 * half_of + (l16 >> 1 & 3);
+      const uint8_t* row = values + t * Row + 8 * (l16 & 1);
 #pragma unroll
-      for (int i = 0; i < PL; ++i) {
-        const i32x2 b = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)(row + 16 * (i ^ S::mix_v(t))));
-        bytes[i][0] = b.x, bytes[i][1] = b.y;
-      }
+      for (int i = 0; i < PL; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const i32x2 b = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+              (__attribute__((address_space(3))) i32x2*)(row + 16 * ((2 * i + side) ^ S::mix_v(t)) + 16 * j * Row));
+          bytes[j][i][0] = b.x, bytes[j][i][1] = b.y;
+        }
     }
   };
   auto widen_values = [&]() __attribute__((always_inline)) {
     if constexpr (TL::ES == 1) {
 #pragma unroll
-      for (int i = 0; i < PL; ++i) {
-        uint32_t w[4];
-        Mma<V>::widen(bytes[i][0], w);
-        Mma<V>::widen(bytes[i][1], w + 2);
-        __builtin_memcpy(&v[i], w, 16);
-      }
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+          uint32_t w[4];
+          Mma<V>::widen(bytes[j][i][0], w);
+          Mma<V>::widen(bytes[j][i][1], w + 2);
+          __builtin_memcpy(&v[j][i], w, 16);
+        }
     }
   };
 
@@ -637,18 +663,9 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
       const int tile = it.tile + step * Subs + sub, t0 = tile * kTokens;
       load_values(step, sub);
       in_place();
-      f32x4 s[NB][2];
+      f32x16 s = zeros();
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-#pragma unroll
-        for (int c = 0; c < NB; ++c) s[c][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int st = 0; st < TL::Steps; ++st) {
-          const typename Mma<T>::op k = tl.k_op(j, st);
-#pragma unroll
-          for (int c = 0; c < NB; ++c) s[c][j] = Mma<T>::mul(k, q[c][st], s[c][j]);
-        }
-      }
+      for (int st = 0; st < Steps; ++st) s = mul32(key_op(st), q[st], s);
       widen_values();
       const uint32_t have = (uint32_t)(pages >> (16 * sub) & 1) | (uint32_t)(pages >> (16 * sub + 7) & 2);
       if (!(t0 >= lo_max && t0 + kTokens <= hi_min && have == 3)) {
@@ -658,52 +675,47 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
         // probability of 0 (the rows that see them get them at the end)
         uint32_t is = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int t = t0 + 16 * (e >> 2) + 4 * g + (e & 3);
-          if ((have >> (e >> 2) & 1) && t >= lo_all && t < hi_all) is |= 1u << e;
-#pragma unroll
-          for (int c = 0; c < NB; ++c)
-            s[c][e >> 2][e & 3] = (is >> e & 1) && t >= lo[c] && t < hi[c] ? s[c][e >> 2][e & 3] : -INFINITY;
+        for (int e = 0; e < 16; ++e) {
+          const int t = t0 + 8 * (e >> 2) + 4 * half_of + (e & 3);
+          if ((have >> (e >> 3) & 1) && t >= lo_all && t < hi_all) is |= 1u << e;
+          s[e] = (is >> e & 1) && t >= lo && t < hi ? s[e] : -INFINITY;
         }
 #pragma unroll
-        for (int i = 0; i < PL; ++i) {
-          uint32_t w[4];
-          __builtin_memcpy(w, &v[i], 16);
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)  // (tokens 2 k and 2 k + 1)
-            w[k] = finite_halves<V>(w[k] & ((is >> (2 * k) & 1 ? 0xFFFFu : 0u) | (is >> (2 * k + 1) & 1 ? 0xFFFF0000u : 0u)), infinite);
-          __builtin_memcpy(&v[i], w, 16);
-        }
+          for (int i = 0; i < PL; ++i) {
+            uint32_t w[4];
+            __builtin_memcpy(w, &v[j][i], 16);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {  // (tokens of scores 8 j + 2 n and the next)
+              const uint32_t bits = is >> (8 * j + 2 * n);
+              w[n] = finite_halves<V>(w[n] & ((bits & 1 ? 0xFFFFu : 0u) | (bits & 2 ? 0xFFFF0000u : 0u)), infinite);
+            }
+            __builtin_memcpy(&v[j][i], w, 16);
+          }
       }
       // exponents of the probabilities (2^lift times them).  The maxima are
       // taken of these, whose products the compiler need not quieten first.
-      float x[NB][8];
+      float x[16];
       auto exponents = [&]() __attribute__((always_inline)) {
 #pragma unroll
-        for (int c = 0; c < NB; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[c][i] = fmaf(s[c][i >> 2][i & 3], factor, over[c]);
+        for (int i = 0; i < 16; ++i) x[i] = fmaf(s[i], factor, over);
       };
       exponents();
-      float top = x[0][0];
+      float top = x[0];
 #pragma unroll
-      for (int c = 0; c < NB; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, x[c][i]);
+      for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
       if (__any(top > kSlack + Mma<V>::lift)) {
+        float most = s[0];
 #pragma unroll
-        for (int c = 0; c < NB; ++c) {
-          float most = s[c][0][0];
+        for (int i = 1; i < 16; ++i) most = fmaxf(most, s[i]);
+        const float mn = fmaxf(m, row_max(most) * factor);
+        const float f = __builtin_amdgcn_exp2f(m - mn);
+        l *= f;
 #pragma unroll
-          for (int i = 1; i < 8; ++i) most = fmaxf(most, s[c][i >> 2][i & 3]);
-          const float mn = fmaxf(m[c], column_max(most) * factor);
-          const float f = __builtin_amdgcn_exp2f(m[c] - mn);
-          l[c] *= f;
-#pragma unroll
-          for (int i = 0; i < PL; ++i) acc[c][i] *= f;
-          m[c] = mn;
-          over[c] = Mma<V>::lift - mn;
-        }
+        for (int i = 0; i < PL; ++i) acc[i] *= f;
+        m = mn;
+        over = Mma<V>::lift - mn;
         exponents();
       }
       // the next tile (after the last one, this one again)
@@ -724,16 +736,16 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
       in_place();
       load_keys(next_step, next_sub);
 #pragma unroll
-      for (int c = 0; c < NB; ++c) {
+      for (int j = 0; j < 2; ++j) {
         float e[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          e[i] = __builtin_amdgcn_exp2f(x[c][i]);
-          l[c] += e[i];
+          e[i] = __builtin_amdgcn_exp2f(x[8 * j + i]);
+          l += e[i];
         }
         const typename Mma<V>::op pr = Mma<V>::round(e);
 #pragma unroll
-        for (int i = 0; i < PL; ++i) acc[c][i] = Mma<V>::mul(v[i], pr, acc[c][i]);
+        for (int i = 0; i < PL; ++i) acc[i] = mul32(v[j][i], pr, acc[i]);
       }
       if (done) break;
       step = next_step, sub = next_sub;
@@ -744,25 +756,25 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   // its sums to the largest maximum, then they are added up
   float(*const red)[RowF] = reinterpret_cast<float(*)[RowF]>(lds);  // [Waves * Rows]
   infinite = __syncthreads_or(infinite);  // (also: the tiles are read)
-#pragma unroll
-  for (int c = 0; c < NB; ++c) {
-    l[c] = none[c] ? 0.0f : column_sum(l[c]);
-    m[c] = none[c] ? -FLT_MAX : m[c];
-    if (g == 0) red_m[wave * S::Rows + 16 * c + r] = m[c];
-  }
+  l = none ? 0.0f : row_sum(l);
+  m = none ? -FLT_MAX : m;
+  if (half_of == 0) red_m[wave * S::Rows + r] = m;
   __syncthreads();
+  {
+    float mw = m;
+    for (int w = wave & (row_waves - 1); w < Waves; w += row_waves) mw = fmaxf(mw, red_m[w * S::Rows + r]);
+    const float f = none ? 0.0f : __builtin_amdgcn_exp2f(m - mw);
+    float* const row = red[wave * S::Rows + r];
 #pragma unroll
-  for (int c = 0; c < NB; ++c) {
-    float mw = m[c];
-    for (int w = wave & (row_waves - 1); w < Waves; w += row_waves) mw = fmaxf(mw, red_m[w * S::Rows + 16 * c + r]);
-    const float f = none[c] ? 0.0f : __builtin_amdgcn_exp2f(m[c] - mw);
-    float* const row = red[wave * S::Rows + 16 * c + r];
+    for (int i = 0; i < PL; ++i)
 #pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      const f32x4 o = acc[c][i] * f;
-      *reinterpret_cast<f32x4*>(row + 16 * i + 4 * g) = none[c] ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : o;
-    }
-    if (g == 0) row[D] = mw, row[D + 1] = none[c] ? 0.0f : l[c] * f;
+      for (int n = 0; n < 4; ++n) {
+        f32x4 o;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = none ? 0.0f : acc[i][4 * n + k] * f;
+        *reinterpret_cast<f32x4*>(row + 32 * i + 8 * n + 4 * half_of) = o;
+      }
+    if (half_of == 0) row[D] = mw, row[D + 1] = none ? 0.0f : l * f;
   }
   __syncthreads();
   const int first_row = it.block * row_waves * S::Rows;
