@@ -9,14 +9,14 @@
 //
 // A workgroup takes up to 256 rows of a key head (128 of wide heads) and a
 // chunk of the prefix; keys and values go from the cache to LDS once for all
-// its waves.  64 sequences of 48/8 heads of 128 behind 32768 tokens of f16: 80
-// us, of which 7.5 pass until the first tiles are there and 4 with the parts
-// at the end (first with every wave loading its own operands 103); 256
-// sequences in two groups behind 5328 and 4112 tokens of bf16 (32/8): 45.6 us
+// its waves.  64 sequences of 48/8 heads of 128 behind 32768 tokens of f16:
+// 76.5 us, of which 7.5 pass until the first tiles are there and 4 with the
+// parts at the end (with every wave loading its own operands 103); 256
+// sequences in two groups behind 5328 and 4112 tokens of bf16 (32/8): 44.4 us
 // (122 then).  The matrix units are busy a third of the time and the vector
-// units a half, LDS 40 %: the waves of a SIMD overlap them in part only, and
-// stand in the queue of the loads to LDS (about 27 cycles per KB) and at the
-// barriers of a step.
+// units 44 %: a tile of two waves on a SIMD takes 1600 to 2200 cycles, where
+// its products and exponentials alone take 1450, and the clock falls to 1.8
+// GHz under them.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -34,7 +34,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // 32x32x16 matrix operations: the same values a cycle as 16x16x32 in half the
 // instructions (products and exponentials of a tile alone, two waves on a
-// SIMD: 1447 cycles against 1551).
+// SIMD: 1447 cycles against 1551; the kernel's cases 2 to 5 % faster but for
+// one of many partly hidden tiles, 27.0 against 28.1 us).
 __device__ __forceinline__ f32x16 mul32(f16x8 a, f16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
@@ -94,7 +95,8 @@ struct PrefixShape {
   // In LDS, piece q of row r lies at piece q ^ mix(r) of the row, so that what
   // is read together lies in different banks (256 bytes hold all banks once):
   // of the keys, piece q of 16 rows; of the values, 64 bytes of rows 4 n .. 4 n
-  // + 3, or 32 bytes (8-bit) of those and of the rows 8 behind them.
+  // + 3, or 32 bytes (8-bit) of those and of the rows 8 behind them.  (With a
+  // mix for other reads half of LDS' cycles were conflicts: 79 us, not 76.5.)
   static __device__ __forceinline__ int mix_k(int r) {
     return Pieces % 16 == 0 ? r & 15 : Pieces % 8 == 0 ? (r >> 1) & 7 : Pieces % 4 == 0 ? (r >> 2) & 3 : (r >> 3) & 1;
   }
@@ -183,7 +185,7 @@ struct Cut {
 // rows with at most a fifth of them empty (396 rows, bf16 heads of 128: eight
 // waves in two workgroups, 19 % empty, against two in seven: 256 sequences
 // 45.9 and 50.8 us; 384 rows: four in three against eight in two, a quarter
-// empty: 79.6 and 90 us).
+// empty: 79.6 and 90 us; both with the 16x16x32 operations of before).
 template <class S>
 __device__ __forceinline__ Cut cut_of(const AttnParams& p, const Batch& s, int g) {
   Cut c;
