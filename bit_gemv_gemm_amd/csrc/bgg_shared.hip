@@ -10,9 +10,9 @@
 // A workgroup takes up to 256 rows of a key head (128 of wide heads) and a
 // chunk of the prefix; keys and values go from the cache to LDS once for all
 // its waves.  64 sequences of 48/8 heads of 128 behind 32768 tokens of f16:
-// 76.5 us, of which 7.5 pass until the first tiles are there and 4 with the
+// 76 to 81 us (by the device's clock), of which 7.5 pass until the first tiles are there and 4 with the
 // parts at the end (with every wave loading its own operands 103); 256
-// sequences in two groups behind 5328 and 4112 tokens of bf16 (32/8): 44.4 us
+// sequences in two groups behind 5328 and 4112 tokens of bf16 (32/8): 43.4 us
 // (122 then).  The matrix units are busy a third of the time and the vector
 // units 44 %: a tile of two waves on a SIMD takes 1600 to 2200 cycles, where
 // its products and exponentials alone take 1450, and the clock falls to 1.8
@@ -656,7 +656,19 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
     return (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)v) |
            (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32;
   };
-  if (it.tile + stream < it.tile_end) {
+  if (__all(none)) {
+    // no row of this wave sees anything: it only fetches, and leaves its SIMD
+    // to the other wave (256 sequences in two groups, a sixth of the row waves
+    // empty: 44.0 -> 43.4 us)
+#pragma unroll 1
+    for (int step = 0; step + 1 < steps; ++step) {
+      landed_barrier<0>();
+      if (step + 2 < steps && fetches) {
+        if (((step + 2) & 63) == 0) load_pages(step + 2);
+        fetch(step + 2);
+      }
+    }
+  } else if (it.tile + stream < it.tile_end) {
     uint64_t pages = pages_of(0);
     int step = 0, sub = stream;
     load_keys(0, sub);
