@@ -10,10 +10,10 @@
 // A workgroup takes up to 256 rows of a key head (128 of wide heads) and a
 // chunk of the prefix; keys and values go from the cache to LDS once for all
 // its waves.  64 sequences of 48/8 heads of 128 behind 32768 tokens of f16:
-// 76 to 81 us (by the device's clock), of which 7.5 pass until the first tiles are there and 4 with the
-// parts at the end (with every wave loading its own operands 103); 256
-// sequences in two groups behind 5328 and 4112 tokens of bf16 (32/8): 43.4 us
-// (122 then).  The matrix units are busy a third of the time and the vector
+// 76 to 81 us (by the device's clock), of which 7.5 pass until the first tiles
+// are there and 4 with the parts at the end (with every wave loading its own
+// operands 103); 256 sequences in two groups behind 5328 and 4112 tokens of
+// bf16 (32/8): 43.4 us (122 then).  The matrix units are busy a third of the time and the vector
 // units 44 %: a tile of two waves on a SIMD takes 1600 to 2200 cycles, where
 // its products and exponentials alone take 1450, and the clock falls to 1.8
 // GHz under them.
