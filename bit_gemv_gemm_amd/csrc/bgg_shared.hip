@@ -9,11 +9,10 @@
 //
 // A workgroup takes up to 256 rows of a key head (128 of wide heads) and a
 // chunk of the prefix; keys and values go from the cache to LDS once for all
-// its waves.  64 sequences of 48/8 heads of 128 behind 32768 tokens of f16:
-// 76 to 81 us (by the device's clock), of which 7.5 pass until the first tiles
-// are there and 4 with the parts at the end (with every wave loading its own
-// operands 103); 256 sequences in two groups behind 5328 and 4112 tokens of
-// bf16 (32/8): 43.4 us (122 then).  The matrix units are busy a third of the time and the vector
+// its waves.  64 sequences of 48/8 heads of 128 behind 32768 tokens of f16: 94
+// us, of which 7.5 pass until the first tiles are there and 4 with the parts at
+// the end; 256 sequences in two groups behind 5328 and 4112 tokens of bf16
+// (32/8): 52 us.  The matrix units are busy a third of the time and the vector
 // units 44 %: a tile of two waves on a SIMD takes 1600 to 2200 cycles, where
 // its products and exponentials alone take 1450, and the clock falls to 1.8
 // GHz under them.
@@ -421,10 +420,13 @@ __device__ __forceinline__ void landed_barrier() {
 
 // The keys and values of a step's tiles go from the cache to LDS without
 // registers, a step or two ahead, four waves a quarter each; all the waves
-// that work on the same tokens read them from there.  Probabilities are one
-// 16-bit term (a rounding of half a step each in the products with the values;
-// their sum is of the unrounded ones): of two, as bgg_paged_attention has them
-// where memory sets the time, the second would double these products.
+// that work on the same tokens read them from there.  Probabilities are a sum
+// of two 16-bit terms in the products with the values, as in
+// bgg_paged_attention (Mma::split).  The second term doubles these products:
+// one alone takes 78.8 us in the place of 94.4 for 64 sequences behind 32768
+// tokens and 43.9 in the place of 52.5 for 256 in two groups, but leaves every
+// probability half a step of 16 bits off (up to 2^-8 of its value for bf16), by
+// which a sequence's result would change with the call that computes it.
 template <class T, class C, int D>
 __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_prefix(AttnParams p) {
   using TL = Tile<T, C, D>;
@@ -757,9 +759,12 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
           e[i] = __builtin_amdgcn_exp2f(x[8 * j + i]);
           l += e[i];
         }
-        const typename Mma<V>::op pr = Mma<V>::round(e);
+        float rest[8];
+        const typename Mma<V>::op hi = Mma<V>::split(e, rest), lo = Mma<V>::round(rest);
 #pragma unroll
-        for (int i = 0; i < PL; ++i) acc[i] = mul32(v[j][i], pr, acc[i]);
+        for (int i = 0; i < PL; ++i) acc[i] = mul32(v[j][i], hi, acc[i]);
+#pragma unroll
+        for (int i = 0; i < PL; ++i) acc[i] = mul32(v[j][i], lo, acc[i]);
       }
       if (done) break;
       step = next_step, sub = next_sub;

@@ -721,11 +721,8 @@ size_t bgg_shared_attention_workspace_size(const bgg_cache_desc* cache, int64_t 
  * read.  Each sequence sees of them what lies below its length (and inside
  * its window), and then its own tokens; sequences outside every group have
  * no shared part.
- * As there, but for the rounding of the shared part: its probabilities enter
- * their product with the values as one 16-bit term (the type of the values;
- * fp16 for E4M3), off by half a step of it at most, so an element of out is
- * off by at most that times sum_t p_t |v_t| over the shared tokens, beside
- * its own rounding.  Softmax statistics and all sums are fp32.
+ * Products, probabilities, softmax statistics and sums of the shared part are
+ * as there; where the tokens are cut, and so the last bits, differs.
  * Workspace as there, of bgg_shared_attention_workspace_size bytes; the two
  * calls may share one.
  * Errors: as bgg_paged_attention.
