@@ -440,6 +440,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   __shared__ __attribute__((aligned(16))) uint8_t lds[at_least(2 * kBuf, at_least(kPlan, kRed))];
   __shared__ float red_m[Waves * S::Rows];
   __shared__ int scratch[Waves];
+  __shared__ __attribute__((aligned(16))) float special[D];  // sums of infinite and NaN values
   __shared__ __attribute__((aligned(8))) uint8_t has_page[2][2 * S::Subs];  // of a step's buffer: half a tile each
 
   int* const plan = (int*)lds;
@@ -774,7 +775,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   // the parts of the waves with the same rows into the chunk's: each brings
   // its sums to the largest maximum, then they are added up
   float(*const red)[RowF] = reinterpret_cast<float(*)[RowF]>(lds);  // [Waves * Rows]
-  infinite = __syncthreads_or(infinite);  // (also: the tiles are read)
+  __syncthreads();  // (the tiles are read)
   l = none ? 0.0f : row_sum(l);
   m = none ? -FLT_MAX : m;
   if (half_of == 0) red_m[wave * S::Rows + r] = m;
@@ -784,6 +785,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
     for (int w = wave & (row_waves - 1); w < Waves; w += row_waves) mw = fmaxf(mw, red_m[w * S::Rows + r]);
     const float f = none ? 0.0f : __builtin_amdgcn_exp2f(m - mw);
     float* const row = red[wave * S::Rows + r];
+    bool nan = false;
 #pragma unroll
     for (int i = 0; i < PL; ++i)
 #pragma unroll
@@ -791,11 +793,37 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
         f32x4 o;
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[k] = none ? 0.0f : acc[i][4 * n + k] * f;
+        nan |= any_nan(o);
         *reinterpret_cast<f32x4*>(row + 32 * i + 8 * n + 4 * half_of) = o;
       }
     if (half_of == 0) row[D] = mw, row[D + 1] = none ? 0.0f : l * f;
+    infinite |= nan && l == l;
   }
-  __syncthreads();
+  // Where an infinite or NaN value is in play: the sums of such values over the
+  // item's tokens, which all threads form once (their order does not matter); a
+  // row that sees only a part of these tokens forms its own (one infinite value
+  // among 32768 tokens of 64 sequences: a call of 137 us, without one 109; with a
+  // sum for every row 5.1 ms).
+  const int all_from = max(lo_all, it.tile * kTokens), all_to = min(hi_all, it.tile_end * kTokens);
+  auto special_of = [&](int from, int to, int d) {
+    return infinite_values<C, D>(table, reinterpret_cast<const typename C::bits_t*>(p.v_cache), p.pages, p.kv_heads, kh,
+                                 p.page_shift, from, to, d);
+  };
+  infinite = __syncthreads_or(infinite);
+  if (__builtin_expect(infinite, false)) {
+    constexpr int kSlices = kThreads / (D / 4);
+    if (threadIdx.x < D) special[threadIdx.x] = 0.0f;
+    __syncthreads();
+    const int d = 4 * (threadIdx.x % (D / 4)), slice = threadIdx.x / (D / 4);
+    const int span = (all_to - all_from + kSlices - 1) / kSlices, from = all_from + slice * span, to = min(all_to, from + span);
+    if (slice < kSlices && from < to) {
+      const f32x4 y = special_of(from, to, d);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (y[j] != 0.0f) atomicAdd(&special[d + j], y[j]);
+    }
+    __syncthreads();
+  }
   const int first_row = it.block * row_waves * S::Rows;
   float* const parts = p.prefix_parts + ((int64_t)it.row + ((int64_t)it.chunk * p.kv_heads + kh) * rows + first_row) * RowF;
 #pragma unroll 1
@@ -808,14 +836,14 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
       o += *reinterpret_cast<const f32x4*>(&red[w * S::Rows + k][d]);
       sum += red[w * S::Rows + k][D + 1];
     }
-    if (__builtin_expect(infinite || any_nan(o), false) && sum == sum) {
-      int seen_lo, seen_hi;
-      visible(p, s0 + (first_row + k) / p.group, seen_lo, seen_hi);
-      seen_lo = max(seen_lo, it.tile * kTokens);
-      seen_hi = min(min(seen_hi, prefix), it.tile_end * kTokens);
-      if (seen_lo < seen_hi) {
-        const f32x4 y = infinite_values<C, D>(table, reinterpret_cast<const typename C::bits_t*>(p.v_cache), p.pages,
-                                              p.kv_heads, kh, p.page_shift, seen_lo, seen_hi, d);
+    if (__builtin_expect(infinite, false) && sum == sum) {
+      int from, to;
+      visible(p, s0 + (first_row + k) / p.group, from, to);
+      from = max(from, it.tile * kTokens);
+      to = min(min(to, prefix), it.tile_end * kTokens);
+      if (from < to) {
+        f32x4 y = *reinterpret_cast<const f32x4*>(special + d);
+        if (from != all_from || to != all_to) y = special_of(from, to, d);
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[j] = y[j] != 0.0f ? y[j] : o[j];
       }

@@ -86,3 +86,36 @@ def test_two_terms(dtype, kv, D, hq, hk):
 def test_spread_scores(dtype, kv, D, hq, hk):
     run_check(case([(40, [1, 30, 200]), (3, [5])], hq=hq, hk=hk, D=D, dtype=dtype, kv=kv, page=32, seed=D, spread=2.0),
               both=True)
+
+
+@pytest.mark.parametrize("kv", ["f16", "bf16", "e4m3"])
+@pytest.mark.parametrize("D,hq,hk", [(64, 16, 1), (128, 12, 2), (192, 3, 3), (256, 4, 1)])
+@pytest.mark.parametrize("window", [0, 6000])
+def test_infinite_values_in_a_long_prefix(kv, D, hq, hk, window):
+    """In several chunks, behind which every row sees the whole chunk or, with
+    a window, some rows a part: the sums of such values are formed once for the
+    former."""
+    c = case([(130, [1, 70, 40, 500])], hq=hq, hk=hk, D=D, page=64, dtype="bf16" if kv == "bf16" else "f16", kv=kv,
+             window=window, seed=D)
+    inf, nan = float("inf"), float("nan")
+    planted = [(7, {5000: nan}), (D - 1, {8319: nan}), (20, {2500: nan})]  # (a window's start lies between 2321 and 2820)
+    if kv != "e4m3":
+        planted += [(8, {5000: inf}), (9, {4100: -inf, 8000: -inf}), (10, {100: inf, 7000: -inf}), (11, {0: inf, 2400: inf}),
+                    (12, {2600: inf})]
+    v, clean = c["caches"][1].clone(), c["caches"][1].clone()
+    for dim, tokens in planted:
+        for t, x in tokens.items():
+            v[int(c["full"][0, t // 64]), :, t % 64, dim], clean[int(c["full"][0, t // 64]), :, t % 64, dim] = x, 0.0
+    got, want = Device(dict(c, caches=[c["caches"][0], v])), Device(dict(c, caches=[c["caches"][0], clean]))
+    got.step(), want.step()
+    torch.cuda.synchronize()
+    B = len(c["lengths"])
+    out, ref = got.out.view(B, hq, D), want.out.view(B, hq, D).clone()
+    for b, n in enumerate(c["lengths"]):
+        for dim, tokens in planted:
+            x = sum(x for t, x in tokens.items() if t >= (max(0, n - window) if window else 0))
+            if x != 0:
+                ref[b, :, dim] = x
+    assert torch.equal(got.lse, want.lse)
+    same = (out == ref) | (torch.isnan(out) & torch.isnan(ref))
+    assert same.all(), (~same).nonzero()[:8]
