@@ -383,7 +383,9 @@ __global__ void __launch_bounds__(64 * WAVES, sizeof(typename C::bits_t) * D > 3
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int t = (tile + WAVES * lane) * kTokens + 16 * j;
-      page_of[j] = tile + WAVES * lane < it.tile_end && t < it.n ? table[t >> p.page_shift] : -1;
+      // (SHARED: an entry below it.lo may be one of the prefix, which is not this sequence's to read)
+      const bool in = tile + WAVES * lane < it.tile_end && t < it.n && (!SHARED || t + 16 > it.lo);
+      page_of[j] = in ? table[t >> p.page_shift] : -1;
       if (page_of[j] >= p.pages) page_of[j] = -1;
     }
   };
