@@ -19,11 +19,11 @@ constexpr int kWaves = 4;
 constexpr int kTokens = 32;  // tokens of a tile: one wave's step
 constexpr int kHeads = 16;   // query heads of a workgroup (columns of the products)
 
-// A sequence of a batch whose groups share prefixes: its first `tokens` are its
-// group's, whose parts of key head kh's head i are rows
-// row + (chunk * kv_heads + kh) * rows + i of the prefix parts.
+// A sequence of a batch whose groups share prefixes: the parts of its group's,
+// of key head kh's head i, are rows row + (chunk * kv_heads + kh) * rows + i of
+// the prefix parts.
 struct SharedSeq {
-  int32_t tokens, chunks, rows, row;
+  int32_t chunks, rows, row;
 };
 // An Item without its head block.
 struct OwnItem {

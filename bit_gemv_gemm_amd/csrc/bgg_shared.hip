@@ -320,12 +320,11 @@ __device__ __forceinline__ void plan_own(const AttnParams& p, const Batch& s, co
     int lo, n;
     own(b, lo, n);
     tiles += (float)tiles_of(lo, n);
-    SharedSeq q{0, 0, 0, 0};
+    SharedSeq q{0, 0, 0};
     const int g = s.group_of(G, b);
     if (s.start[g] <= b && b < s.start[g + 1]) {
       Cut c = cut_of<S>(p, s, g);
       cut_tiles<S>(c, size_of_prefix);
-      q.tokens = s.prefix(p, g);
       q.chunks = c.chunks;
       q.rows = c.rows;
       q.row = base[g] + (b - s.start[g]) * p.group;
