@@ -405,10 +405,13 @@ constexpr int at_least(int a, int b) { return a > b ? a : b; }
 // 16 bytes per lane from base + from to LDS, lane l's at `to` + 16 l, without
 // registers.  In assembly, so that the compiler, which does not see what is
 // read while they are in flight, does not wait for every load before it reads
-// LDS; landed_barrier is what waits.  (Nothing else in these kernels uses m0.)
+// LDS; landed_barrier is what waits.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // (that m0 is reserved: the compiler writes it where it needs it)
 __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(from), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(from), "s"(base) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 // All but the youngest N of this wave's loads have landed (those to LDS
 // included) and its LDS reads are done, and so for the other waves.
 template <int N>
