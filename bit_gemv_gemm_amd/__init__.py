@@ -443,9 +443,13 @@ def bgg_rotary_append(cache: bgg_cache_desc, k_cache, v_cache, positions, slots,
 def bgg_rotary_axes(sections, arrangement="blocks") -> np.ndarray:
     """uint8 [pairs]: the axis whose position turns each pair, with
     sections[a] pairs for axis a."""
-    s = np.ascontiguousarray(sections, dtype=np.int64)
-    if s.ndim != 1:
-        raise ValueError("sections must be one number per axis")
+    given = np.asarray(sections)
+    if given.ndim != 1 or given.dtype.kind not in "iuf":
+        raise ValueError("sections must be one whole number per axis")
+    with np.errstate(invalid="ignore"):
+        s = np.ascontiguousarray(given, dtype=np.int64)
+    if (s != given).any():
+        raise ValueError("sections must be one whole number per axis")
     out = np.zeros(128, dtype=np.uint8)
     kind = AXES_ARRANGEMENTS[arrangement] if isinstance(arrangement, str) else int(arrangement)
     _ok(_lib.bgg_rotary_axes(s.ctypes.data, s.size, kind, out.ctypes.data), "bgg_rotary_axes")
