@@ -676,8 +676,11 @@ size_t bgg_attention_workspace_size(const bgg_cache_desc* cache, int64_t q_heads
  * NaN meet, whatever the token's probability.
  * Products q.k are exact in fp32 sums; softmax statistics and sums are
  * fp32; the probabilities enter their product with the values as a sum of
- * two 16-bit terms; out is rounded once.  The cache is read once per 16
- * query heads of a key head.  The same call gives the same bits; how a
+ * two 16-bit terms (the type of the values; fp16 for E4M3), off by at most
+ * 2^-16 of their value (bf16) or by the larger of 2^-22 of it and 2^-32 of the
+ * row's largest probability (fp16: a token of less than that counts for
+ * nothing); out is rounded once.  The cache is read once per 16 query heads of
+ * a key head.  The same call gives the same bits; how a
  * sequence is cut, and so its last bits, follows the lengths of all
  * sequences of the call.
  * `workspace`: its first BGG_ATTENTION_COUNTER_BYTES count the parts of a

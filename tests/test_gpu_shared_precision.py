@@ -119,3 +119,23 @@ def test_infinite_values_in_a_long_prefix(kv, D, hq, hk, window):
     assert torch.equal(got.lse, want.lse)
     same = (out == ref) | (torch.isnan(out) & torch.isnan(ref))
     assert same.all(), (~same).nonzero()[:8]
+
+
+@pytest.mark.parametrize("dtype,kv", KINDS)
+@pytest.mark.parametrize("gap", [10, 16, 21, 24, 27, 31])
+def test_a_first_token_that_takes_nearly_all(dtype, kv, gap):
+    """Its values are zero, and every other token's probability is 2^-gap of its
+    own: the elements are sums of small probabilities alone.  The stated bound,
+    2^-32 of the largest probability a token for fp16 and E4M3 values, is all
+    that separates them from 0 at the end of the range."""
+    D, hq, hk = 64, 4, 1
+    c = case([(125, [1, 30, 200])], hq=hq, hk=hk, D=D, dtype=dtype, kv=kv, page=16, seed=gap)
+    k, v = torch.zeros(c["caches"][0].shape), c["caches"][1].float().abs()
+    first = int(c["full"][0, 0])
+    k[first, :, 0, 0] = 256.0  # (exact in every type)
+    v[first, :, 0] = 0.0
+    c["caches"] = [k.to(TYPES[kv]), v.to(TYPES[kv])]
+    c["q"] = torch.zeros_like(c["q"])
+    c["q"].view(-1, hq, D)[:, :, 0] = 8.0
+    c["scale"] = gap * math.log(2) / (8.0 * 256.0 * (float(c["scales"][0][0]) if kv == "e4m3" else 1.0))
+    run_check(c, both=True)
