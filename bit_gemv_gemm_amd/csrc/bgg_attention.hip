@@ -560,7 +560,12 @@ struct AttnPlan {
 // call's shape, so that one workspace serves any sequence of calls: a
 // sequence of several chunks counts in the word of its first part.
 constexpr uint64_t kCounterBytes = BGG_ATTENTION_COUNTER_BYTES;
-static_assert(2 * kMaxItems * 4 <= kCounterBytes, "a counter per part");
+constexpr int64_t kSingle = 4;  // items of one wave that are cut in the place of one of four
+static_assert(2 * kSingle * kMaxItems * 4 <= kCounterBytes, "a counter per part");
+
+uint64_t own_part_bytes(const bgg_cache_desc* c, int64_t q_heads, int64_t parts) {
+  return align256(4 * (uint64_t)(parts * part_floats(std::min<int64_t>(kHeads, q_heads / c->kv_heads), c->head_dim)));
+}
 
 AttnPlan plan_attention(const bgg_cache_desc* c, int64_t q_heads, int64_t batch) {
   AttnPlan p;
@@ -572,8 +577,7 @@ AttnPlan plan_attention(const bgg_cache_desc* c, int64_t q_heads, int64_t batch)
   p.items = p.target + batch * p.heads;
   // (a sequence of n > 1 chunks has more than (n - 1) >= n / 2 full ones)
   p.parts = 2 * kMaxItems;  // (whatever the device, so that the size does not depend on it)
-  p.total_bytes = kCounterBytes + align256(
-      4 * (uint64_t)(p.parts * part_floats(std::min<int64_t>(kHeads, q_heads / c->kv_heads), c->head_dim)));
+  p.total_bytes = kCounterBytes + own_part_bytes(c, q_heads, p.parts);
   return p;
 }
 
@@ -610,8 +614,11 @@ struct SharedPlan {
 };
 SharedPlan plan_shared(const bgg_cache_desc* c, int64_t q_heads, int64_t batch) {
   SharedPlan p;
-  p.items = plan_attention(c, q_heads, batch).total_bytes + 256;  // (the count before it)
-  p.seqs = p.items + align256((kMaxItems + batch) * sizeof(OwnItem));
+  // (kSingle times the items only if the batch alone is as many)
+  const int64_t heads = c->kv_heads * ceil_div(q_heads / c->kv_heads, kHeads);
+  const int64_t items = std::max<int64_t>(kMaxItems, std::min(kSingle * kMaxItems, batch * heads));
+  p.items = kCounterBytes + own_part_bytes(c, q_heads, 2 * items) + 256;  // (the count before it)
+  p.seqs = p.items + align256((items + batch) * sizeof(OwnItem));
   p.parts = p.seqs + align256(batch * sizeof(SharedSeq));
   p.total_bytes = p.parts + align256(4 * (uint64_t)prefix_part_floats(c, q_heads, batch, kMaxItems));
   return p;
@@ -671,22 +678,30 @@ bgg_status attend(const char* who, const bgg_cache_desc* c, const bgg_attention_
   p.prefix_target = (int)plan.target;
   // A batch of so many sequences and head blocks fills the GPU with one wave
   // for each, and the starts and ends of workgroups of four cost more than
-  // four waves to a sequence save (256 sequences of up to 200 own tokens, 8 key
-  // heads of 128: one wave 19.1 us, four 25.8; where fewer workgroups are there
-  // four are faster: 64 sequences of up to 300, 15.6 against 12.4 us).
-  const bool single = a->batch * plan.heads >= 4 * plan.target;
+  // four waves to a sequence save; chunks are then cut for kSingle times as many
+  // items.  One wave and four, us (8 key heads of 128 f16, 128, 256, 512 and 1024
+  // sequences): up to 40 own tokens each 12.1, 17.0, 24.4, 39.4 and 14.1, 22.1, 35.0,
+  // 64.1; up to 200 18.4, 28.6, 48.2, 106 and 21.4, 33.8, 59.3, 126; up to 1000
+  // 70.6, 130, 232, 415 and 68.2, 131, 218, 404; up to 100 but for one of 65536 76.8,
+  // 86.5, 104, 128 and 66.8, 79.2, 98.6, 135 (with chunks for as many items as four
+  // waves have 84.4, 103, 122, 163).  Heads of 256 bf16 gain more (up to 200: 54.7
+  // and 81.7), short 8-bit rows lose most behind one long sequence (128 of e4m3
+  // heads of 64: 38.6 and 22.5).
+  const bool single = a->batch * plan.heads >= kSingle * plan.target;
+  p.own_target = (int)(single ? kSingle * plan.target : plan.target);
   p.own_chunks = most_chunks(single ? 1 : kWaves);
   p.own_count = (int32_t*)(w + more.items - 256);
   p.own_items = (OwnItem*)(w + more.items);
   p.seqs = (SharedSeq*)(w + more.seqs);
   p.prefix_parts = (float*)(w + more.parts);
+  const int64_t items = p.own_target + a->batch * plan.heads;
   launch_prefix(p, a->type, e4m3, c->head_dim, s);
   const bgg_status st = hip_check(who);
   if (st) return st;
-  if (p.own_chunks == kMaxChunks)
-    launch_attention<true, kWaves>(p, plan.items, a->type, e4m3, c->head_dim, s);
+  if (!single)
+    launch_attention<true, kWaves>(p, items, a->type, e4m3, c->head_dim, s);
   else
-    launch_attention<true, 1>(p, plan.items, a->type, e4m3, c->head_dim, s);
+    launch_attention<true, 1>(p, items, a->type, e4m3, c->head_dim, s);
   return hip_check(who);
 }
 

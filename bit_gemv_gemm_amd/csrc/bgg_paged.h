@@ -49,7 +49,7 @@ struct AttnParams {
   // sequences that share a prefix (bgg_shared_attention)
   const int32_t *group_starts, *shared_pages;
   int groups, prefix_target;
-  int own_chunks;  // chunks of a sequence at most
+  int own_target, own_chunks;  // items of own tokens (as target_items); chunks of a sequence at most
   int32_t* own_count;  // [1]: entries of own_items
   OwnItem* own_items;
   SharedSeq* seqs;     // [batch]

@@ -312,7 +312,12 @@ __device__ __forceinline__ void plan_own(const AttnParams& p, const Batch& s, co
     const int g = s.group_of(G, b);
     if (s.start[g] <= b && b < s.start[g + 1]) lo = max(lo, s.prefix(p, g));
   };
-  auto own_chunks = [&](int tiles, int size) { return chunks_of(tiles, max(size, (tiles + p.own_chunks - 1) / p.own_chunks)); };
+  // (by one wave a sequence of up to two shares stays whole: two items side by
+  // side gain less than their join costs)
+  const int whole = p.own_target > p.target_items ? 2 : 1;
+  auto own_chunks = [&](int tiles, int size) {
+    return tiles <= whole * size ? 1 : chunks_of(tiles, max(size, (tiles + p.own_chunks - 1) / p.own_chunks));
+  };
   float* const sums = reinterpret_cast<float*>(scratch);
   float tiles = 0.0f;
 #pragma unroll 1
@@ -338,7 +343,7 @@ __device__ __forceinline__ void plan_own(const AttnParams& p, const Batch& s, co
 #pragma unroll
   for (int w = 0; w < S::Waves; ++w) all += sums[w];
   __syncthreads();
-  const float even = fminf(ceilf(all * (float)H / (float)p.target_items * 1.0001f), 1e8f);
+  const float even = fminf(ceilf(all * (float)H / (float)p.own_target * 1.0001f), 1e8f);
   int size = 0, mine = 0, before = 0;
 #pragma unroll 1
   for (int k = 8; k <= 16; k += 2) {
@@ -362,7 +367,7 @@ __device__ __forceinline__ void plan_own(const AttnParams& p, const Batch& s, co
     }
     __syncthreads();
     if (tid == 0) *p.own_count = total & 0xFFFF;
-    if (p.batch * H > p.target_items || (total & 0xFFFF) * H <= p.target_items) break;
+    if (p.batch * H > p.own_target || (total & 0xFFFF) * H <= p.own_target) break;
   }
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
