@@ -59,6 +59,9 @@ __device__ __forceinline__ float row_sum(float v) {
 
 constexpr int kGroupsMax = (int)kMaxBatch;
 
+// (the last tile of the longest table ends at 2^31, behind every token: cut)
+__device__ __forceinline__ int first_token(int tile) { return (int)min((uint32_t)tile * kTokens, 0x7FFFFFFFu); }
+
 // The shape of the kernel's work.
 template <class T, class C, int D>
 struct PrefixShape {
@@ -496,7 +499,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   // a row that sees nothing of the item's tokens (an unused sequence, a
   // window) does not keep the others from the fast path: it is emptied at the
   // end instead
-  const bool none = row0 + r >= rows || max(lo, it.tile * kTokens) >= min(hi, it.tile_end * kTokens);
+  const bool none = row0 + r >= rows || max(lo, first_token(it.tile)) >= min(hi, first_token(it.tile_end));
   int lo_max = none ? 0 : lo, hi_min = none ? 0x7FFFFFFF : hi;
   // over the rows (the same in both lanes of a row)
 #pragma unroll
@@ -692,7 +695,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
       for (int st = 0; st < Steps; ++st) s = mul32(key_op(st), q[st], s);
       widen_values();
       const uint32_t have = (uint32_t)(pages >> (16 * sub) & 1) | (uint32_t)(pages >> (16 * sub + 7) & 2);
-      if (!(t0 >= lo_max && t0 + kTokens <= hi_min && have == 3)) {
+      if (!(t0 >= lo_max && t0 <= hi_min - kTokens && have == 3)) {
         // some row does not see some token: no score there.  Nobody sees a
         // token outside lo_all .. hi_all - 1 or without a page; the values
         // of the others stay, but for those that would be NaN times a
@@ -811,7 +814,7 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
   // row that sees only a part of these tokens forms its own (one infinite value
   // among 32768 tokens of 64 sequences: a call of 137 us, without one 109; with a
   // sum for every row 5.1 ms).
-  const int all_from = max(lo_all, it.tile * kTokens), all_to = min(hi_all, it.tile_end * kTokens);
+  const int all_from = max(lo_all, first_token(it.tile)), all_to = min(hi_all, first_token(it.tile_end));
   auto special_of = [&](int from, int to, int d) {
     return infinite_values<C, D>(table, reinterpret_cast<const typename C::bits_t*>(p.v_cache), p.pages, p.kv_heads, kh,
                                  p.page_shift, from, to, d);
@@ -846,8 +849,8 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
     if (__builtin_expect(infinite, false) && sum == sum) {
       int from, to;
       visible(p, s0 + (first_row + k) / p.group, from, to);
-      from = max(from, it.tile * kTokens);
-      to = min(min(to, prefix), it.tile_end * kTokens);
+      from = max(from, first_token(it.tile));
+      to = min(min(to, prefix), first_token(it.tile_end));
       if (from < to) {
         f32x4 y = *reinterpret_cast<const f32x4*>(special + d);
         if (from != all_from || to != all_to) y = special_of(from, to, d);
