@@ -9,13 +9,20 @@
 //
 // A workgroup takes up to 256 rows of a key head (128 of wide heads) and a
 // chunk of the prefix; keys and values go from the cache to LDS once for all
-// its waves.  64 sequences of 48/8 heads of 128 behind 32768 tokens of f16: 94
+// its waves.  64 sequences of 48/8 heads of 128 behind 32768 tokens of f16: 93
 // us, of which 7.5 pass until the first tiles are there and 4 with the parts at
 // the end; 256 sequences in two groups behind 5328 and 4112 tokens of bf16
-// (32/8): 52 us.  The matrix units are busy a third of the time and the vector
-// units 44 %: a tile of two waves on a SIMD takes 1600 to 2200 cycles, where
-// its products and exponentials alone take 1450, and the clock falls to 1.8
-// GHz under them.
+// (32/8): 51 us.  The matrix units are busy 48 and 34 % of the time and the
+// vector units 54 and 46 %, and the clock falls to about 1.8 GHz under them.
+// (Where both sides of a choice are given below, they were measured with
+// probabilities of one term.)
+//
+// What grows with the groups is the schedule: every workgroup works it out by
+// itself, a part of them only to find nothing left, and one at a time runs on a
+// CU.  us, of 32/8 heads of 128 f16 behind 1024 tokens, with bgg_paged_attention
+// of the same batch: 32, 64, 128, 512 groups of 8 sequences 53, 115, 230, 1110
+// (100, 225, 507, 3420); 64, 512, 2048 groups of 2 77, 690, 6200 (64, 628, 3800);
+// 64, 256, 1024, 4096 groups of one 69, 289, 1540, 22700 (45, 198, 785, 4280).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -204,7 +211,10 @@ __device__ __forceinline__ Cut cut_of(const AttnParams& p, const Batch& s, int g
   return c;
 }
 // Chunks, and the tiles of each, at a size of items in tiles times row waves:
-// a tile or more for every stream of tokens.
+// a tile or more for every stream of tokens.  (Nothing weighs the parts against
+// that: 64 sequences of 16 heads on one key head behind 2048 tokens have 32
+// chunks of two tiles, 35 MB of parts, and take 35 us, bgg_paged_attention 15;
+// 128 of 32/8 heads 46 and 85.)
 template <class S>
 __device__ __forceinline__ void cut_tiles(Cut& c, int size) {
   const int streams = S::WaveBits - c.wave_bits;
@@ -433,8 +443,8 @@ __device__ __forceinline__ void landed_barrier() {
 // that work on the same tokens read them from there.  Probabilities are a sum
 // of two 16-bit terms in the products with the values, as in
 // bgg_paged_attention (Mma::split).  The second term doubles these products:
-// one alone takes 78.8 us in the place of 94.4 for 64 sequences behind 32768
-// tokens and 43.9 in the place of 52.5 for 256 in two groups, but leaves every
+// one alone takes 78.8 us in the place of 93 for 64 sequences behind 32768
+// tokens and 43.9 in the place of 51.4 for 256 in two groups, but leaves every
 // probability half a step of 16 bits off (up to 2^-8 of its value for bf16), by
 // which a sequence's result would change with the call that computes it.
 template <class T, class C, int D>
