@@ -835,9 +835,10 @@ __global__ void __launch_bounds__((64 * PrefixShape<T, C, D>::Waves)) k_shared_p
     if (threadIdx.x < D) special[threadIdx.x] = 0.0f;
     __syncthreads();
     const int d = 4 * (threadIdx.x % (D / 4)), slice = threadIdx.x / (D / 4);
-    const int span = (all_to - all_from + kSlices - 1) / kSlices, from = all_from + slice * span, to = min(all_to, from + span);
+    const uint32_t all = (uint32_t)max(all_to - all_from, 0), span = all / kSlices + 1;  // (tokens up to 2^31 - 16)
+    const uint32_t from = min(all, slice * span), to = min(all, from + span);
     if (slice < kSlices && from < to) {
-      const f32x4 y = special_of(from, to, d);
+      const f32x4 y = special_of(all_from + (int)from, all_from + (int)to, d);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (y[j] != 0.0f) atomicAdd(&special[d + j], y[j]);
